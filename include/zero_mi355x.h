@@ -21,6 +21,9 @@
  *                           stepped in one launch
  *   zero_reduce_adamw_step  the reduce and the update in one pass, for a step
  *                           with no global norm between them
+ *   zero_shard_adamw8_step, zero_mt8_table_*, zero_reduce_adamw8_step  the three
+ *                           AdamW forms with the moments held in 8 bits
+ *   zero_state8_quantize, zero_state8_dequantize  those moments from and to fp32
  *   zero_gather_params      bf16 shards back to per-tensor parameters
  *                           (all-gather output layout, then un-flatten)
  *   zero_flatten_params     per-tensor bf16 buffers into the padded flat buffer
@@ -471,6 +474,143 @@ zero_status zero_mt_table_adamw_step(const zero_mt_table* table, int64_t step, d
 zero_status zero_mt_table_adamw_step_scheduled(const zero_mt_table* table,
                                                const zero_adamw_schedule* schedule,
                                                const float* clip_scale, hipStream_t stream);
+
+/* ------------------------------------------------------------------ AdamW, moments in 8 bits
+ *
+ * [ZF] "Static Memory Allocation": the two fp32 moments are 8 of a parameter's
+ * 16 bytes. These entry points hold them in 8 bits: an array of n moments is
+ * cut into blocks of ZERO_STATE8_BLOCK consecutive elements (the last one may
+ * be shorter), with one code byte per element and one scale byte per block
+ * (ceil(n / ZERO_STATE8_BLOCK) of them), 2.02 bytes for both moments instead
+ * of 8. The master weights stay fp32.
+ *
+ * Format. A code is an OCP 8-bit float e4m3 (bias 7, largest 448, no
+ * infinity), a scale byte an e8m0 power of two: value = e4m3(code) *
+ * 2^(byte - 127). Byte 255 stands for a block that held an infinity or NaN:
+ * it reads as NaN throughout (its codes are written as 0). All-zero bytes are
+ * zeros, so cleared arrays are the moments of a new run.
+ * Encoding a block. E = the biased exponent field of the largest magnitude;
+ * byte = 255 if E = 255, else max(E - 7, 0) (that magnitude then lies in
+ * [2^7, 2^8) in code units and never saturates). y = |x| * 2^(7 - byte),
+ * rounded once to fp32 (inexact only for subnormal y); code =
+ * (bits(y) + r) >> 20 with a 20-bit r, and the sign in bit 7. In the second
+ * moment a positive x has a code of at least 1 (never rounded to zero).
+ * r is a random word's 20 bits in the steps (stochastic rounding: a moment
+ * that moves by less than a code's step still moves in the mean) and 0x7FFFF +
+ * (bit 20 of y) in zero_state8_quantize (to nearest, ties to even).
+ * Random words. Element e of step t of a run with `seed` has a 32-bit word
+ * that depends on (seed, t, e) only, all arithmetic unsigned:
+ *   z = seed + t * 0x6A09E667F3BCC909;  z = (z ^ z >> 32) * 0xBB67AE8584CAA73B;
+ *   z = (z ^ z >> 29) * 0x3C6EF372FE94F82B;  z ^= z >> 32;          (64 bits)
+ *   q = e / 8, j = e % 8;  a = (low(q) ^ low(z)) * 0xA54FF53B;  a ^= a >> 16;
+ *   a = (a + high(q) + high(z)) * 0x510E527F;  a ^= a >> 15;
+ *   b = a * 0x9B05688D;  b = (b ^ b >> 16) | 1;  word = a + j * b   (32 bits)
+ * The first moment's r is word >> 12, the second's word & 0xFFFFF.
+ * first_element (a multiple of ZERO_STATE8_BLOCK, >= 0) is the number e of the
+ * arrays' first element: a rank passes its shard's place in the flat buffer,
+ * and a shard stepped window by window rounds as the whole shard does.
+ *
+ * The update per element is zero_shard_adamw_step's, in its order, on the
+ * decoded m and v: the new fp32 m and v update p, and then are encoded.
+ * Accesses: any pointer alignment; with master 16-byte, codes 8-byte, grad and
+ * param_out 16-byte aligned the vector path runs, with identical results.
+ *
+ * zero_shard_adamw8_step
+ * master       device [n] fp32, updated in place.
+ * exp_avg, exp_avg_sq  device [n] codes, updated in place.
+ * exp_avg_scale, exp_avg_sq_scale  device [ceil(n / 128)] bytes, in place.
+ * grad, param_out, n, step, lr, beta1, beta2, eps, weight_decay, clip_scale:
+ *              as zero_shard_adamw_step (a non-finite coefficient skips the
+ *              update). The six written arrays must not overlap one another
+ *              or grad. A gradient that makes a moment infinite or NaN makes
+ *              that moment's block NaN from the next step on.
+ * Errors: as zero_shard_adamw_step; ZERO_EINVAL for a first_element that is
+ * negative or no multiple of ZERO_STATE8_BLOCK; ZERO_ERANGE when first_element
+ * + n overflows or n is past 2^48.
+ * zero_shard_adamw8_step_scheduled: the step's scalars, and the step number of
+ * the random words, read on the device from the schedule (which it does not
+ * move on). Errors: as zero_shard_adamw_step_scheduled, and the above. */
+#define ZERO_STATE8_BLOCK 128
+zero_status zero_shard_adamw8_step(float* master, uint8_t* exp_avg, uint8_t* exp_avg_scale,
+                                   uint8_t* exp_avg_sq, uint8_t* exp_avg_sq_scale,
+                                   const uint16_t* grad, uint16_t* param_out, int64_t n,
+                                   int64_t first_element, int64_t step, double lr, double beta1,
+                                   double beta2, double eps, double weight_decay, uint64_t seed,
+                                   const float* clip_scale, hipStream_t stream);
+zero_status zero_shard_adamw8_step_scheduled(float* master, uint8_t* exp_avg, uint8_t* exp_avg_scale,
+                                             uint8_t* exp_avg_sq, uint8_t* exp_avg_sq_scale,
+                                             const uint16_t* grad, uint16_t* param_out, int64_t n,
+                                             int64_t first_element,
+                                             const zero_adamw_schedule* schedule, uint64_t seed,
+                                             const float* clip_scale, hipStream_t stream);
+
+/* Many tensors, through a device table (zero_mt_table_*'s counterpart): each
+ * tensor has its own arrays, and its own blocks, counted from its first
+ * element. Tensor t's elements are numbered from first_element plus the
+ * lengths of the tensors before it, each rounded up to a multiple of
+ * ZERO_STATE8_BLOCK. Create, step, free, blocks and the caller's duties as
+ * zero_mt_table_* (create: hipMalloc and a synchronous hipMemcpy on the
+ * current device, once; 128 bytes per tensor and 4 per workgroup of 2,048
+ * elements); the results are zero_shard_adamw8_step's on each tensor.
+ * Errors: as zero_mt_table_*, and zero_shard_adamw8_step's on first_element. */
+typedef struct zero_mt8_table zero_mt8_table;
+zero_status zero_mt8_table_create(float* const* masters, uint8_t* const* exp_avgs,
+                                  uint8_t* const* exp_avg_scales, uint8_t* const* exp_avg_sqs,
+                                  uint8_t* const* exp_avg_sq_scales, const uint16_t* const* grads,
+                                  uint16_t* const* params_out, const int64_t* numels,
+                                  int32_t n_tensors, int64_t first_element, zero_mt8_table** out);
+void zero_mt8_table_free(zero_mt8_table* table);
+int64_t zero_mt8_table_blocks(const zero_mt8_table* table);
+zero_status zero_mt8_table_adamw8_step(const zero_mt8_table* table, int64_t step, double lr,
+                                       double beta1, double beta2, double eps, double weight_decay,
+                                       uint64_t seed, const float* clip_scale, hipStream_t stream);
+zero_status zero_mt8_table_adamw8_step_scheduled(const zero_mt8_table* table,
+                                                 const zero_adamw_schedule* schedule, uint64_t seed,
+                                                 const float* clip_scale, hipStream_t stream);
+
+/* Reduce and update in one pass, moments in 8 bits (zero_reduce_adamw_step's
+ * counterpart): the averaged gradient is zero_grad_reduce_shard's, the update
+ * zero_shard_adamw8_step's on it, bit for bit the two calls in sequence;
+ * 2R + 14 bytes per element. The state arrays are the rank's shard ([S] and
+ * ceil(S / 128) scales), first_element the number of the shard's first
+ * element. A block is encoded whole, so the window's part of the shard must
+ * start at a multiple of ZERO_STATE8_BLOCK elements of the shard and end at
+ * one or at the shard's end (ZERO_EINVAL otherwise).
+ * Other arguments and errors: as zero_reduce_adamw_step and
+ * zero_shard_adamw8_step. */
+zero_status zero_reduce_adamw8_step(const zero_plan* plan, int32_t rank,
+                                    const uint16_t* const* replicas, int32_t n_replicas,
+                                    int64_t begin, int64_t count, float* master, uint8_t* exp_avg,
+                                    uint8_t* exp_avg_scale, uint8_t* exp_avg_sq,
+                                    uint8_t* exp_avg_sq_scale, uint16_t* param_out,
+                                    uint16_t* shard_grad, int64_t first_element, int64_t step,
+                                    double lr, double beta1, double beta2, double eps,
+                                    double weight_decay, uint64_t seed, const float* clip_scale,
+                                    hipStream_t stream);
+zero_status zero_reduce_adamw8_step_scheduled(const zero_plan* plan, int32_t rank,
+                                              const uint16_t* const* replicas, int32_t n_replicas,
+                                              int64_t begin, int64_t count, float* master,
+                                              uint8_t* exp_avg, uint8_t* exp_avg_scale,
+                                              uint8_t* exp_avg_sq, uint8_t* exp_avg_sq_scale,
+                                              uint16_t* param_out, uint16_t* shard_grad,
+                                              int64_t first_element,
+                                              const zero_adamw_schedule* schedule, uint64_t seed,
+                                              const float* clip_scale, hipStream_t stream);
+
+/* Moments between fp32 and 8 bits (a checkpoint read or written, a run moved
+ * from or to 32-bit moments).
+ * zero_state8_quantize: x device [n] fp32 into codes [n] and scales
+ * [ceil(n / 128)], rounded to nearest, ties to even; second_moment != 0 keeps
+ * a positive x at code 1 or more. The written arrays must not overlap one
+ * another or x. zero_state8_dequantize: the values, out device [n] fp32 (exact
+ * but for fp32 subnormals, which round to nearest); out must not overlap the
+ * codes or the scales.
+ * Errors: ZERO_EINVAL (n < 0; with n > 0, null pointers or overlapping arrays,
+ * named in zero_last_error()); ZERO_ERANGE for n past 2^48; ZERO_EHIP. */
+zero_status zero_state8_quantize(const float* x, int64_t n, int32_t second_moment, uint8_t* codes,
+                                 uint8_t* scales, hipStream_t stream);
+zero_status zero_state8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n,
+                                   float* out, hipStream_t stream);
 
 /* ------------------------------------------------------------------ gather
  *

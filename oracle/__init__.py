@@ -36,4 +36,6 @@ from .gather import gather_params, gather_params_shard0  # noqa: F401
 from .plan import Plan, Shard0Plan, memory_bytes, partition_plan, partition_plan_shard0  # noqa: F401
 from .reduce import reduce_shard  # noqa: F401
 from .sqnorm import SqnormAccumulator, sqnorm, sqnorm_fsum  # noqa: F401
+from . import state8  # noqa: F401
+from .state8 import adamw8_step  # noqa: F401
 from .step import rank_step  # noqa: F401

@@ -9,6 +9,9 @@ The entry points mirror the C ABI in include/zero_mi355x.h one for one:
     zero_clip_scale         global-norm clip coefficient (device scalar)
     zero_shard_adamw_step   fused fp32 AdamW update with bf16 parameter emit
     zero_multi_tensor_adamw_step  the same over a ragged list of tensors
+    zero_shard_adamw8_step  the AdamW update with both moments in 8 bits (also
+                            MultiTensor8Table, zero_reduce_adamw8_step)
+    zero_state8_quantize    fp32 moments -> 8 bits, and zero_state8_dequantize back
     zero_gather_params      bf16 shards -> per-tensor parameters
     zero_flatten_params     per-tensor buffers -> padded flat buffer
     zero_host_adamw_step    the same update on the host CPU (ZeRO-Offload)
@@ -41,4 +44,8 @@ from ._binding import (LIB_PATH, ZERO_MAX_REPLICAS, AdamWSchedule, CopyTable,  #
                        zero_grad_sqnorm, zero_last_error, zero_partition_plan,
                        zero_partition_plan_shard0, zero_host_adamw_step, zero_offload_adamw_step,
                        zero_multi_tensor_adamw_step,
-                       zero_shard_adamw_step, zero_sqnorm_workspace_bytes, zero_status_string)
+                       zero_shard_adamw_step, zero_sqnorm_workspace_bytes, zero_status_string,
+                       ZERO_STATE8_BLOCK, MultiTensor8Table, state8_blocks, zero_reduce_adamw8_step,
+                       zero_reduce_adamw8_step_scheduled, zero_shard_adamw8_step,
+                       zero_shard_adamw8_step_scheduled, zero_state8_dequantize,
+                       zero_state8_quantize)

@@ -18,6 +18,7 @@ LIB_PATH = os.environ.get("ZERO_MI355X_LIB") or os.path.join(
 
 ZERO_OK, ZERO_EINVAL, ZERO_ERANGE, ZERO_ENOMEM, ZERO_EHIP, ZERO_ENOSPACE = range(6)
 ZERO_MAX_REPLICAS = 64
+ZERO_STATE8_BLOCK = 128
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
@@ -27,6 +28,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 c_i32, c_i64, c_dbl, c_sz, c_vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_double, ctypes.c_size_t, \
     ctypes.c_void_p
+c_u64 = ctypes.c_uint64
 
 
 class zero_segment(ctypes.Structure):
@@ -115,6 +117,24 @@ _reduce_adamw_sched = _fn("zero_reduce_adamw_step_scheduled", c_i32,
                            c_vp, c_vp, c_vp, c_vp])
 _step_scalars = _fn("zero_adamw_step_scalars", c_i32,
                     [c_i64, c_dbl, c_dbl, c_dbl, c_dbl, c_dbl, ctypes.POINTER(ctypes.c_float)])
+_adamw8 = _fn("zero_shard_adamw8_step", c_i32,
+              [c_vp] * 7 + [c_i64, c_i64, c_i64, c_dbl, c_dbl, c_dbl, c_dbl, c_dbl, c_u64, c_vp, c_vp])
+_adamw8_sched = _fn("zero_shard_adamw8_step_scheduled", c_i32,
+                    [c_vp] * 7 + [c_i64, c_i64, c_vp, c_u64, c_vp, c_vp])
+_mt8_create = _fn("zero_mt8_table_create", c_i32, [c_vp] * 8 + [c_i32, c_i64, ctypes.POINTER(c_vp)])
+_mt8_free = _fn("zero_mt8_table_free", None, [c_vp])
+_mt8_blocks = _fn("zero_mt8_table_blocks", c_i64, [c_vp])
+_mt8_step = _fn("zero_mt8_table_adamw8_step", c_i32,
+                [c_vp, c_i64, c_dbl, c_dbl, c_dbl, c_dbl, c_dbl, c_u64, c_vp, c_vp])
+_mt8_step_sched = _fn("zero_mt8_table_adamw8_step_scheduled", c_i32, [c_vp, c_vp, c_u64, c_vp, c_vp])
+_reduce_adamw8 = _fn("zero_reduce_adamw8_step", c_i32,
+                     [c_vp, c_i32, ctypes.POINTER(c_vp), c_i32, c_i64, c_i64] + [c_vp] * 7 +
+                     [c_i64, c_i64, c_dbl, c_dbl, c_dbl, c_dbl, c_dbl, c_u64, c_vp, c_vp])
+_reduce_adamw8_sched = _fn("zero_reduce_adamw8_step_scheduled", c_i32,
+                           [c_vp, c_i32, ctypes.POINTER(c_vp), c_i32, c_i64, c_i64] + [c_vp] * 7 +
+                           [c_i64, c_vp, c_u64, c_vp, c_vp])
+_quantize8 = _fn("zero_state8_quantize", c_i32, [c_vp, c_i64, c_i32, c_vp, c_vp, c_vp])
+_dequantize8 = _fn("zero_state8_dequantize", c_i32, [c_vp, c_vp, c_i64, c_vp, c_vp])
 _rt_blocks = _fn("zero_reduce_table_blocks", c_i64, [c_vp])
 _rt_free = _fn("zero_reduce_table_free", None, [c_vp])
 _status_string = _fn("zero_status_string", ctypes.c_char_p, [c_i32])
@@ -910,3 +930,223 @@ def prepare_flatten_params(plan: Plan, tensors: Sequence, flat, stream) -> Prepa
                  "zero_flatten_params")
     p._keep = (tp, tensors, flat)
     return p
+
+
+# --------------------------------------------------------------------------- moments in 8 bits
+
+def state8_blocks(n: int) -> int:
+    """Scale bytes of n elements: one per block of ZERO_STATE8_BLOCK, the last block maybe shorter."""
+    return -(-n // ZERO_STATE8_BLOCK)
+
+
+_STATE8 = (("master", 4), ("exp_avg", 1), ("exp_avg_scale", 1), ("exp_avg_sq", 1), ("exp_avg_sq_scale", 1))
+
+
+def _state8_ptrs(n: int, arrays, grad, param_out) -> List[int]:
+    """The seven pointers of an 8-bit update over n elements (grad None where the call takes none)."""
+    named = list(zip(arrays, _STATE8)) + [(grad, ("grad", 2)), (param_out, ("param_out", 2))]
+    for t, (what, _) in named:
+        _need(t, state8_blocks(n) if what.endswith("_scale") else n, what)
+    return [_ptr(t, size, what) for t, (what, size) in named]
+
+
+def _seed(seed: int) -> int:
+    if not 0 <= int(seed) < 1 << 64:
+        raise ValueError("seed must lie in [0, 2^64)")
+    return int(seed)
+
+
+def prepare_shard_adamw8_step(master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad, param_out,
+                              lr: float, beta1: float, beta2: float, eps: float, weight_decay: float,
+                              seed: int = 0, first_element: int = 0, clip_scale=None, n: Optional[int] = None,
+                              stream=None) -> Prepared:
+    """zero_shard_adamw8_step with its arguments marshalled once; call the result with the step number."""
+    n = master.numel() if n is None else n
+    arrays = (master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale)
+    _need(clip_scale, 1, "clip_scale")
+    p = Prepared(_adamw8, _state8_ptrs(n, arrays, grad, param_out) +
+                 [n, first_element, 1, lr, beta1, beta2, eps, weight_decay, _seed(seed),
+                  _ptr(clip_scale, 4, "clip_scale"), _stream(stream, master)],
+                 "zero_shard_adamw8_step", step_index=9)
+    p._keep = (arrays, grad, param_out, clip_scale)
+    return p
+
+
+def zero_shard_adamw8_step(master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad, param_out,
+                           step: int, lr: float, beta1: float, beta2: float, eps: float, weight_decay: float,
+                           seed: int = 0, first_element: int = 0, clip_scale=None, n: Optional[int] = None,
+                           stream=None) -> None:
+    """zero_shard_adamw_step with both moments in 8 bits: exp_avg and exp_avg_sq hold one-byte e4m3 codes
+    (torch.uint8 or torch.float8_e4m3fn), the *_scale tensors a power-of-two byte per 128 elements. `seed`
+    is the run's, `first_element` the number of element 0 in its random words (a multiple of 128)."""
+    prepare_shard_adamw8_step(master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad, param_out, lr,
+                              beta1, beta2, eps, weight_decay, seed, first_element, clip_scale, n, stream)(step)
+
+
+def prepare_shard_adamw8_step_scheduled(master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad,
+                                        param_out, schedule: AdamWSchedule, seed: int = 0,
+                                        first_element: int = 0, clip_scale=None, stream=None) -> Prepared:
+    """zero_shard_adamw8_step_scheduled with its arguments marshalled once."""
+    n = master.numel()
+    arrays = (master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale)
+    _need(clip_scale, 1, "clip_scale")
+    p = Prepared(_adamw8_sched, _state8_ptrs(n, arrays, grad, param_out) +
+                 [n, first_element, schedule.handle, _seed(seed), _ptr(clip_scale, 4, "clip_scale"),
+                  _stream(stream, master)], "zero_shard_adamw8_step_scheduled")
+    p._keep = (arrays, grad, param_out, schedule, clip_scale)
+    return p
+
+
+def zero_shard_adamw8_step_scheduled(master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad,
+                                     param_out, schedule: AdamWSchedule, seed: int = 0, first_element: int = 0,
+                                     clip_scale=None, stream=None) -> None:
+    """zero_shard_adamw8_step with the step's scalars and number read on the device from `schedule`."""
+    prepare_shard_adamw8_step_scheduled(master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad,
+                                        param_out, schedule, seed, first_element, clip_scale, stream)()
+
+
+class MultiTensor8Table:
+    """Owner of a zero_mt8_table: a fixed list of per-parameter tensors with their moments in 8 bits,
+    described once in device memory (on the current device), stepped in one launch. The tensors are held
+    here, so their buffers outlive the table."""
+
+    def __init__(self, masters, exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_scales, grads, params_out,
+                 first_element: int = 0):
+        lists = (masters, exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_scales, grads, params_out)
+        T = len(masters)
+        if any(len(x) != T for x in lists):
+            raise ValueError("the seven lists must have the same length")
+        rows = [_state8_ptrs(x[0].numel(), x[:5], x[5], x[6]) for x in zip(*lists)]
+        tabs = [(c_vp * max(T, 1))(*[row[k] for row in rows]) for k in range(7)]
+        ns = (c_i64 * max(T, 1))(*[t.numel() for t in masters])
+        h = c_vp()
+        _check(_mt8_create(*tabs, ns, T, first_element, ctypes.byref(h)), "zero_mt8_table_create")
+        self._h = h
+        self._free = _mt8_free         # held by the instance for interpreter exit
+        self._keep = lists
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        free = getattr(self, "_free", None)
+        if h is not None and h.value and free is not None:
+            free(h)
+            h.value = None
+
+    @property
+    def handle(self) -> c_vp:
+        return self._h
+
+    @property
+    def blocks(self) -> int:
+        return int(_mt8_blocks(self._h))
+
+    def _stream_of(self, stream) -> int:
+        if stream is not None:
+            return int(stream)
+        return _stream(None, self._keep[0][0]) if self._keep[0] else 0
+
+    def prepare_step(self, lr: float, beta1: float, beta2: float, eps: float, weight_decay: float, seed: int = 0,
+                     clip_scale=None, stream=None) -> Prepared:
+        """zero_mt8_table_adamw8_step with its arguments marshalled once; call the result with the step."""
+        _need(clip_scale, 1, "clip_scale")
+        p = Prepared(_mt8_step, [self._h, 1, lr, beta1, beta2, eps, weight_decay, _seed(seed),
+                                 _ptr(clip_scale, 4, "clip_scale"), self._stream_of(stream)],
+                     "zero_mt8_table_adamw8_step", step_index=1)
+        p._keep = (self, clip_scale)
+        return p
+
+    def step(self, step: int, lr: float, beta1: float, beta2: float, eps: float, weight_decay: float,
+             seed: int = 0, clip_scale=None, stream=None) -> None:
+        self.prepare_step(lr, beta1, beta2, eps, weight_decay, seed, clip_scale, stream)(step)
+
+    def prepare_step_scheduled(self, schedule: AdamWSchedule, seed: int = 0, clip_scale=None,
+                               stream=None) -> Prepared:
+        """zero_mt8_table_adamw8_step_scheduled with its arguments marshalled once."""
+        _need(clip_scale, 1, "clip_scale")
+        p = Prepared(_mt8_step_sched, [self._h, schedule.handle, _seed(seed), _ptr(clip_scale, 4, "clip_scale"),
+                                       self._stream_of(stream)], "zero_mt8_table_adamw8_step_scheduled")
+        p._keep = (self, schedule, clip_scale)
+        return p
+
+    def step_scheduled(self, schedule: AdamWSchedule, seed: int = 0, clip_scale=None, stream=None) -> None:
+        self.prepare_step_scheduled(schedule, seed, clip_scale, stream)()
+
+
+def _reduce8_args(plan: Plan, rank: int, replicas, begin: int, count: int, arrays, param_out, shard_grad,
+                  clip_scale):
+    """The arguments up to shard_grad of zero_reduce_adamw8_step; the state arrays are the rank's shard ([S])."""
+    for r in replicas:
+        _need(r, count, "a replica")
+    _need(shard_grad, plan.shard_numel, "shard_grad")
+    _need(clip_scale, 1, "clip_scale")
+    ptrs = (c_vp * max(len(replicas), 1))(*[_ptr(r, 2, "replica") for r in replicas])
+    state = _state8_ptrs(plan.shard_numel, arrays, None, param_out)
+    return [plan.handle, rank, ptrs, len(replicas), begin, count] + state[:5] + [
+        state[6], _ptr(shard_grad, 2, "shard_grad")]
+
+
+def prepare_reduce_adamw8_step(plan: Plan, rank: int, replicas: Sequence, begin: int, count: int, master, exp_avg,
+                               exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, param_out, lr: float, beta1: float,
+                               beta2: float, eps: float, weight_decay: float, seed: int = 0, first_element: int = 0,
+                               clip_scale=None, shard_grad=None, stream=None) -> Prepared:
+    """zero_reduce_adamw8_step with its arguments marshalled once; call the result with the step number."""
+    arrays = (master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale)
+    args = _reduce8_args(plan, rank, replicas, begin, count, arrays, param_out, shard_grad, clip_scale)
+    p = Prepared(_reduce_adamw8, args + [first_element, 1, lr, beta1, beta2, eps, weight_decay, _seed(seed),
+                                         _ptr(clip_scale, 4, "clip_scale"), _stream(stream, master)],
+                 "zero_reduce_adamw8_step", step_index=14)
+    p._keep = (args, plan, replicas, arrays, param_out, shard_grad, clip_scale)
+    return p
+
+
+def zero_reduce_adamw8_step(plan: Plan, rank: int, replicas: Sequence, begin: int, count: int, master, exp_avg,
+                            exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, param_out, step: int, lr: float,
+                            beta1: float, beta2: float, eps: float, weight_decay: float, seed: int = 0,
+                            first_element: int = 0, clip_scale=None, shard_grad=None, stream=None) -> None:
+    """The rank's averaged gradient and its 8-bit AdamW update in one pass: the bits of zero_grad_reduce_shard
+    then zero_shard_adamw8_step. The window's part of the shard starts and ends at whole blocks of 128."""
+    prepare_reduce_adamw8_step(plan, rank, replicas, begin, count, master, exp_avg, exp_avg_scale, exp_avg_sq,
+                               exp_avg_sq_scale, param_out, lr, beta1, beta2, eps, weight_decay, seed,
+                               first_element, clip_scale, shard_grad, stream)(step)
+
+
+def prepare_reduce_adamw8_step_scheduled(plan: Plan, rank: int, replicas: Sequence, begin: int, count: int, master,
+                                         exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, param_out,
+                                         schedule: AdamWSchedule, seed: int = 0, first_element: int = 0,
+                                         clip_scale=None, shard_grad=None, stream=None) -> Prepared:
+    """zero_reduce_adamw8_step_scheduled with its arguments marshalled once."""
+    arrays = (master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale)
+    args = _reduce8_args(plan, rank, replicas, begin, count, arrays, param_out, shard_grad, clip_scale)
+    p = Prepared(_reduce_adamw8_sched, args + [first_element, schedule.handle, _seed(seed),
+                                               _ptr(clip_scale, 4, "clip_scale"), _stream(stream, master)],
+                 "zero_reduce_adamw8_step_scheduled")
+    p._keep = (args, plan, replicas, arrays, param_out, shard_grad, schedule, clip_scale)
+    return p
+
+
+def zero_reduce_adamw8_step_scheduled(plan: Plan, rank: int, replicas: Sequence, begin: int, count: int, master,
+                                      exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, param_out,
+                                      schedule: AdamWSchedule, seed: int = 0, first_element: int = 0,
+                                      clip_scale=None, shard_grad=None, stream=None) -> None:
+    """zero_reduce_adamw8_step with the step's scalars and number read on the device from `schedule`."""
+    prepare_reduce_adamw8_step_scheduled(plan, rank, replicas, begin, count, master, exp_avg, exp_avg_scale,
+                                         exp_avg_sq, exp_avg_sq_scale, param_out, schedule, seed, first_element,
+                                         clip_scale, shard_grad, stream)()
+
+
+def zero_state8_quantize(x, codes, scales, second_moment: bool = False, stream=None) -> None:
+    """fp32 moments into e4m3 codes (one byte an element) and scale bytes, to nearest even."""
+    n = x.numel()
+    _need(codes, n, "codes")
+    _need(scales, state8_blocks(n), "scales")
+    _check(_quantize8(_ptr(x, 4, "x"), n, int(second_moment), _ptr(codes, 1, "codes"), _ptr(scales, 1, "scales"),
+                      _stream(stream, x)), "zero_state8_quantize")
+
+
+def zero_state8_dequantize(codes, scales, out, stream=None) -> None:
+    """The fp32 values of codes and scale bytes; out's length gives the count."""
+    n = out.numel()
+    _need(codes, n, "codes")
+    _need(scales, state8_blocks(n), "scales")
+    _check(_dequantize8(_ptr(codes, 1, "codes"), _ptr(scales, 1, "scales"), n, _ptr(out, 4, "out"),
+                        _stream(stream, out)), "zero_state8_dequantize")

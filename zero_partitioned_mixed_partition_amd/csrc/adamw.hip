@@ -30,6 +30,7 @@
 #include "device_common.hpp"
 #include "internal.hpp"
 #include "schedule.hpp"
+#include "schedule_device.hpp"
 
 #pragma clang fp contract(off)
 
@@ -216,15 +217,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(float* __restrict__ mas
     adamw_body<E>(master, m, v, grad, param, n, c, clip);
 }
 
-// A step schedule's device state: the scalars of the next step to apply and
-// the number of updates applied so far. The scheduled AdamW reads `next`; the
-// advance kernel, once per step, moves both on.
-struct alignas(64) AdamState {
-    AdamScalars next;
-    int64_t applied;
-    int64_t unused[3];
-};
-static_assert(sizeof(AdamState) == 64, "one 64-byte state");
+using zero::adam::AdamState;
 
 // The flat update with the step's scalars read from the schedule's state (one
 // 32-byte load per wave, beside the clip coefficient's), so a captured graph
@@ -575,14 +568,6 @@ extern "C" zero_status zero_shard_adamw_step(float* master, float* exp_avg, floa
 
 // ------------------------------------------------------------ step schedule
 
-struct zero_adamw_schedule {
-    int device = -1;
-    void* mem = nullptr;               // the state, then the table
-    AdamState* state = nullptr;
-    const AdamScalars* table = nullptr;
-    int64_t length = 0;
-};
-
 extern "C" zero_status zero_adamw_step_scalars(int64_t step, double lr, double beta1, double beta2,
                                                double eps, double weight_decay, float* out) {
     static const char* const who = "zero_adamw_step_scalars";
@@ -662,9 +647,9 @@ extern "C" zero_status zero_adamw_schedule_applied(const zero_adamw_schedule* sc
     return st;
 }
 
-namespace {
+using zero::adam::check_schedule_device;
 
-zero_status check_schedule_device(const zero_adamw_schedule* schedule, const char* who) {
+zero_status zero::adam::check_schedule_device(const zero_adamw_schedule* schedule, const char* who) {
     int dev = -1;
     const zero_status st = zero::check_hip(hipGetDevice(&dev), who);
     if (st != ZERO_OK) return st;
@@ -674,8 +659,6 @@ zero_status check_schedule_device(const zero_adamw_schedule* schedule, const cha
                                            std::to_string(dev));
     return ZERO_OK;
 }
-
-}  // namespace
 
 extern "C" zero_status zero_adamw_schedule_advance(zero_adamw_schedule* schedule, const float* clip_scale,
                                                    hipStream_t stream) {

@@ -1,0 +1,822 @@
+// AdamW with the two moments held in 8 bits (gfx950): the flat shard, many
+// tensors through a device table, and the reduce and the update in one pass;
+// and the moments' conversions to and from fp32. The format is state8.hpp's.
+//
+// "Zero Redundancy Optimizer (ZeRO) and Fully Sharded Data Parallelism (FSDP):
+// Mathematical Foundations ...", section "Static Memory Allocation" (fp32
+// master, m_t and v_t are 12 of the 16 bytes of a parameter; here the moments
+// take 2.02 bytes instead of 8) and "Execution Flow for ZeRO-1" steps 3-4.
+//
+// Per element: the moments are decoded, updated with the 32-bit AdamW's fp32
+// operations in its order (the update uses the fp32 m and v, before they are
+// rounded), and encoded with the block's new scale. A block is held by 16 or
+// 32 neighbouring lanes of one wave, so its maximum is a few cross-lane
+// operations and every array is read and written once: 16 bytes an element and
+// 4 per block of 128.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <new>
+#include <string>
+#include <vector>
+
+#include "device_common.hpp"
+#include "internal.hpp"
+#include "schedule_device.hpp"
+#include "state8.hpp"
+
+#pragma clang fp contract(off)
+
+namespace {
+
+using zero::dev::f32x4;
+using zero::dev::u32x2;
+using zero::dev::u32x4;
+using zero::adam::AdamState;
+using AdamScalars = zero::adam::StepScalars;
+using zero::state8::Key;
+using zero::state8::Words;
+using zero::state8::kBlock;
+
+constexpr int kThreads = 256;
+
+#ifndef ZERO_ADAMW8_EPT
+#define ZERO_ADAMW8_EPT 8
+#endif
+constexpr int kEpt = ZERO_ADAMW8_EPT;          // consecutive elements a lane
+constexpr int64_t kChunk = int64_t(kThreads) * kEpt;
+static_assert(kChunk % kBlock == 0, "whole blocks a workgroup");
+
+// The arrays of one update.
+struct Arrays {
+    float* p;
+    uint8_t* m;
+    uint8_t* ms;
+    uint8_t* v;
+    uint8_t* vs;
+    const uint16_t* g;
+    uint16_t* o;
+};
+
+// One element, in zero_shard_adamw_step's documented order; every line is one
+// IEEE fp32 operation.
+__device__ __forceinline__ void adam_elem(float& p, float& m, float& v, float g, const AdamScalars& c) {
+    const float bm = c.beta1 * m;
+    const float gm = c.one_minus_beta1 * g;
+    m = bm + gm;
+    const float bv = c.beta2 * v;
+    const float gg = g * g;
+    const float gv = c.one_minus_beta2 * gg;
+    v = bv + gv;
+    p = p * c.decay;
+    const float root = sqrtf(v);
+    const float denom = root / c.sqrt_bc2 + c.eps;
+    const float ratio = m / denom;
+    p = p - c.step_size * ratio;
+}
+
+__device__ __forceinline__ float read_clip(const float* clip_scale) {
+    return clip_scale != nullptr ? *clip_scale : 1.0f;
+}
+
+// What a lane holds of its kEpt elements.
+struct Lane {
+    float p[kEpt];
+    uint32_t m[kEpt / 4], v[kEpt / 4];     // codes, four a word
+    uint32_t ms = 0, vs = 0;
+    int live = 0;                          // of the kEpt elements, those below n
+};
+
+// VEC: every array allows accesses of kEpt elements. Lanes with fewer than
+// kEpt elements left, and all lanes where VEC does not hold, go one by one.
+template <bool VEC>
+__device__ __forceinline__ void load_state(Lane& l, const Arrays& a, int64_t n, int64_t i) {
+    const int64_t left = n - i;
+    l.live = left <= 0 ? 0 : (left < kEpt ? static_cast<int>(left) : kEpt);
+#pragma unroll
+    for (int k = 0; k < kEpt; ++k) l.p[k] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kEpt / 4; ++w) l.m[w] = l.v[w] = 0;
+    if (l.live == 0) return;
+    l.ms = a.ms[i / kBlock];
+    l.vs = a.vs[i / kBlock];
+    if (VEC && l.live == kEpt) {
+#pragma unroll
+        for (int w = 0; w < kEpt / 4; ++w) {
+            const f32x4 x = zero::dev::ld_stream(reinterpret_cast<const f32x4*>(a.p + i) + w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) l.p[4 * w + k] = x[k];
+        }
+        if (kEpt == 8) {
+            const u32x2 m = zero::dev::ld_stream(reinterpret_cast<const u32x2*>(a.m + i));
+            const u32x2 v = zero::dev::ld_stream(reinterpret_cast<const u32x2*>(a.v + i));
+            l.m[0] = m[0];
+            l.v[0] = v[0];
+            l.m[kEpt / 4 - 1] = m[1];
+            l.v[kEpt / 4 - 1] = v[1];
+        } else {
+            l.m[0] = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(a.m + i));
+            l.v[0] = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(a.v + i));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kEpt; ++k) {
+            if (k < l.live) {
+                l.p[k] = a.p[i + k];
+                l.m[k / 4] |= static_cast<uint32_t>(a.m[i + k]) << (8 * (k % 4));
+                l.v[k / 4] |= static_cast<uint32_t>(a.v[i + k]) << (8 * (k % 4));
+            }
+        }
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load_grad(float (&g)[kEpt], const uint16_t* grad, int live, int64_t i) {
+#pragma unroll
+    for (int k = 0; k < kEpt; ++k) g[k] = 0.0f;
+    if (VEC && live == kEpt) {
+#pragma unroll
+        for (int w = 0; w < kEpt / 4; ++w) {
+            const u32x2 x = zero::dev::ld_stream(reinterpret_cast<const u32x2*>(grad + i) + w);
+            g[4 * w] = zero::dev::lo_bf16(x[0]);
+            g[4 * w + 1] = zero::dev::hi_bf16(x[0]);
+            g[4 * w + 2] = zero::dev::lo_bf16(x[1]);
+            g[4 * w + 3] = zero::dev::hi_bf16(x[1]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kEpt; ++k)
+            if (k < live) g[k] = zero::dev::bf16_to_f32(grad[i + k]);
+    }
+}
+
+// Updates a lane's elements from their clipped gradients and writes them back.
+// Every lane of the wave calls it (the block maxima cross lanes).
+template <bool VEC>
+__device__ __forceinline__ void update_and_store(Lane& l, const float (&g)[kEpt], const Arrays& a, int64_t i,
+                                                 int64_t first, const AdamScalars& c, Key key) {
+    float m[kEpt], v[kEpt];
+#pragma unroll
+    for (int w = 0; w < kEpt / 4; ++w) {
+        zero::state8::decode4(l.m[w], l.ms, m + 4 * w);
+        zero::state8::decode4(l.v[w], l.vs, v + 4 * w);
+    }
+    uint32_t mm = 0, vm = 0;
+#pragma unroll
+    for (int k = 0; k < kEpt; ++k) {
+        adam_elem(l.p[k], m[k], v[k], g[k], c);
+        if (k < l.live) {
+            mm = zero::state8::umax(mm, zero::state8::magnitude(m[k]));
+            vm = zero::state8::umax(vm, zero::state8::magnitude(v[k]));
+        }
+    }
+    const uint32_t ms = zero::state8::scale_byte(zero::state8::block_max<kEpt>(mm));
+    const uint32_t vs = zero::state8::scale_byte(zero::state8::block_max<kEpt>(vm));
+    if (l.live == 0) return;
+    const uint64_t e = static_cast<uint64_t>(first + i);
+    const Words words = zero::state8::group_words(e >> 3, key);
+    uint32_t r = words.a + (static_cast<uint32_t>(e) & 7u) * words.b;
+    uint32_t mc[kEpt], vc[kEpt], mw[kEpt / 4], vw[kEpt / 4];
+#pragma unroll
+    for (int k = 0; k < kEpt; ++k) {
+        mc[k] = zero::state8::first_code(m[k], ms, r);
+        vc[k] = zero::state8::second_code(v[k], vs, r);
+        r += words.b;
+    }
+#pragma unroll
+    for (int w = 0; w < kEpt / 4; ++w) {
+        mw[w] = zero::state8::pack4(mc[4 * w], mc[4 * w + 1], mc[4 * w + 2], mc[4 * w + 3]);
+        vw[w] = zero::state8::pack4(vc[4 * w], vc[4 * w + 1], vc[4 * w + 2], vc[4 * w + 3]);
+        if (ms == 255u) mw[w] = 0;
+        if (vs == 255u) vw[w] = 0;
+    }
+    if (i % kBlock == 0) {                 // the block's first lane
+        a.ms[i / kBlock] = static_cast<uint8_t>(ms);
+        a.vs[i / kBlock] = static_cast<uint8_t>(vs);
+    }
+    if (VEC && l.live == kEpt) {
+#pragma unroll
+        for (int w = 0; w < kEpt / 4; ++w) {
+            const f32x4 x = {l.p[4 * w], l.p[4 * w + 1], l.p[4 * w + 2], l.p[4 * w + 3]};
+            zero::dev::st_stream(reinterpret_cast<f32x4*>(a.p + i) + w, x);
+        }
+        if (kEpt == 8) {
+            zero::dev::st_stream(reinterpret_cast<u32x2*>(a.m + i), u32x2{mw[0], mw[kEpt / 4 - 1]});
+            zero::dev::st_stream(reinterpret_cast<u32x2*>(a.v + i), u32x2{vw[0], vw[kEpt / 4 - 1]});
+            const u32x4 o = {zero::dev::pack_bf16(l.p[0], l.p[1]), zero::dev::pack_bf16(l.p[2], l.p[3]),
+                             zero::dev::pack_bf16(l.p[kEpt - 4], l.p[kEpt - 3]),
+                             zero::dev::pack_bf16(l.p[kEpt - 2], l.p[kEpt - 1])};
+            zero::dev::st_stream(reinterpret_cast<u32x4*>(a.o + i), o);
+        } else {
+            zero::dev::st_stream(reinterpret_cast<uint32_t*>(a.m + i), mw[0]);
+            zero::dev::st_stream(reinterpret_cast<uint32_t*>(a.v + i), vw[0]);
+            const u32x2 o = {zero::dev::pack_bf16(l.p[0], l.p[1]), zero::dev::pack_bf16(l.p[2], l.p[3])};
+            zero::dev::st_stream(reinterpret_cast<u32x2*>(a.o + i), o);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kEpt; ++k) {
+            if (k < l.live) {
+                a.p[i + k] = l.p[k];
+                a.m[i + k] = static_cast<uint8_t>(mw[k / 4] >> (8 * (k % 4)));
+                a.v[i + k] = static_cast<uint8_t>(vw[k / 4] >> (8 * (k % 4)));
+                a.o[i + k] = static_cast<uint16_t>(zero::dev::f32_to_bf16(l.p[k]));
+            }
+        }
+    }
+}
+
+// One workgroup's kChunk elements from `base` of arrays of n elements.
+template <bool VEC>
+__device__ __forceinline__ void update_chunk(const Arrays& a, int64_t n, int64_t base, int64_t first,
+                                             const AdamScalars& c, Key key, const float* clip_scale) {
+    const int64_t i = base + int64_t(threadIdx.x) * kEpt;
+    Lane l;
+    load_state<VEC>(l, a, n, i);
+    float g[kEpt];
+    load_grad<VEC>(g, a.g, l.live, i);
+    const float clip = read_clip(clip_scale);   // after the loads are issued
+    if (!isfinite(clip)) return;                // the same in every lane
+#pragma unroll
+    for (int k = 0; k < kEpt; ++k) g[k] = g[k] * clip;
+    update_and_store<VEC>(l, g, a, i, first, c, key);
+}
+
+// The step's scalars and key: from the call, or from a schedule's state.
+struct CallStep {
+    AdamScalars c;
+    Key key;
+    __device__ __forceinline__ AdamScalars scalars() const { return c; }
+    __device__ __forceinline__ Key random_key() const { return key; }
+};
+struct ScheduleStep {
+    const AdamState* state;
+    uint64_t seed;
+    __device__ __forceinline__ AdamScalars scalars() const { return state->next; }
+    __device__ __forceinline__ Key random_key() const {
+        return zero::state8::step_key(seed, static_cast<uint64_t>(state->applied + 1));
+    }
+};
+
+__device__ __forceinline__ int64_t workgroup() {
+    return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+}
+
+template <bool VEC, typename Step>
+__global__ __launch_bounds__(kThreads) void adamw8_kernel(Arrays a, int64_t n, int64_t first, Step step,
+                                                          const float* __restrict__ clip_scale) {
+    update_chunk<VEC>(a, n, workgroup() * kChunk, first, step.scalars(), step.random_key(), clip_scale);
+}
+
+// Many tensors: one 128-byte descriptor per non-empty tensor and, per
+// workgroup, the index of its descriptor.
+struct alignas(128) Desc {
+    Arrays a;
+    int64_t n;
+    int64_t first;          // the tensor's first element, in the list's numbering of random words
+    int64_t first_block;
+    int64_t vec;
+};
+static_assert(sizeof(Desc) == 128, "one 128-byte descriptor per tensor");
+
+template <typename Step>
+__global__ __launch_bounds__(kThreads) void adamw8_table_kernel(const Desc* __restrict__ table,
+                                                                const uint32_t* __restrict__ index,
+                                                                int64_t blk0, int64_t per, Step step,
+                                                                const float* __restrict__ clip_scale) {
+    const int64_t blk = blk0 + static_cast<int64_t>(blockIdx.x);
+    const Desc d = table[index[zero::dev::xcd_major_entry(blk0, per)]];
+    const int64_t base = (blk - d.first_block) * kChunk;
+    if (d.vec)
+        update_chunk<true>(d.a, d.n, base, d.first, step.scalars(), step.random_key(), clip_scale);
+    else
+        update_chunk<false>(d.a, d.n, base, d.first, step.scalars(), step.random_key(), clip_scale);
+}
+
+// The reduce and the update in one pass: the averaged gradient is the
+// reduce's (fp32 sum in replica order, one division by R, one rounding to
+// bf16), used where it is formed.
+struct Replicas {
+    const uint16_t* p[ZERO_MAX_REPLICAS];
+};
+constexpr int kReplicaBatch = 8;           // replica loads in flight per lane
+
+template <bool VEC>
+__device__ __forceinline__ void mean_grad(float (&g)[kEpt], const Replicas& reps, int n_rep, int64_t src_off,
+                                          int live, int64_t i) {
+    float acc[kEpt];
+#pragma unroll
+    for (int k = 0; k < kEpt; ++k) acc[k] = 0.0f;
+    const float count = static_cast<float>(n_rep);
+    if (VEC && live == kEpt) {
+        typedef typename std::conditional<kEpt == 8, u32x4, u32x2>::type V;
+        zero::dev::for_replicas<kReplicaBatch, V>(reps.p, n_rep, src_off, i / kEpt, [&](V x) {
+#pragma unroll
+            for (int w = 0; w < kEpt / 2; ++w) {
+                acc[2 * w] = acc[2 * w] + zero::dev::lo_bf16(x[w]);
+                acc[2 * w + 1] = acc[2 * w + 1] + zero::dev::hi_bf16(x[w]);
+            }
+        });
+    } else if (live > 0) {
+        for (int r = 0; r < n_rep; ++r) {
+            const uint16_t* p = reps.p[r] + src_off + i;
+#pragma unroll
+            for (int k = 0; k < kEpt; ++k)
+                if (k < live) acc[k] = acc[k] + zero::dev::bf16_to_f32(p[k]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kEpt; ++k)
+        g[k] = zero::dev::bf16_to_f32(zero::dev::f32_to_bf16(acc[k] / count));
+}
+
+template <bool VEC, typename Step>
+__global__ __launch_bounds__(kThreads) void reduce_adamw8_kernel(Replicas reps, int n_rep, int64_t src_off, Arrays a,
+                                                                 uint16_t* __restrict__ grad_out, int64_t n,
+                                                                 int64_t first, Step step,
+                                                                 const float* __restrict__ clip_scale) {
+    const int64_t i = workgroup() * kChunk + int64_t(threadIdx.x) * kEpt;
+    Lane l;
+    load_state<VEC>(l, a, n, i);
+    float g[kEpt];
+    mean_grad<VEC>(g, reps, n_rep, src_off, l.live, i);
+    if (grad_out != nullptr) {
+        if (VEC && l.live == kEpt) {
+#pragma unroll
+            for (int w = 0; w < kEpt / 4; ++w)
+                zero::dev::st_stream(reinterpret_cast<u32x2*>(grad_out + i) + w,
+                                     u32x2{zero::dev::pack_bf16(g[4 * w], g[4 * w + 1]),
+                                           zero::dev::pack_bf16(g[4 * w + 2], g[4 * w + 3])});
+        } else {
+#pragma unroll
+            for (int k = 0; k < kEpt; ++k)
+                if (k < l.live) grad_out[i + k] = static_cast<uint16_t>(zero::dev::f32_to_bf16(g[k]));
+        }
+    }
+    const float clip = read_clip(clip_scale);
+    if (!isfinite(clip)) return;
+#pragma unroll
+    for (int k = 0; k < kEpt; ++k) g[k] = g[k] * clip;
+    update_and_store<VEC>(l, g, a, i, first, step.scalars(), step.random_key());
+}
+
+// ------------------------------------------------------------ conversions
+
+// fp32 to codes and scales, rounded to nearest even.
+template <bool VEC>
+__global__ __launch_bounds__(kThreads) void quantize_kernel(const float* __restrict__ x, uint8_t* __restrict__ codes,
+                                                            uint8_t* __restrict__ scales, int64_t n, int second) {
+    const int64_t i = (workgroup() * kThreads + threadIdx.x) * 4;
+    const int64_t left = n - i;
+    const int live = left <= 0 ? 0 : (left < 4 ? static_cast<int>(left) : 4);
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (VEC && live == 4) {
+        const f32x4 q = zero::dev::ld_stream(reinterpret_cast<const f32x4*>(x + i));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = q[k];
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < live) v[k] = x[i + k];
+    }
+    uint32_t big = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) big = zero::state8::umax(big, zero::state8::magnitude(v[k]));
+    const uint32_t byte = zero::state8::scale_byte(zero::state8::block_max<4>(big));
+    if (live == 0) return;
+    uint32_t c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] = zero::state8::nearest_code(v[k], byte, second != 0);
+    uint32_t w = zero::state8::pack4(c[0], c[1], c[2], c[3]);
+    if (byte == 255u) w = 0;
+    if (i % kBlock == 0) scales[i / kBlock] = static_cast<uint8_t>(byte);
+    if (VEC && live == 4) {
+        zero::dev::st_stream(reinterpret_cast<uint32_t*>(codes + i), w);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < live) codes[i + k] = static_cast<uint8_t>(w >> (8 * k));
+    }
+}
+
+template <bool VEC>
+__global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __restrict__ codes,
+                                                              const uint8_t* __restrict__ scales,
+                                                              float* __restrict__ out, int64_t n) {
+    const int64_t i = (workgroup() * kThreads + threadIdx.x) * 4;
+    const int64_t left = n - i;
+    const int live = left <= 0 ? 0 : (left < 4 ? static_cast<int>(left) : 4);
+    if (live == 0) return;
+    const uint32_t byte = scales[i / kBlock];
+    uint32_t w = 0;
+    if (VEC && live == 4) {
+        w = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(codes + i));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < live) w |= static_cast<uint32_t>(codes[i + k]) << (8 * k);
+    }
+    float v[4];
+    zero::state8::decode4(w, byte, v);
+    if (VEC && live == 4) {
+        zero::dev::st_stream(reinterpret_cast<f32x4*>(out + i), f32x4{v[0], v[1], v[2], v[3]});
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < live) out[i + k] = v[k];
+    }
+}
+
+// ------------------------------------------------------------ host side
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+bool vector_ok(const Arrays& a) {
+    return aligned(a.p, 16) && aligned(a.m, kEpt) && aligned(a.v, kEpt) && aligned(a.g, 2 * kEpt) &&
+           aligned(a.o, 2 * kEpt);
+}
+
+// Rows of workgroups: a grid dimension holds fewer than 2^32 work-items.
+zero_status grid_for(int64_t items, int64_t per_workgroup, dim3* grid, const char* who) {
+    constexpr int64_t kMaxRow = (int64_t(1) << 32) / kThreads - 1;
+    const int64_t blocks = (items - 1) / per_workgroup + 1;
+    const int64_t rows = (blocks + kMaxRow - 1) / kMaxRow;
+    if (rows > 0xFFFF) return zero::fail(ZERO_ERANGE, std::string(who) + ": n too large for one dispatch");
+    *grid = dim3(static_cast<unsigned>((blocks + rows - 1) / rows), static_cast<unsigned>(rows));
+    return ZERO_OK;
+}
+
+// first: a multiple of the block, and first + n an int64.
+zero_status check_first(int64_t first, int64_t n, const char* who) {
+    if (first < 0 || first % kBlock != 0)
+        return zero::fail(ZERO_EINVAL, std::string(who) + ": first_element must be a multiple of " +
+                                           std::to_string(kBlock) + ", >= 0");
+    if (n > INT64_MAX - first) return zero::fail(ZERO_ERANGE, std::string(who) + ": first_element + n overflows");
+    return ZERO_OK;
+}
+
+// No NULL array, no written array overlapping another array of the update
+// (n > 0). `extra`: another written span (p NULL for none).
+std::string array_clash(const Arrays& a, int64_t n) {
+    const size_t nb = static_cast<size_t>(zero::state8::blocks_of(n)), b = static_cast<size_t>(n);
+    const zero::Span wr[] = {{a.p, 4 * b, "master"},          {a.m, b, "exp_avg"}, {a.ms, nb, "exp_avg_scale"},
+                             {a.v, b, "exp_avg_sq"}, {a.vs, nb, "exp_avg_sq_scale"}, {a.o, 2 * b, "param_out"}};
+    const zero::Span rd[] = {{a.g, 2 * b, "grad"}};
+    return zero::first_overlap(wr, 6, rd, 1);
+}
+
+bool any_null(const Arrays& a) { return !a.p || !a.m || !a.ms || !a.v || !a.vs || !a.g || !a.o; }
+
+template <typename Step>
+zero_status launch_flat(const Arrays& a, int64_t n, int64_t first, const Step& step, const float* clip_scale,
+                        hipStream_t stream, const char* who) {
+    using zero::fail;
+    zero_status st = check_first(first, n, who);
+    if (st != ZERO_OK) return st;
+    if (n == 0) return ZERO_OK;
+    if (any_null(a)) return fail(ZERO_EINVAL, std::string(who) + ": NULL array");
+    const std::string clash = array_clash(a, n);
+    if (!clash.empty()) return fail(ZERO_EINVAL, std::string(who) + ": " + clash);
+    dim3 grid;
+    st = grid_for(n, kChunk, &grid, who);
+    if (st != ZERO_OK) return st;
+    if (vector_ok(a))
+        hipLaunchKernelGGL((adamw8_kernel<true, Step>), grid, dim3(kThreads), 0, stream, a, n, first, step, clip_scale);
+    else
+        hipLaunchKernelGGL((adamw8_kernel<false, Step>), grid, dim3(kThreads), 0, stream, a, n, first, step, clip_scale);
+    return zero::check_hip(hipGetLastError(), who);
+}
+
+}  // namespace
+
+extern "C" zero_status zero_shard_adamw8_step(float* master, uint8_t* exp_avg, uint8_t* exp_avg_scale,
+                                              uint8_t* exp_avg_sq, uint8_t* exp_avg_sq_scale, const uint16_t* grad,
+                                              uint16_t* param_out, int64_t n, int64_t first_element, int64_t step,
+                                              double lr, double beta1, double beta2, double eps, double weight_decay,
+                                              uint64_t seed, const float* clip_scale, hipStream_t stream) {
+    static const char* const who = "zero_shard_adamw8_step";
+    zero::clear_error();
+    if (n < 0) return zero::fail(ZERO_EINVAL, "zero_shard_adamw8_step: n < 0");
+    zero_status st = zero::adam::check_hyper(step, lr, beta1, beta2, eps, weight_decay, who);
+    if (st != ZERO_OK) return st;
+    CallStep s{};
+    st = zero::adam::step_scalars(step, lr, beta1, beta2, weight_decay, eps, &s.c, who);
+    if (st != ZERO_OK) return st;
+    s.key = zero::state8::step_key(seed, static_cast<uint64_t>(step));
+    return launch_flat(Arrays{master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad, param_out}, n,
+                       first_element, s, clip_scale, stream, who);
+}
+
+extern "C" zero_status zero_shard_adamw8_step_scheduled(float* master, uint8_t* exp_avg, uint8_t* exp_avg_scale,
+                                                        uint8_t* exp_avg_sq, uint8_t* exp_avg_sq_scale,
+                                                        const uint16_t* grad, uint16_t* param_out, int64_t n,
+                                                        int64_t first_element, const zero_adamw_schedule* schedule,
+                                                        uint64_t seed, const float* clip_scale, hipStream_t stream) {
+    static const char* const who = "zero_shard_adamw8_step_scheduled";
+    zero::clear_error();
+    if (schedule == nullptr) return zero::fail(ZERO_EINVAL, "zero_shard_adamw8_step_scheduled: NULL schedule");
+    if (n < 0) return zero::fail(ZERO_EINVAL, "zero_shard_adamw8_step_scheduled: n < 0");
+    const zero_status st = zero::adam::check_schedule_device(schedule, who);
+    if (st != ZERO_OK) return st;
+    return launch_flat(Arrays{master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad, param_out}, n,
+                       first_element, ScheduleStep{schedule->state, seed}, clip_scale, stream, who);
+}
+
+// ------------------------------------------------------------ device table
+
+struct zero_mt8_table {
+    int device = -1;
+    void* mem = nullptr;          // descriptors, then the per-workgroup index
+    const Desc* table = nullptr;
+    const uint32_t* index = nullptr;
+    int64_t blocks = 0;           // workgroups of one step
+};
+
+extern "C" zero_status zero_mt8_table_create(float* const* masters, uint8_t* const* exp_avgs,
+                                             uint8_t* const* exp_avg_scales, uint8_t* const* exp_avg_sqs,
+                                             uint8_t* const* exp_avg_sq_scales, const uint16_t* const* grads,
+                                             uint16_t* const* params_out, const int64_t* numels, int32_t n_tensors,
+                                             int64_t first_element, zero_mt8_table** out) {
+    using zero::fail;
+    static const char* const who = "zero_mt8_table_create";
+    zero::clear_error();
+    const std::string w(who);
+    if (!out) return fail(ZERO_EINVAL, w + ": NULL out");
+    *out = nullptr;
+    if (n_tensors < 0) return fail(ZERO_EINVAL, w + ": n_tensors < 0");
+    if (n_tensors > 0 && (!masters || !exp_avgs || !exp_avg_scales || !exp_avg_sqs || !exp_avg_sq_scales || !grads ||
+                          !params_out || !numels))
+        return fail(ZERO_EINVAL, w + ": NULL array of pointers");
+    zero_status st = check_first(first_element, 0, who);
+    if (st != ZERO_OK) return st;
+    std::vector<Desc> descs;
+    std::vector<uint32_t> index;
+    zero_mt8_table* tab = nullptr;
+    try {
+        int64_t blocks = 0, first = first_element;
+        for (int32_t t = 0; t < n_tensors; ++t) {
+            const int64_t n = numels[t];
+            const std::string of = " of tensor " + std::to_string(t);
+            if (n < 0) return fail(ZERO_EINVAL, w + ": numel < 0" + of);
+            if (n == 0) continue;
+            const int64_t wgs = (n - 1) / kChunk + 1;
+            if (blocks + wgs > 0x7FFFFFFF) return fail(ZERO_ERANGE, w + ": more than 2^31 workgroups in one list");
+            const int64_t padded = zero::state8::blocks_of(n) * kBlock;
+            if (padded > INT64_MAX - first) return fail(ZERO_ERANGE, w + ": first_element + n overflows" + of);
+            Desc d{};
+            d.a = Arrays{masters[t], exp_avgs[t], exp_avg_scales[t], exp_avg_sqs[t], exp_avg_sq_scales[t], grads[t],
+                         params_out[t]};
+            if (any_null(d.a)) return fail(ZERO_EINVAL, w + ": NULL array" + of);
+            const std::string clash = array_clash(d.a, n);
+            if (!clash.empty()) return fail(ZERO_EINVAL, w + ": " + clash + of);
+            d.n = n;
+            d.first = first;
+            d.first_block = blocks;
+            d.vec = vector_ok(d.a);
+            index.insert(index.end(), static_cast<size_t>(wgs), static_cast<uint32_t>(descs.size()));
+            descs.push_back(d);
+            blocks += wgs;
+            first += padded;
+        }
+        if (blocks > 0) index = zero::xcd_major_index(index);
+        tab = new zero_mt8_table;
+        tab->blocks = blocks;
+    } catch (const std::bad_alloc&) {
+        return fail(ZERO_ENOMEM, w + ": host allocation failed");
+    }
+    if (tab->blocks > 0) {        // an empty list needs no device
+        st = zero::check_hip(hipGetDevice(&tab->device), "zero_mt8_table_create: hipGetDevice");
+        const size_t table_bytes = descs.size() * sizeof(Desc), index_bytes = index.size() * sizeof(uint32_t);
+        if (st == ZERO_OK)
+            st = zero::check_hip(hipMalloc(&tab->mem, table_bytes + index_bytes), "zero_mt8_table_create: hipMalloc");
+        if (st == ZERO_OK) {
+            tab->table = static_cast<const Desc*>(tab->mem);
+            tab->index = reinterpret_cast<const uint32_t*>(static_cast<char*>(tab->mem) + table_bytes);
+            st = zero::check_hip(hipMemcpy(tab->mem, descs.data(), table_bytes, hipMemcpyHostToDevice),
+                                 "zero_mt8_table_create: hipMemcpy");
+        }
+        if (st == ZERO_OK)
+            st = zero::check_hip(hipMemcpy(const_cast<uint32_t*>(tab->index), index.data(), index_bytes,
+                                           hipMemcpyHostToDevice), "zero_mt8_table_create: hipMemcpy");
+    }
+    if (st != ZERO_OK) {
+        if (tab->mem) (void)hipFree(tab->mem);
+        delete tab;
+        return st;
+    }
+    *out = tab;
+    return ZERO_OK;
+}
+
+extern "C" void zero_mt8_table_free(zero_mt8_table* table) {
+    if (!table) return;
+    if (table->mem) (void)hipFree(table->mem);
+    delete table;
+}
+
+extern "C" int64_t zero_mt8_table_blocks(const zero_mt8_table* table) { return table ? table->blocks : -1; }
+
+namespace {
+
+template <typename Step>
+zero_status launch_table(const zero_mt8_table* table, const Step& step, const float* clip_scale, hipStream_t stream,
+                         const char* who) {
+    // A dispatch holds fewer than 2^32 work-items: longer lists take several launches.
+    constexpr int64_t kMaxBlocks = zero::kTableLaunchBlocks;
+    for (int64_t b0 = 0; b0 < table->blocks; b0 += kMaxBlocks) {
+        const int64_t nb = table->blocks - b0 < kMaxBlocks ? table->blocks - b0 : kMaxBlocks;
+        hipLaunchKernelGGL(adamw8_table_kernel<Step>, dim3(static_cast<unsigned>(nb)), dim3(kThreads), 0, stream,
+                           table->table, table->index, b0, (nb + 7) / 8, step, clip_scale);
+        const zero_status st = zero::check_hip(hipGetLastError(), who);
+        if (st != ZERO_OK) return st;
+    }
+    return ZERO_OK;
+}
+
+zero_status check_table_device(const zero_mt8_table* table, const char* who) {
+    int dev = -1;
+    const zero_status st = zero::check_hip(hipGetDevice(&dev), who);
+    if (st != ZERO_OK) return st;
+    if (dev != table->device)
+        return zero::fail(ZERO_EINVAL, std::string(who) + ": the table lives on device " +
+                                           std::to_string(table->device) + ", the current device is " +
+                                           std::to_string(dev));
+    return ZERO_OK;
+}
+
+}  // namespace
+
+extern "C" zero_status zero_mt8_table_adamw8_step(const zero_mt8_table* table, int64_t step, double lr, double beta1,
+                                                  double beta2, double eps, double weight_decay, uint64_t seed,
+                                                  const float* clip_scale, hipStream_t stream) {
+    static const char* const who = "zero_mt8_table_adamw8_step";
+    zero::clear_error();
+    if (!table) return zero::fail(ZERO_EINVAL, "zero_mt8_table_adamw8_step: NULL table");
+    zero_status st = zero::adam::check_hyper(step, lr, beta1, beta2, eps, weight_decay, who);
+    if (st != ZERO_OK) return st;
+    CallStep s{};
+    st = zero::adam::step_scalars(step, lr, beta1, beta2, weight_decay, eps, &s.c, who);
+    if (st != ZERO_OK) return st;
+    if (table->blocks == 0) return ZERO_OK;
+    st = check_table_device(table, who);
+    if (st != ZERO_OK) return st;
+    s.key = zero::state8::step_key(seed, static_cast<uint64_t>(step));
+    return launch_table(table, s, clip_scale, stream, who);
+}
+
+extern "C" zero_status zero_mt8_table_adamw8_step_scheduled(const zero_mt8_table* table,
+                                                            const zero_adamw_schedule* schedule, uint64_t seed,
+                                                            const float* clip_scale, hipStream_t stream) {
+    static const char* const who = "zero_mt8_table_adamw8_step_scheduled";
+    zero::clear_error();
+    if (!table || !schedule)
+        return zero::fail(ZERO_EINVAL, "zero_mt8_table_adamw8_step_scheduled: NULL table or schedule");
+    zero_status st = zero::adam::check_schedule_device(schedule, who);
+    if (st != ZERO_OK) return st;
+    if (table->blocks == 0) return ZERO_OK;
+    st = check_table_device(table, who);
+    if (st != ZERO_OK) return st;
+    return launch_table(table, ScheduleStep{schedule->state, seed}, clip_scale, stream, who);
+}
+
+// ------------------------------------------------------------ reduce and update
+
+namespace {
+
+template <typename Step>
+zero_status launch_reduce(const zero_plan* plan, int32_t rank, const uint16_t* const* replicas, int32_t n_replicas,
+                          int64_t begin, int64_t count, Arrays a, uint16_t* shard_grad, int64_t first,
+                          const Step& step, const float* clip_scale, hipStream_t stream, const char* who) {
+    using zero::fail;
+    const std::string w(who);
+    if (plan == nullptr || replicas == nullptr) return fail(ZERO_EINVAL, w + ": NULL plan or replicas");
+    if (rank < 0 || rank >= plan->n_ranks) return fail(ZERO_EINVAL, w + ": rank out of range");
+    if (n_replicas < 1 || n_replicas > ZERO_MAX_REPLICAS)
+        return fail(ZERO_EINVAL, w + ": n_replicas must be 1.." + std::to_string(ZERO_MAX_REPLICAS));
+    if (begin < 0 || count < 0 || begin > plan->padded || count > plan->padded - begin)
+        return fail(ZERO_EINVAL, w + ": window outside [0, P)");
+    zero_status st = check_first(first, plan->shard, who);
+    if (st != ZERO_OK) return st;
+    const int64_t shard_lo = static_cast<int64_t>(rank) * plan->shard, shard_hi = shard_lo + plan->shard;
+    const int64_t lo = std::max(begin, shard_lo), hi = std::min(begin + count, shard_hi);
+    if (lo >= hi) return ZERO_OK;
+    const int64_t at = lo - shard_lo, n = hi - lo, src_off = lo - begin;
+    if (at % kBlock != 0 || (hi != shard_hi && n % kBlock != 0))
+        return fail(ZERO_EINVAL, w + ": the window's part of the shard [" + std::to_string(at) + ", " +
+                                     std::to_string(at + n) + ") must start and end at multiples of " +
+                                     std::to_string(kBlock) + " elements or the shard's end");
+    a.g = replicas[0];
+    if (any_null(a)) return fail(ZERO_EINVAL, w + (replicas[0] ? ": NULL state array" : ": NULL replica"));
+    Replicas table{};
+    for (int32_t k = 0; k < n_replicas; ++k) {
+        if (replicas[k] == nullptr) return fail(ZERO_EINVAL, w + ": NULL replica");
+        table.p[k] = replicas[k];
+    }
+    a = Arrays{a.p + at, a.m + at, a.ms + at / kBlock, a.v + at, a.vs + at / kBlock, nullptr, a.o + at};
+    uint16_t* const grad_out = shard_grad != nullptr ? shard_grad + at : nullptr;
+    const size_t b = static_cast<size_t>(n), nb = static_cast<size_t>(zero::state8::blocks_of(n));
+    const zero::Span wr[] = {{a.p, 4 * b, "master"},          {a.m, b, "exp_avg"}, {a.ms, nb, "exp_avg_scale"},
+                             {a.v, b, "exp_avg_sq"}, {a.vs, nb, "exp_avg_sq_scale"}, {a.o, 2 * b, "param_out"},
+                             {grad_out, grad_out ? 2 * b : 0, "shard_grad"}};
+    zero::Span rd[ZERO_MAX_REPLICAS];
+    for (int32_t k = 0; k < n_replicas; ++k) rd[k] = {replicas[k] + src_off, 2 * b, "replica", k};
+    const std::string clash = zero::first_overlap(wr, 7, rd, n_replicas);
+    if (!clash.empty()) return fail(ZERO_EINVAL, w + ": " + clash);
+    bool vec = vector_ok(a) && (grad_out == nullptr || aligned(grad_out, 2 * kEpt));
+    for (int32_t k = 0; k < n_replicas; ++k) vec = vec && aligned(replicas[k] + src_off, 2 * kEpt);
+    dim3 grid;
+    st = grid_for(n, kChunk, &grid, who);
+    if (st != ZERO_OK) return st;
+    if (vec)
+        hipLaunchKernelGGL((reduce_adamw8_kernel<true, Step>), grid, dim3(kThreads), 0, stream, table, n_replicas,
+                           src_off, a, grad_out, n, first + at, step, clip_scale);
+    else
+        hipLaunchKernelGGL((reduce_adamw8_kernel<false, Step>), grid, dim3(kThreads), 0, stream, table, n_replicas,
+                           src_off, a, grad_out, n, first + at, step, clip_scale);
+    return zero::check_hip(hipGetLastError(), who);
+}
+
+}  // namespace
+
+extern "C" zero_status zero_reduce_adamw8_step(const zero_plan* plan, int32_t rank, const uint16_t* const* replicas,
+                                               int32_t n_replicas, int64_t begin, int64_t count, float* master,
+                                               uint8_t* exp_avg, uint8_t* exp_avg_scale, uint8_t* exp_avg_sq,
+                                               uint8_t* exp_avg_sq_scale, uint16_t* param_out, uint16_t* shard_grad,
+                                               int64_t first_element, int64_t step, double lr, double beta1,
+                                               double beta2, double eps, double weight_decay, uint64_t seed,
+                                               const float* clip_scale, hipStream_t stream) {
+    static const char* const who = "zero_reduce_adamw8_step";
+    zero::clear_error();
+    zero_status st = zero::adam::check_hyper(step, lr, beta1, beta2, eps, weight_decay, who);
+    if (st != ZERO_OK) return st;
+    CallStep s{};
+    st = zero::adam::step_scalars(step, lr, beta1, beta2, weight_decay, eps, &s.c, who);
+    if (st != ZERO_OK) return st;
+    s.key = zero::state8::step_key(seed, static_cast<uint64_t>(step));
+    return launch_reduce(plan, rank, replicas, n_replicas, begin, count,
+                         Arrays{master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, nullptr, param_out},
+                         shard_grad, first_element, s, clip_scale, stream, who);
+}
+
+extern "C" zero_status zero_reduce_adamw8_step_scheduled(
+    const zero_plan* plan, int32_t rank, const uint16_t* const* replicas, int32_t n_replicas, int64_t begin,
+    int64_t count, float* master, uint8_t* exp_avg, uint8_t* exp_avg_scale, uint8_t* exp_avg_sq,
+    uint8_t* exp_avg_sq_scale, uint16_t* param_out, uint16_t* shard_grad, int64_t first_element,
+    const zero_adamw_schedule* schedule, uint64_t seed, const float* clip_scale, hipStream_t stream) {
+    static const char* const who = "zero_reduce_adamw8_step_scheduled";
+    zero::clear_error();
+    if (schedule == nullptr) return zero::fail(ZERO_EINVAL, "zero_reduce_adamw8_step_scheduled: NULL schedule");
+    const zero_status st = zero::adam::check_schedule_device(schedule, who);
+    if (st != ZERO_OK) return st;
+    return launch_reduce(plan, rank, replicas, n_replicas, begin, count,
+                         Arrays{master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, nullptr, param_out},
+                         shard_grad, first_element, ScheduleStep{schedule->state, seed}, clip_scale, stream, who);
+}
+
+// ------------------------------------------------------------ conversions
+
+extern "C" zero_status zero_state8_quantize(const float* x, int64_t n, int32_t second_moment, uint8_t* codes,
+                                            uint8_t* scales, hipStream_t stream) {
+    using zero::fail;
+    static const char* const who = "zero_state8_quantize";
+    zero::clear_error();
+    if (n < 0) return fail(ZERO_EINVAL, "zero_state8_quantize: n < 0");
+    if (n == 0) return ZERO_OK;
+    if (!x || !codes || !scales) return fail(ZERO_EINVAL, "zero_state8_quantize: NULL array");
+    const size_t b = static_cast<size_t>(n);
+    const zero::Span wr[] = {{codes, b, "codes"}, {scales, static_cast<size_t>(zero::state8::blocks_of(n)), "scales"}};
+    const zero::Span rd[] = {{x, 4 * b, "x"}};
+    const std::string clash = zero::first_overlap(wr, 2, rd, 1);
+    if (!clash.empty()) return fail(ZERO_EINVAL, "zero_state8_quantize: " + clash);
+    dim3 grid;
+    const zero_status st = grid_for(n, int64_t(kThreads) * 4, &grid, who);
+    if (st != ZERO_OK) return st;
+    if (aligned(x, 16) && aligned(codes, 4))
+        hipLaunchKernelGGL(quantize_kernel<true>, grid, dim3(kThreads), 0, stream, x, codes, scales, n, second_moment);
+    else
+        hipLaunchKernelGGL(quantize_kernel<false>, grid, dim3(kThreads), 0, stream, x, codes, scales, n, second_moment);
+    return zero::check_hip(hipGetLastError(), who);
+}
+
+extern "C" zero_status zero_state8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, float* out,
+                                              hipStream_t stream) {
+    using zero::fail;
+    static const char* const who = "zero_state8_dequantize";
+    zero::clear_error();
+    if (n < 0) return fail(ZERO_EINVAL, "zero_state8_dequantize: n < 0");
+    if (n == 0) return ZERO_OK;
+    if (!codes || !scales || !out) return fail(ZERO_EINVAL, "zero_state8_dequantize: NULL array");
+    const size_t b = static_cast<size_t>(n);
+    const zero::Span wr[] = {{out, 4 * b, "out"}};
+    const zero::Span rd[] = {{codes, b, "codes"}, {scales, static_cast<size_t>(zero::state8::blocks_of(n)), "scales"}};
+    const std::string clash = zero::first_overlap(wr, 1, rd, 2);
+    if (!clash.empty()) return fail(ZERO_EINVAL, "zero_state8_dequantize: " + clash);
+    dim3 grid;
+    const zero_status st = grid_for(n, int64_t(kThreads) * 4, &grid, who);
+    if (st != ZERO_OK) return st;
+    if (aligned(out, 16) && aligned(codes, 4))
+        hipLaunchKernelGGL(dequantize_kernel<true>, grid, dim3(kThreads), 0, stream, codes, scales, out, n);
+    else
+        hipLaunchKernelGGL(dequantize_kernel<false>, grid, dim3(kThreads), 0, stream, codes, scales, out, n);
+    return zero::check_hip(hipGetLastError(), who);
+}

@@ -81,6 +81,14 @@ class RankStep:
                  replayed for successive steps. Flat or per-parameter device
                  state, and the one-pass update; not with offload (the host
                  update computes its own scalars).
+    state_bits   32 (fp32 moments) or 8: exp_avg and exp_avg_sq hold e4m3 codes
+                 (uint8) and exp_avg_scale and exp_avg_sq_scale a power-of-two
+                 byte per 128 elements (zero_shard_adamw8_step; 10 bytes a
+                 parameter with the gradient instead of 16). Every form of the step but
+                 offload; load_moments() and moments() convert from and to fp32.
+    seed         with state_bits=8, the run's seed of the stochastic rounding (the
+                 same on every rank: each rank draws the words of its own place in
+                 the flat buffer).
     """
 
     # Measured on MI355X, no clip: with 8 replicas per window the one pass takes
@@ -92,11 +100,17 @@ class RankStep:
     def __init__(self, plan: zb.Plan, rank: int, n_windows: int, hyper: Hyper, max_norm: float,
                  device: torch.device, gather: bool = True, offload: bool = False,
                  offload_chunk: int = 1 << 21, host_threads: int = 0, fuse: bool = True,
-                 per_param: bool = False, device_step: bool = False):
+                 per_param: bool = False, device_step: bool = False, state_bits: int = 32,
+                 seed: int = 0):
         if per_param and offload:
             raise ValueError("per-parameter state and ZeRO-Offload are separate layouts")
         if device_step and offload:
             raise ValueError("the device-counted step takes device state, not ZeRO-Offload's")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits is 8 or 32")
+        if state_bits == 8 and offload:
+            raise ValueError("ZeRO-Offload's host update takes fp32 moments")
+        self.state_bits, self.seed = state_bits, seed
         self.plan, self.rank, self.hyper, self.max_norm = plan, rank, hyper, max_norm
         self.device = device
         self.offload, self.host_threads = offload, host_threads
@@ -106,14 +120,20 @@ class RankStep:
         # moved STAGGER bytes past the previous end (the value measured best
         # on MI355X; see STAGGER).
         self.segments = plan.segments(rank) if per_param else []
+        moment = torch.float32 if state_bits == 32 else torch.uint8
+        self.exp_avg_scale = self.exp_avg_sq_scale = None
         if per_param:
             views, self.arena = _staggered_arena([(s, torch.int16), (s, torch.int16)], device)
             self.grad, own_param = views
             self.master = self.exp_avg = self.exp_avg_sq = None
             lens = [ln for (_, _, _, ln) in self.segments]
             self.master_tensors = [torch.zeros(n, dtype=torch.float32, device=device) for n in lens]
-            self.exp_avg_tensors = [torch.zeros(n, dtype=torch.float32, device=device) for n in lens]
-            self.exp_avg_sq_tensors = [torch.zeros(n, dtype=torch.float32, device=device) for n in lens]
+            self.exp_avg_tensors = [torch.zeros(n, dtype=moment, device=device) for n in lens]
+            self.exp_avg_sq_tensors = [torch.zeros(n, dtype=moment, device=device) for n in lens]
+            if state_bits == 8:
+                self.exp_avg_scale_tensors = [torch.zeros(zb.state8_blocks(n), dtype=torch.uint8, device=device)
+                                              for n in lens]
+                self.exp_avg_sq_scale_tensors = [torch.zeros_like(x) for x in self.exp_avg_scale_tensors]
         elif offload:
             views, self.arena = _staggered_arena([(s, torch.int16), (s, torch.int16)], device)
             self.grad, own_param = views
@@ -122,10 +142,13 @@ class RankStep:
             self.exp_avg_sq = torch.zeros(s, dtype=torch.float32)
             self.staging = torch.empty(4 * max(int(offload_chunk), 1), dtype=torch.int16).pin_memory()
         else:
-            views, self.arena = _staggered_arena(
-                [(s, torch.float32), (s, torch.float32), (s, torch.float32), (s, torch.int16),
-                 (s, torch.int16)], device)
-            self.master, self.exp_avg, self.exp_avg_sq, self.grad, own_param = views
+            specs = [(s, torch.float32), (s, moment), (s, moment), (s, torch.int16), (s, torch.int16)]
+            if state_bits == 8:
+                specs += [(zb.state8_blocks(s), torch.uint8)] * 2
+            views, self.arena = _staggered_arena(specs, device)
+            self.master, self.exp_avg, self.exp_avg_sq, self.grad, own_param = views[:5]
+            if state_bits == 8:
+                self.exp_avg_scale, self.exp_avg_sq_scale = views[5:]
         # per-rank partials [0, N_d) (own slot left 0), then one per own window
         self.partials = torch.zeros(nd + n_windows, dtype=torch.float64, device=device)
         self.scale = torch.ones(1, dtype=torch.float32, device=device)
@@ -207,6 +230,9 @@ class RankStep:
         lowers self.t.)"""
         self.t += 1
         clip = self.scale if self.max_norm > 0 else None
+        if self.state_bits == 8:
+            self._adamw8(clip, stream)
+            return
         if self.device_step:    # the step's scalars on the device, then the count moves on
             if self.per_param:
                 self._prepared("adamw", stream, lambda st: self._mt_table().prepare_step_scheduled(
@@ -230,6 +256,73 @@ class RankStep:
         self._prepared("adamw", stream, lambda st: zb.prepare_shard_adamw_step(
             self.master, self.exp_avg, self.exp_avg_sq, self.grad, self.param_shards[self.rank],
             clip_scale=clip, stream=st, **self.hyper.as_kwargs()))(self.t)
+
+    @property
+    def first_element(self) -> int:
+        """The number of this rank's first element in the 8-bit update's random words: its place in the
+        flat buffer (each rank's part rounded up to whole blocks of 128, and with per-parameter state up to
+        a block more per tensor)."""
+        blocks = zb.state8_blocks(self.plan.shard_numel) + (self.plan.num_tensors if self.per_param else 0)
+        return self.rank * blocks * zb.ZERO_STATE8_BLOCK
+
+    def _state8(self):
+        return (self.master, self.exp_avg, self.exp_avg_scale, self.exp_avg_sq, self.exp_avg_sq_scale)
+
+    def _adamw8(self, clip, stream) -> None:
+        """adamw() with the moments in 8 bits."""
+        own, hyper = self.param_shards[self.rank], self.hyper.as_kwargs()
+        if self.per_param:
+            if self.device_step:
+                self._prepared("adamw", stream, lambda st: self._mt8_table().prepare_step_scheduled(
+                    self.schedule, self.seed, clip, st))()
+            else:
+                self._prepared("adamw", stream, lambda st: self._mt8_table().prepare_step(
+                    seed=self.seed, clip_scale=clip, stream=st, **hyper))(self.t)
+        elif self.device_step:
+            self._prepared("adamw", stream, lambda st: zb.prepare_shard_adamw8_step_scheduled(
+                *self._state8(), self.grad, own, self.schedule, self.seed, self.first_element, clip, st))()
+        else:
+            self._prepared("adamw", stream, lambda st: zb.prepare_shard_adamw8_step(
+                *self._state8(), self.grad, own, seed=self.seed, first_element=self.first_element,
+                clip_scale=clip, stream=st, **hyper))(self.t)
+        if self.device_step:
+            self._prepared("advance", stream, lambda st: self.schedule.prepare_advance(clip, st))()
+
+    def _mt8_table(self) -> zb.MultiTensor8Table:
+        own = self.param_shards[self.rank]
+        sl = [slice(soff, soff + ln) for (_, _, soff, ln) in self.segments]
+        return zb.MultiTensor8Table(self.master_tensors, self.exp_avg_tensors, self.exp_avg_scale_tensors,
+                                    self.exp_avg_sq_tensors, self.exp_avg_sq_scale_tensors,
+                                    [self.grad[x] for x in sl], [own[x] for x in sl], self.first_element)
+
+    def _moment_sets(self):
+        """(codes, scales, whether the second moment) of every 8-bit moment array."""
+        if self.state_bits != 8:
+            raise ValueError("the moments are held in 8 bits only with state_bits=8")
+        if self.per_param:
+            return ([(c, s, False) for c, s in zip(self.exp_avg_tensors, self.exp_avg_scale_tensors)],
+                    [(c, s, True) for c, s in zip(self.exp_avg_sq_tensors, self.exp_avg_sq_scale_tensors)])
+        return ([(self.exp_avg, self.exp_avg_scale, False)], [(self.exp_avg_sq, self.exp_avg_sq_scale, True)])
+
+    def load_moments(self, exp_avg, exp_avg_sq, stream=None) -> None:
+        """Sets the 8-bit moments from fp32 ones, rounded to nearest (a fp32 checkpoint): a device tensor of
+        shard_numel elements each, or with per_param a list of one per segment."""
+        for given, held in zip((exp_avg, exp_avg_sq), self._moment_sets()):
+            given = list(given) if self.per_param else [given]
+            if len(given) != len(held) or any(x.numel() != c.numel() for x, (c, _, _) in zip(given, held)):
+                raise ValueError("the moments differ in length from the rank's")
+            for x, (codes, scales, second) in zip(given, held):
+                zb.zero_state8_quantize(x, codes, scales, second, stream)
+
+    def moments(self, stream=None):
+        """The 8-bit moments as new fp32 tensors (exp_avg, exp_avg_sq), laid out as load_moments takes them."""
+        out = []
+        for held in self._moment_sets():
+            values = [torch.empty(c.numel(), dtype=torch.float32, device=self.device) for c, _, _ in held]
+            for x, (codes, scales, _) in zip(values, held):
+                zb.zero_state8_dequantize(codes, scales, x, stream)
+            out.append(values if self.per_param else values[0])
+        return tuple(out)
 
     def _mt_table(self) -> zb.MultiTensorTable:
         """The per-parameter state's device table (the gradient and the parameter
@@ -259,10 +352,21 @@ class RankStep:
         spans = sorted((b, b + c) for b, c, _ in windows if c > 0)
         if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
             raise ValueError("windows overlap: the one-pass update needs disjoint windows")
+        if not self._whole_blocks(windows):
+            raise ValueError("a window cuts a block of 128 elements of the 8-bit moments")
         self.t += 1
         for w, (begin, count, reps) in enumerate(windows):
             sig = (begin, count, tuple(r.data_ptr() for r in reps))
-            if self.device_step:
+            if self.state_bits == 8 and self.device_step:
+                self._prepared(("reduce_update", w), stream, lambda st: zb.prepare_reduce_adamw8_step_scheduled(
+                    self.plan, self.rank, reps, begin, count, *self._state8(), self.param_shards[self.rank],
+                    self.schedule, self.seed, self.first_element, stream=st), sig)()
+            elif self.state_bits == 8:
+                self._prepared(("reduce_update", w), stream, lambda st: zb.prepare_reduce_adamw8_step(
+                    self.plan, self.rank, reps, begin, count, *self._state8(), self.param_shards[self.rank],
+                    seed=self.seed, first_element=self.first_element, stream=st,
+                    **self.hyper.as_kwargs()), sig)(self.t)
+            elif self.device_step:
                 self._prepared(("reduce_update", w), stream, lambda st: zb.prepare_reduce_adamw_step_scheduled(
                     self.plan, self.rank, reps, begin, count, self.master, self.exp_avg,
                     self.exp_avg_sq, self.param_shards[self.rank], self.schedule, stream=st), sig)()
@@ -281,12 +385,23 @@ class RankStep:
             self._prepared("gather", stream, lambda st: zb.CopyTable.gather(
                 self.plan, self.param_shards, self.tensors).prepare_run(st))()
 
+    def _whole_blocks(self, windows) -> bool:
+        """Whether every window's part of the shard holds whole blocks of the 8-bit moments."""
+        if self.state_bits == 32:
+            return True
+        s, block = self.plan.shard_numel, zb.ZERO_STATE8_BLOCK
+        for begin, count, _ in windows:
+            lo, hi = max(begin - self.rank * s, 0), min(begin + count - self.rank * s, s)
+            if lo < hi and (lo % block or (hi != s and hi % block)):
+                return False
+        return True
+
     def step(self, windows, stream=None) -> None:
         spans = sorted((b, b + c) for b, c, _ in windows if c > 0)
         disjoint = all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
         narrow = all(len(reps) <= self.FUSE_MAX_REPLICAS for _, _, reps in windows)
         if (self.fuse and self.max_norm <= 0 and not self.offload and not self.per_param
-                and disjoint and narrow):
+                and disjoint and narrow and self._whole_blocks(windows)):
             self.reduce_update(windows, stream)
         else:
             self.reduce(windows, stream)
