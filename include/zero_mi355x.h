@@ -491,13 +491,13 @@ zero_status zero_mt_table_adamw_step_scheduled(const zero_mt_table* table,
  * zeros, so cleared arrays are the moments of a new run.
  * Encoding a block. E = the biased exponent field of the largest magnitude;
  * byte = 255 if E = 255, else max(E - 7, 0) (that magnitude then lies in
- * [2^7, 2^8) in code units and never saturates). y = |x| * 2^(7 - byte),
- * rounded once to fp32 (inexact only for subnormal y); code =
- * (bits(y) + r) >> 20 with a 20-bit r, and the sign in bit 7. In the second
- * moment a positive x has a code of at least 1 (never rounded to zero).
- * r is a random word's 20 bits in the steps (stochastic rounding: a moment
- * that moves by less than a code's step still moves in the mean) and 0x7FFFF +
- * (bit 20 of y) in zero_state8_quantize (to nearest, ties to even).
+ * [2^7, 2^8) in code units and never saturates). In the steps, y = |x| *
+ * 2^(7 - byte) as fp32, bits below its least subnormal dropped (every other y
+ * is exact), and code = (bits(y) + r) >> 20 with 20 bits r of a random word,
+ * and the sign in bit 7: stochastic rounding, so that a moment that moves by
+ * less than a code's step still moves in the mean. zero_state8_quantize rounds
+ * to the nearest code, ties to even. In the second moment a positive x has a
+ * code of at least 1 (never rounded to zero).
  * Random words. Element e of step t of a run with `seed` has a 32-bit word
  * that depends on (seed, t, e) only, all arithmetic unsigned:
  *   z = seed + t * 0x6A09E667F3BCC909;  z = (z ^ z >> 32) * 0xBB67AE8584CAA73B;
@@ -512,8 +512,8 @@ zero_status zero_mt_table_adamw_step_scheduled(const zero_mt_table* table,
  *
  * The update per element is zero_shard_adamw_step's, in its order, on the
  * decoded m and v: the new fp32 m and v update p, and then are encoded.
- * Accesses: any pointer alignment; with master 16-byte, codes 8-byte, grad and
- * param_out 16-byte aligned the vector path runs, with identical results.
+ * Accesses: any pointer alignment; with master 16-byte, codes 4-byte, grad and
+ * param_out 8-byte aligned the vector path runs, with identical results.
  *
  * zero_shard_adamw8_step
  * master       device [n] fp32, updated in place.
@@ -550,7 +550,7 @@ zero_status zero_shard_adamw8_step_scheduled(float* master, uint8_t* exp_avg, ui
  * lengths of the tensors before it, each rounded up to a multiple of
  * ZERO_STATE8_BLOCK. Create, step, free, blocks and the caller's duties as
  * zero_mt_table_* (create: hipMalloc and a synchronous hipMemcpy on the
- * current device, once; 128 bytes per tensor and 4 per workgroup of 2,048
+ * current device, once; 128 bytes per tensor and 4 per workgroup of 1,024
  * elements); the results are zero_shard_adamw8_step's on each tensor.
  * Errors: as zero_mt_table_*, and zero_shard_adamw8_step's on first_element. */
 typedef struct zero_mt8_table zero_mt8_table;

@@ -73,26 +73,31 @@ def words(n: int, first: int, seed: int, step: int) -> np.ndarray:
 
 def encode(x: np.ndarray, second: bool, draw: np.ndarray = None):
     """(codes, scales) of fp32 x. draw: a 20-bit integer per element (stochastic
-    rounding: up where the dropped 20 bits and the draw carry), or None (to
-    nearest, ties to even)."""
+    rounding: up where the dropped 20 bits and the draw carry), or None (to the
+    nearest code, ties to even)."""
     n = len(x)
     rows = _rows(np.asarray(x, np.float32))
     big = np.abs(rows).max(axis=1)                       # NaN where the row has one
     field = (big.view(np.uint32) >> 23).astype(np.int64) & 255
     scales = np.where(field == 255, 255, np.maximum(field - 7, 0))
-    with np.errstate(invalid="ignore", under="ignore"):
-        # code units, as the fp32 whose exponent field is the code's: 2^-120 below them
-        y = np.ldexp(np.abs(rows).astype(np.float64), 7 - scales[:, None]).astype(np.float32)
-    bits = y.view(np.uint32).astype(np.int64)
+    finite = np.where((scales == 255)[:, None], np.float32(0), rows)
+    # |x| in units of 2^-149 beside a scale of 2^-120: subnormal (below 2^23) a count of
+    # them, its fraction dropped; normal the fp32 bits of the scaled value, exact.
+    y = np.ldexp(np.abs(finite).astype(np.float64), 7 - scales[:, None])
+    small = y < 2.0 ** -126
+    bits = np.where(small, np.floor(np.ldexp(np.where(small, y, 0), 149)).astype(np.int64),
+                    np.where(small, 0, y).astype(np.float32).view(np.uint32).astype(np.int64))
     kept, dropped = bits >> 20, bits & 0xFFFFF
     if draw is None:
-        up = (dropped > 0x80000) | ((dropped == 0x80000) & (kept & 1 == 1))
+        step = np.ldexp(1.0, np.maximum((bits >> 23), 1) - 127 - 3)      # between codes at y
+        kept = np.rint(y / step).astype(np.int64)                        # exact quotient, ties to even
+        kept = np.where(bits >> 23 > 0, kept + ((bits >> 23) - 1) * 8, kept)
+        code = kept
     else:
-        up = dropped + _rows(np.asarray(draw, np.int64)) >= 1 << 20
-    code = kept + up
+        code = kept + (dropped + _rows(np.asarray(draw, np.int64)) >= 1 << 20)
     if second:
         code = np.where((code == 0) & (rows > 0), 1, code)
-    code |= np.signbit(rows).astype(np.int64) << 7
+    code = code | (np.signbit(rows).astype(np.int64) << 7)
     code[scales == 255] = 0
     return code.reshape(-1)[:n].astype(np.uint8), scales.astype(np.uint8)
 

@@ -9,10 +9,19 @@
 //
 // Per element: the moments are decoded, updated with the 32-bit AdamW's fp32
 // operations in its order (the update uses the fp32 m and v, before they are
-// rounded), and encoded with the block's new scale. A block is held by 16 or
-// 32 neighbouring lanes of one wave, so its maximum is a few cross-lane
-// operations and every array is read and written once: 16 bytes an element and
-// 4 per block of 128.
+// rounded), and encoded with the block's new scale. A block is held by 32
+// neighbouring lanes of one wave, so its maximum is a few cross-lane operations
+// and every array is read and written once: 16 bytes an element and 4 per block
+// of 128.
+//
+// Bound: HBM. With the moments at a byte, the bytes fall from 28 to 16 while the
+// arithmetic grows, to about 90 vector issue slots an element (45 of them the
+// IEEE square root and two divisions), against the 100 that fit beside the
+// memory time; the conversions in one instruction each are what keeps the sum
+// under it. Four elements a lane: with 8 a lane's two 16-byte stores of the
+// master leave half-written lines behind each other and the write-through stores
+// fell to 3.1 TB/s (662 us at 125 M elements); with 2 the random words, shared
+// by 8 elements, are computed four times over (about 400 us).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -40,10 +49,7 @@ using zero::state8::kBlock;
 
 constexpr int kThreads = 256;
 
-#ifndef ZERO_ADAMW8_EPT
-#define ZERO_ADAMW8_EPT 8
-#endif
-constexpr int kEpt = ZERO_ADAMW8_EPT;          // consecutive elements a lane
+constexpr int kEpt = zero::state8::kLaneElems;
 constexpr int64_t kChunk = int64_t(kThreads) * kEpt;
 static_assert(kChunk % kBlock == 0, "whole blocks a workgroup");
 
@@ -79,12 +85,12 @@ __device__ __forceinline__ float read_clip(const float* clip_scale) {
     return clip_scale != nullptr ? *clip_scale : 1.0f;
 }
 
-// What a lane holds of its kEpt elements.
+// What a lane holds of its elements: those at or past n are zeros.
 struct Lane {
-    float p[kEpt];
-    uint32_t m[kEpt / 4], v[kEpt / 4];     // codes, four a word
+    float p[kEpt] = {};
+    uint32_t m = 0, v = 0;                 // codes, the first lowest
     uint32_t ms = 0, vs = 0;
-    int live = 0;                          // of the kEpt elements, those below n
+    int live = 0;                          // elements below n
 };
 
 // VEC: every array allows accesses of kEpt elements. Lanes with fewer than
@@ -93,40 +99,25 @@ template <bool VEC>
 __device__ __forceinline__ void load_state(Lane& l, const Arrays& a, int64_t n, int64_t i) {
     const int64_t left = n - i;
     l.live = left <= 0 ? 0 : (left < kEpt ? static_cast<int>(left) : kEpt);
-#pragma unroll
-    for (int k = 0; k < kEpt; ++k) l.p[k] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kEpt / 4; ++w) l.m[w] = l.v[w] = 0;
-    if (l.live == 0) return;
-    l.ms = a.ms[i / kBlock];
-    l.vs = a.vs[i / kBlock];
     if (VEC && l.live == kEpt) {
+        const f32x4 x = zero::dev::ld_stream(reinterpret_cast<const f32x4*>(a.p + i));
+        l.m = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(a.m + i));
+        l.v = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(a.v + i));
 #pragma unroll
-        for (int w = 0; w < kEpt / 4; ++w) {
-            const f32x4 x = zero::dev::ld_stream(reinterpret_cast<const f32x4*>(a.p + i) + w);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) l.p[4 * w + k] = x[k];
-        }
-        if (kEpt == 8) {
-            const u32x2 m = zero::dev::ld_stream(reinterpret_cast<const u32x2*>(a.m + i));
-            const u32x2 v = zero::dev::ld_stream(reinterpret_cast<const u32x2*>(a.v + i));
-            l.m[0] = m[0];
-            l.v[0] = v[0];
-            l.m[kEpt / 4 - 1] = m[1];
-            l.v[kEpt / 4 - 1] = v[1];
-        } else {
-            l.m[0] = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(a.m + i));
-            l.v[0] = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(a.v + i));
-        }
+        for (int k = 0; k < kEpt; ++k) l.p[k] = x[k];
     } else {
 #pragma unroll
         for (int k = 0; k < kEpt; ++k) {
             if (k < l.live) {
                 l.p[k] = a.p[i + k];
-                l.m[k / 4] |= static_cast<uint32_t>(a.m[i + k]) << (8 * (k % 4));
-                l.v[k / 4] |= static_cast<uint32_t>(a.v[i + k]) << (8 * (k % 4));
+                l.m |= static_cast<uint32_t>(a.m[i + k]) << (8 * k);
+                l.v |= static_cast<uint32_t>(a.v[i + k]) << (8 * k);
             }
         }
+    }
+    if (l.live > 0) {
+        l.ms = a.ms[i / kBlock];
+        l.vs = a.vs[i / kBlock];
     }
 }
 
@@ -135,14 +126,11 @@ __device__ __forceinline__ void load_grad(float (&g)[kEpt], const uint16_t* grad
 #pragma unroll
     for (int k = 0; k < kEpt; ++k) g[k] = 0.0f;
     if (VEC && live == kEpt) {
-#pragma unroll
-        for (int w = 0; w < kEpt / 4; ++w) {
-            const u32x2 x = zero::dev::ld_stream(reinterpret_cast<const u32x2*>(grad + i) + w);
-            g[4 * w] = zero::dev::lo_bf16(x[0]);
-            g[4 * w + 1] = zero::dev::hi_bf16(x[0]);
-            g[4 * w + 2] = zero::dev::lo_bf16(x[1]);
-            g[4 * w + 3] = zero::dev::hi_bf16(x[1]);
-        }
+        const u32x2 x = zero::dev::ld_stream(reinterpret_cast<const u32x2*>(grad + i));
+        g[0] = zero::dev::lo_bf16(x[0]);
+        g[1] = zero::dev::hi_bf16(x[0]);
+        g[2] = zero::dev::lo_bf16(x[1]);
+        g[3] = zero::dev::hi_bf16(x[1]);
     } else {
 #pragma unroll
         for (int k = 0; k < kEpt; ++k)
@@ -151,75 +139,46 @@ __device__ __forceinline__ void load_grad(float (&g)[kEpt], const uint16_t* grad
 }
 
 // Updates a lane's elements from their clipped gradients and writes them back.
-// Every lane of the wave calls it (the block maxima cross lanes).
+// Every lane of the wave calls it (the block maxima cross lanes); a lane past n
+// brings zeros, which change no maximum.
 template <bool VEC>
 __device__ __forceinline__ void update_and_store(Lane& l, const float (&g)[kEpt], const Arrays& a, int64_t i,
                                                  int64_t first, const AdamScalars& c, Key key) {
     float m[kEpt], v[kEpt];
+    zero::state8::decode4(l.m, l.ms, m);
+    zero::state8::decode4(l.v, l.vs, v);
 #pragma unroll
-    for (int w = 0; w < kEpt / 4; ++w) {
-        zero::state8::decode4(l.m[w], l.ms, m + 4 * w);
-        zero::state8::decode4(l.v[w], l.vs, v + 4 * w);
-    }
-    uint32_t mm = 0, vm = 0;
-#pragma unroll
-    for (int k = 0; k < kEpt; ++k) {
-        adam_elem(l.p[k], m[k], v[k], g[k], c);
-        if (k < l.live) {
-            mm = zero::state8::umax(mm, zero::state8::magnitude(m[k]));
-            vm = zero::state8::umax(vm, zero::state8::magnitude(v[k]));
-        }
-    }
-    const uint32_t ms = zero::state8::scale_byte(zero::state8::block_max<kEpt>(mm));
-    const uint32_t vs = zero::state8::scale_byte(zero::state8::block_max<kEpt>(vm));
+    for (int k = 0; k < kEpt; ++k) adam_elem(l.p[k], m[k], v[k], g[k], c);
+    const uint32_t ms = zero::state8::scale_byte(zero::state8::block_max(zero::state8::max_bits4(m)));
+    const uint32_t vs = zero::state8::scale_byte(zero::state8::block_max(zero::state8::max_bits4(v)));
     if (l.live == 0) return;
     const uint64_t e = static_cast<uint64_t>(first + i);
     const Words words = zero::state8::group_words(e >> 3, key);
-    uint32_t r = words.a + (static_cast<uint32_t>(e) & 7u) * words.b;
-    uint32_t mc[kEpt], vc[kEpt], mw[kEpt / 4], vw[kEpt / 4];
+    uint32_t rm[kEpt], rv[kEpt];
+    rm[0] = words.a + (static_cast<uint32_t>(e) & 7u) * words.b;
 #pragma unroll
-    for (int k = 0; k < kEpt; ++k) {
-        mc[k] = zero::state8::first_code(m[k], ms, r);
-        vc[k] = zero::state8::second_code(v[k], vs, r);
-        r += words.b;
-    }
+    for (int k = 1; k < kEpt; ++k) rm[k] = rm[k - 1] + words.b;
 #pragma unroll
-    for (int w = 0; w < kEpt / 4; ++w) {
-        mw[w] = zero::state8::pack4(mc[4 * w], mc[4 * w + 1], mc[4 * w + 2], mc[4 * w + 3]);
-        vw[w] = zero::state8::pack4(vc[4 * w], vc[4 * w + 1], vc[4 * w + 2], vc[4 * w + 3]);
-        if (ms == 255u) mw[w] = 0;
-        if (vs == 255u) vw[w] = 0;
-    }
+    for (int k = 0; k < kEpt; ++k) rv[k] = rm[k] << 12;      // the word's low 20 bits, as a seed's high ones
+    const uint32_t mw = zero::state8::encode4(m, ms, rm);
+    const uint32_t vw = zero::state8::positive4(zero::state8::encode4(v, vs, rv), v, vs);
     if (i % kBlock == 0) {                 // the block's first lane
         a.ms[i / kBlock] = static_cast<uint8_t>(ms);
         a.vs[i / kBlock] = static_cast<uint8_t>(vs);
     }
     if (VEC && l.live == kEpt) {
-#pragma unroll
-        for (int w = 0; w < kEpt / 4; ++w) {
-            const f32x4 x = {l.p[4 * w], l.p[4 * w + 1], l.p[4 * w + 2], l.p[4 * w + 3]};
-            zero::dev::st_stream(reinterpret_cast<f32x4*>(a.p + i) + w, x);
-        }
-        if (kEpt == 8) {
-            zero::dev::st_stream(reinterpret_cast<u32x2*>(a.m + i), u32x2{mw[0], mw[kEpt / 4 - 1]});
-            zero::dev::st_stream(reinterpret_cast<u32x2*>(a.v + i), u32x2{vw[0], vw[kEpt / 4 - 1]});
-            const u32x4 o = {zero::dev::pack_bf16(l.p[0], l.p[1]), zero::dev::pack_bf16(l.p[2], l.p[3]),
-                             zero::dev::pack_bf16(l.p[kEpt - 4], l.p[kEpt - 3]),
-                             zero::dev::pack_bf16(l.p[kEpt - 2], l.p[kEpt - 1])};
-            zero::dev::st_stream(reinterpret_cast<u32x4*>(a.o + i), o);
-        } else {
-            zero::dev::st_stream(reinterpret_cast<uint32_t*>(a.m + i), mw[0]);
-            zero::dev::st_stream(reinterpret_cast<uint32_t*>(a.v + i), vw[0]);
-            const u32x2 o = {zero::dev::pack_bf16(l.p[0], l.p[1]), zero::dev::pack_bf16(l.p[2], l.p[3])};
-            zero::dev::st_stream(reinterpret_cast<u32x2*>(a.o + i), o);
-        }
+        zero::dev::st_stream(reinterpret_cast<f32x4*>(a.p + i), f32x4{l.p[0], l.p[1], l.p[2], l.p[3]});
+        zero::dev::st_stream(reinterpret_cast<uint32_t*>(a.m + i), mw);
+        zero::dev::st_stream(reinterpret_cast<uint32_t*>(a.v + i), vw);
+        zero::dev::st_stream(reinterpret_cast<u32x2*>(a.o + i),
+                             u32x2{zero::dev::pack_bf16(l.p[0], l.p[1]), zero::dev::pack_bf16(l.p[2], l.p[3])});
     } else {
 #pragma unroll
         for (int k = 0; k < kEpt; ++k) {
             if (k < l.live) {
                 a.p[i + k] = l.p[k];
-                a.m[i + k] = static_cast<uint8_t>(mw[k / 4] >> (8 * (k % 4)));
-                a.v[i + k] = static_cast<uint8_t>(vw[k / 4] >> (8 * (k % 4)));
+                a.m[i + k] = static_cast<uint8_t>(mw >> (8 * k));
+                a.v[i + k] = static_cast<uint8_t>(vw >> (8 * k));
                 a.o[i + k] = static_cast<uint16_t>(zero::dev::f32_to_bf16(l.p[k]));
             }
         }
@@ -309,13 +268,11 @@ __device__ __forceinline__ void mean_grad(float (&g)[kEpt], const Replicas& reps
     for (int k = 0; k < kEpt; ++k) acc[k] = 0.0f;
     const float count = static_cast<float>(n_rep);
     if (VEC && live == kEpt) {
-        typedef typename std::conditional<kEpt == 8, u32x4, u32x2>::type V;
-        zero::dev::for_replicas<kReplicaBatch, V>(reps.p, n_rep, src_off, i / kEpt, [&](V x) {
-#pragma unroll
-            for (int w = 0; w < kEpt / 2; ++w) {
-                acc[2 * w] = acc[2 * w] + zero::dev::lo_bf16(x[w]);
-                acc[2 * w + 1] = acc[2 * w + 1] + zero::dev::hi_bf16(x[w]);
-            }
+        zero::dev::for_replicas<kReplicaBatch, u32x2>(reps.p, n_rep, src_off, i / kEpt, [&](u32x2 x) {
+            acc[0] = acc[0] + zero::dev::lo_bf16(x[0]);
+            acc[1] = acc[1] + zero::dev::hi_bf16(x[0]);
+            acc[2] = acc[2] + zero::dev::lo_bf16(x[1]);
+            acc[3] = acc[3] + zero::dev::hi_bf16(x[1]);
         });
     } else if (live > 0) {
         for (int r = 0; r < n_rep; ++r) {
@@ -342,11 +299,8 @@ __global__ __launch_bounds__(kThreads) void reduce_adamw8_kernel(Replicas reps, 
     mean_grad<VEC>(g, reps, n_rep, src_off, l.live, i);
     if (grad_out != nullptr) {
         if (VEC && l.live == kEpt) {
-#pragma unroll
-            for (int w = 0; w < kEpt / 4; ++w)
-                zero::dev::st_stream(reinterpret_cast<u32x2*>(grad_out + i) + w,
-                                     u32x2{zero::dev::pack_bf16(g[4 * w], g[4 * w + 1]),
-                                           zero::dev::pack_bf16(g[4 * w + 2], g[4 * w + 3])});
+            zero::dev::st_stream(reinterpret_cast<u32x2*>(grad_out + i),
+                                 u32x2{zero::dev::pack_bf16(g[0], g[1]), zero::dev::pack_bf16(g[2], g[3])});
         } else {
 #pragma unroll
             for (int k = 0; k < kEpt; ++k)
@@ -366,7 +320,7 @@ __global__ __launch_bounds__(kThreads) void reduce_adamw8_kernel(Replicas reps, 
 template <bool VEC>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const float* __restrict__ x, uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales, int64_t n, int second) {
-    const int64_t i = (workgroup() * kThreads + threadIdx.x) * 4;
+    const int64_t i = (workgroup() * kThreads + threadIdx.x) * kEpt;
     const int64_t left = n - i;
     const int live = left <= 0 ? 0 : (left < 4 ? static_cast<int>(left) : 4);
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -379,16 +333,10 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const float* __restr
         for (int k = 0; k < 4; ++k)
             if (k < live) v[k] = x[i + k];
     }
-    uint32_t big = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) big = zero::state8::umax(big, zero::state8::magnitude(v[k]));
-    const uint32_t byte = zero::state8::scale_byte(zero::state8::block_max<4>(big));
+    const uint32_t byte = zero::state8::scale_byte(zero::state8::block_max(zero::state8::max_bits4(v)));
     if (live == 0) return;
-    uint32_t c[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) c[k] = zero::state8::nearest_code(v[k], byte, second != 0);
-    uint32_t w = zero::state8::pack4(c[0], c[1], c[2], c[3]);
-    if (byte == 255u) w = 0;
+    uint32_t w = zero::state8::nearest4(v, byte);
+    if (second) w = zero::state8::positive4(w, v, byte);
     if (i % kBlock == 0) scales[i / kBlock] = static_cast<uint8_t>(byte);
     if (VEC && live == 4) {
         zero::dev::st_stream(reinterpret_cast<uint32_t*>(codes + i), w);
@@ -403,7 +351,7 @@ template <bool VEC>
 __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __restrict__ codes,
                                                               const uint8_t* __restrict__ scales,
                                                               float* __restrict__ out, int64_t n) {
-    const int64_t i = (workgroup() * kThreads + threadIdx.x) * 4;
+    const int64_t i = (workgroup() * kThreads + threadIdx.x) * kEpt;
     const int64_t left = n - i;
     const int live = left <= 0 ? 0 : (left < 4 ? static_cast<int>(left) : 4);
     if (live == 0) return;
@@ -789,7 +737,7 @@ extern "C" zero_status zero_state8_quantize(const float* x, int64_t n, int32_t s
     const std::string clash = zero::first_overlap(wr, 2, rd, 1);
     if (!clash.empty()) return fail(ZERO_EINVAL, "zero_state8_quantize: " + clash);
     dim3 grid;
-    const zero_status st = grid_for(n, int64_t(kThreads) * 4, &grid, who);
+    const zero_status st = grid_for(n, kChunk, &grid, who);
     if (st != ZERO_OK) return st;
     if (aligned(x, 16) && aligned(codes, 4))
         hipLaunchKernelGGL(quantize_kernel<true>, grid, dim3(kThreads), 0, stream, x, codes, scales, n, second_moment);
@@ -812,7 +760,7 @@ extern "C" zero_status zero_state8_dequantize(const uint8_t* codes, const uint8_
     const std::string clash = zero::first_overlap(wr, 1, rd, 2);
     if (!clash.empty()) return fail(ZERO_EINVAL, "zero_state8_dequantize: " + clash);
     dim3 grid;
-    const zero_status st = grid_for(n, int64_t(kThreads) * 4, &grid, who);
+    const zero_status st = grid_for(n, kChunk, &grid, who);
     if (st != ZERO_OK) return st;
     if (aligned(out, 16) && aligned(codes, 4))
         hipLaunchKernelGGL(dequantize_kernel<true>, grid, dim3(kThreads), 0, stream, codes, scales, out, n);

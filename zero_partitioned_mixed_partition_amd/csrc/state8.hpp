@@ -16,10 +16,12 @@
 //
 // Code. e4m3 (4 exponent bits, 3 mantissa bits, gradual underflow) is fp32
 // with the low exponents 0..15 and the mantissa cut to 3 bits: with |x| scaled
-// to y = |x| * 2^(7 - byte), whose exponent field is then e4m3's, the code is
-// (bits(y) + r) >> 20 for a 20-bit r, subnormal codes included (y is then a
-// subnormal fp32). r uniform gives stochastic rounding, E[value] = x exactly
-// where y is normal; r = 0x7FFFF + (bit 20) gives round to nearest even.
+// to y = |x| * 2^(7 - byte), whose exponent field is then e4m3's (bits below
+// fp32's least subnormal dropped), the code is (bits(y) + r) >> 20 for a 20-bit
+// r, subnormal codes included. r uniform is stochastic rounding. gfx950
+// converts so in one instruction (scale, add the seed's high 20 bits, cut,
+// place the byte), to nearest even in another, and back in a third; the GPU
+// tests compare all three with this formula over every code and scale.
 //
 // Why stochastic. With beta2 = 0.999 the second moment moves by about 0.1% a
 // step, against code steps of 6-12%: rounding to nearest would return the old
@@ -92,24 +94,28 @@ __device__ __forceinline__ uint32_t dpp(uint32_t x) {
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// The largest x over the 128 / E lanes that hold one block (E elements a lane,
-// the wave's lanes in order), in every one of them. All lanes take part. Rows
-// of 16 lanes by rotations within the row; 32 lanes by one swap of row pairs.
-template <int E>
+constexpr int kLaneElems = 4;      // consecutive elements a lane holds in every kernel here
+
+// The largest x over the 32 lanes that hold one block (4 elements a lane, the
+// wave's lanes in order), in every one of them. All lanes take part. Rows of 16
+// lanes by rotations within the row, then one swap of neighbouring rows.
 __device__ __forceinline__ uint32_t block_max(uint32_t x) {
-    static_assert(E == 4 || E == 8, "16 or 32 lanes a block");
     x = umax(x, dpp<0x128>(x));     // row_ror:8
     x = umax(x, dpp<0x124>(x));     // row_ror:4
     x = umax(x, dpp<0x122>(x));     // row_ror:2
     x = umax(x, dpp<0x121>(x));     // row_ror:1
-    if (E == 4) {
-        const auto s = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-        x = umax(s[0], s[1]);
-    }
-    return x;
+    const auto s = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return umax(s[0], s[1]);
 }
 
-__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+// The bits of the largest magnitude of four values; a NaN wins (the IEEE
+// maximum, one v_maximum3 per two values).
+__device__ __forceinline__ uint32_t max_bits4(const float (&x)[4]) {
+    float m = __builtin_elementwise_maximum(__builtin_fabsf(x[0]), __builtin_fabsf(x[1]));
+    m = __builtin_elementwise_maximum(m, __builtin_fabsf(x[2]));
+    m = __builtin_elementwise_maximum(m, __builtin_fabsf(x[3]));
+    return __float_as_uint(m) & 0x7FFFFFFFu;
+}
 
 // The scale byte of a block whose largest magnitude has these bits.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t max_bits) {
@@ -119,54 +125,53 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t max_bits) {
 
 // ------------------------------------------------------------ codes
 
+// The scale as the conversions take it: the power of two in an fp32's exponent
+// field (byte 0 stands for 2^-127 there, byte 255 for NaN).
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
 // Four codes as fp32 (in a block with this scale byte).
-__device__ __forceinline__ void decode4(uint32_t word, uint32_t byte, float* out) {
-    word = byte == 255u ? 0x7F7F7F7Fu : word;          // e4m3's NaN
-    const int e = static_cast<int>(byte) - 127;
-    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(word), false);
-    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(word), true);
-    out[0] = ldexpf(lo[0], e);
-    out[1] = ldexpf(lo[1], e);
-    out[2] = ldexpf(hi[0], e);
-    out[3] = ldexpf(hi[1], e);
+__device__ __forceinline__ void decode4(uint32_t word, uint32_t byte, float (&out)[4]) {
+    const float s = scale_of(byte);
+    const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(word, s, false);
+    const auto hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(word, s, true);
+    out[0] = lo[0];
+    out[1] = lo[1];
+    out[2] = hi[0];
+    out[3] = hi[1];
 }
 
-// |x| in code units, as the fp32 whose exponent field is e4m3's.
-__device__ __forceinline__ uint32_t code_bits(float x, uint32_t byte) {
-    return magnitude(ldexpf(x, 7 - static_cast<int>(byte)));
+// Four elements stochastically rounded with the high 20 bits of r[0..3], as one
+// word; zeros in a block that is not finite.
+__device__ __forceinline__ uint32_t encode4(const float (&x)[4], uint32_t byte, const uint32_t (&r)[4]) {
+    const float s = scale_of(byte);
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[0], r[0], s, 0);
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[1], r[1], s, 1);
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[2], r[2], s, 2);
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[3], r[3], s, 3);
+    return byte == 255u ? 0u : w;
 }
 
-// A code in the top byte of a word: t holds the rounded bits(y), whose bit 27
-// and above are clear.
-__device__ __forceinline__ uint32_t top_code(uint32_t t, float x) {
-    return ((t << 4) & 0x7FFFFFFFu) | (__float_as_uint(x) & 0x80000000u);
+// The same, rounded to nearest even.
+__device__ __forceinline__ uint32_t nearest4(const float (&x)[4], uint32_t byte) {
+    typedef short s16x2 __attribute__((ext_vector_type(2)));
+    const float s = scale_of(byte);
+    s16x2 w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[0], x[1], s, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[2], x[3], s, true);
+    return byte == 255u ? 0u : __builtin_bit_cast(uint32_t, w);
 }
 
-// The top bytes of four words as one word, the first lowest.
-__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0C0C0703u);
-    const uint32_t hi = __builtin_amdgcn_perm(d, c, 0x07030C0Cu);
-    return lo | hi;
-}
-
-// Element x of the first moment, stochastically rounded with word r.
-__device__ __forceinline__ uint32_t first_code(float x, uint32_t byte, uint32_t r) {
-    return top_code(code_bits(x, byte) + (r >> 12), x);
-}
-
-// Element x of the second moment: at least code 1 where x is positive.
-__device__ __forceinline__ uint32_t second_code(float x, uint32_t byte, uint32_t r) {
-    uint32_t t = code_bits(x, byte) + (r & 0xFFFFFu);
-    t = umax(t, x > 0.0f ? 1u << 20 : 0u);
-    return top_code(t, x);
-}
-
-// Element x rounded to nearest even.
-__device__ __forceinline__ uint32_t nearest_code(float x, uint32_t byte, bool second) {
-    const uint32_t y = code_bits(x, byte);
-    uint32_t t = y + 0x7FFFFu + ((y >> 20) & 1u);
-    if (second) t = umax(t, x > 0.0f ? 1u << 20 : 0u);
-    return top_code(t, x);
+// Raises the zero codes of positive elements to 1 (second moments), in a block
+// with a finite scale. Zero codes are rare (the element is below 2^-16 of its
+// block's largest, or zero), so one test of the word decides for the four.
+__device__ __forceinline__ uint32_t positive4(uint32_t w, const float (&x)[4], uint32_t byte) {
+    if (((w - 0x01010101u) & ~w & 0x80808080u) != 0u && byte != 255u) {      // a zero byte
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (((w >> (8 * k)) & 0xFFu) == 0u && x[k] > 0.0f) w |= 1u << (8 * k);
+    }
+    return w;
 }
 
 }  // namespace state8
