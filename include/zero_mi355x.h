@@ -486,7 +486,9 @@ zero_status zero_mt_table_adamw_step_scheduled(const zero_mt_table* table,
  *
  * Format. A code is an OCP 8-bit float e4m3 (bias 7, largest 448, no
  * infinity), a scale byte an e8m0 power of two: value = e4m3(code) *
- * 2^(byte - 127). Byte 255 stands for a block that held an infinity or NaN:
+ * 2^(byte - 127): 3 bits of mantissa down to 2^-13 of the block's largest, the
+ * least code at 2^-17 to 2^-16 of it. Byte 255 stands for a block that held an
+ * infinity or NaN:
  * it reads as NaN throughout (its codes are written as 0). All-zero bytes are
  * zeros, so cleared arrays are the moments of a new run.
  * Encoding a block. E = the biased exponent field of the largest magnitude;
@@ -550,7 +552,7 @@ zero_status zero_shard_adamw8_step_scheduled(float* master, uint8_t* exp_avg, ui
  * lengths of the tensors before it, each rounded up to a multiple of
  * ZERO_STATE8_BLOCK. Create, step, free, blocks and the caller's duties as
  * zero_mt_table_* (create: hipMalloc and a synchronous hipMemcpy on the
- * current device, once; 128 bytes per tensor and 4 per workgroup of 1,024
+ * current device, once; 128 bytes per tensor and 4 per workgroup of 512
  * elements); the results are zero_shard_adamw8_step's on each tensor.
  * Errors: as zero_mt_table_*, and zero_shard_adamw8_step's on first_element. */
 typedef struct zero_mt8_table zero_mt8_table;

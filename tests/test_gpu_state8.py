@@ -231,7 +231,7 @@ def _ragged(zm, seed, misaligned):
 def test_table_step_matches_oracle_per_tensor(zm, misaligned):
     numels, states, grads, lists = _ragged(zm, 30, misaligned)
     table = zm.MultiTensor8Table(*lists, first_element=256)
-    assert table.blocks == sum(-(-n // 1024) for n in numels)
+    assert table.blocks == sum(-(-n // 512) for n in numels)
     clip = torch.full((1,), 0.25, device=dev())
     for t in (1, 2):
         table.step(t, seed=11, clip_scale=clip, **HP)

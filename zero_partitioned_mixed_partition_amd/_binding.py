@@ -939,15 +939,16 @@ def state8_blocks(n: int) -> int:
     return -(-n // ZERO_STATE8_BLOCK)
 
 
-_STATE8 = (("master", 4), ("exp_avg", 1), ("exp_avg_scale", 1), ("exp_avg_sq", 1), ("exp_avg_sq_scale", 1))
+_STATE8 = (("master", 4), ("exp_avg", 1), ("exp_avg_scale", 1), ("exp_avg_sq", 1), ("exp_avg_sq_scale", 1),
+           ("grad", 2), ("param_out", 2))
 
 
-def _state8_ptrs(n: int, arrays, grad, param_out) -> List[int]:
-    """The seven pointers of an 8-bit update over n elements (grad None where the call takes none)."""
-    named = list(zip(arrays, _STATE8)) + [(grad, ("grad", 2)), (param_out, ("param_out", 2))]
-    for t, (what, _) in named:
-        _need(t, state8_blocks(n) if what.endswith("_scale") else n, what)
-    return [_ptr(t, size, what) for t, (what, size) in named]
+def _state8_ptrs(n: int, tensors) -> List[int]:
+    """The pointers of an 8-bit update's seven tensors over n elements (None where the call takes none)."""
+    blocks = state8_blocks(n)
+    for t, (what, _) in zip(tensors, _STATE8):
+        _need(t, blocks if what.endswith("scale") else n, what)
+    return [_ptr(t, size, what) for t, (what, size) in zip(tensors, _STATE8)]
 
 
 def _seed(seed: int) -> int:
@@ -962,13 +963,13 @@ def prepare_shard_adamw8_step(master, exp_avg, exp_avg_scale, exp_avg_sq, exp_av
                               stream=None) -> Prepared:
     """zero_shard_adamw8_step with its arguments marshalled once; call the result with the step number."""
     n = master.numel() if n is None else n
-    arrays = (master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale)
+    tensors = (master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad, param_out)
     _need(clip_scale, 1, "clip_scale")
-    p = Prepared(_adamw8, _state8_ptrs(n, arrays, grad, param_out) +
+    p = Prepared(_adamw8, _state8_ptrs(n, tensors) +
                  [n, first_element, 1, lr, beta1, beta2, eps, weight_decay, _seed(seed),
                   _ptr(clip_scale, 4, "clip_scale"), _stream(stream, master)],
                  "zero_shard_adamw8_step", step_index=9)
-    p._keep = (arrays, grad, param_out, clip_scale)
+    p._keep = (tensors, clip_scale)
     return p
 
 
@@ -979,8 +980,11 @@ def zero_shard_adamw8_step(master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_s
     """zero_shard_adamw_step with both moments in 8 bits: exp_avg and exp_avg_sq hold one-byte e4m3 codes
     (torch.uint8 or torch.float8_e4m3fn), the *_scale tensors a power-of-two byte per 128 elements. `seed`
     is the run's, `first_element` the number of element 0 in its random words (a multiple of 128)."""
-    prepare_shard_adamw8_step(master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad, param_out, lr,
-                              beta1, beta2, eps, weight_decay, seed, first_element, clip_scale, n, stream)(step)
+    n = master.numel() if n is None else n
+    _need(clip_scale, 1, "clip_scale")
+    _check(_adamw8(*_state8_ptrs(n, (master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad, param_out)),
+                   n, first_element, step, lr, beta1, beta2, eps, weight_decay, _seed(seed),
+                   _ptr(clip_scale, 4, "clip_scale"), _stream(stream, master)), "zero_shard_adamw8_step")
 
 
 def prepare_shard_adamw8_step_scheduled(master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad,
@@ -988,12 +992,12 @@ def prepare_shard_adamw8_step_scheduled(master, exp_avg, exp_avg_scale, exp_avg_
                                         first_element: int = 0, clip_scale=None, stream=None) -> Prepared:
     """zero_shard_adamw8_step_scheduled with its arguments marshalled once."""
     n = master.numel()
-    arrays = (master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale)
+    tensors = (master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad, param_out)
     _need(clip_scale, 1, "clip_scale")
-    p = Prepared(_adamw8_sched, _state8_ptrs(n, arrays, grad, param_out) +
+    p = Prepared(_adamw8_sched, _state8_ptrs(n, tensors) +
                  [n, first_element, schedule.handle, _seed(seed), _ptr(clip_scale, 4, "clip_scale"),
                   _stream(stream, master)], "zero_shard_adamw8_step_scheduled")
-    p._keep = (arrays, grad, param_out, schedule, clip_scale)
+    p._keep = (tensors, schedule, clip_scale)
     return p
 
 
@@ -1016,7 +1020,7 @@ class MultiTensor8Table:
         T = len(masters)
         if any(len(x) != T for x in lists):
             raise ValueError("the seven lists must have the same length")
-        rows = [_state8_ptrs(x[0].numel(), x[:5], x[5], x[6]) for x in zip(*lists)]
+        rows = [_state8_ptrs(x[0].numel(), x) for x in zip(*lists)]
         tabs = [(c_vp * max(T, 1))(*[row[k] for row in rows]) for k in range(7)]
         ns = (c_i64 * max(T, 1))(*[t.numel() for t in masters])
         h = c_vp()
@@ -1057,7 +1061,9 @@ class MultiTensor8Table:
 
     def step(self, step: int, lr: float, beta1: float, beta2: float, eps: float, weight_decay: float,
              seed: int = 0, clip_scale=None, stream=None) -> None:
-        self.prepare_step(lr, beta1, beta2, eps, weight_decay, seed, clip_scale, stream)(step)
+        _need(clip_scale, 1, "clip_scale")
+        _check(_mt8_step(self._h, step, lr, beta1, beta2, eps, weight_decay, _seed(seed),
+                         _ptr(clip_scale, 4, "clip_scale"), self._stream_of(stream)), "zero_mt8_table_adamw8_step")
 
     def prepare_step_scheduled(self, schedule: AdamWSchedule, seed: int = 0, clip_scale=None,
                                stream=None) -> Prepared:
@@ -1080,7 +1086,7 @@ def _reduce8_args(plan: Plan, rank: int, replicas, begin: int, count: int, array
     _need(shard_grad, plan.shard_numel, "shard_grad")
     _need(clip_scale, 1, "clip_scale")
     ptrs = (c_vp * max(len(replicas), 1))(*[_ptr(r, 2, "replica") for r in replicas])
-    state = _state8_ptrs(plan.shard_numel, arrays, None, param_out)
+    state = _state8_ptrs(plan.shard_numel, (*arrays, None, param_out))
     return [plan.handle, rank, ptrs, len(replicas), begin, count] + state[:5] + [
         state[6], _ptr(shard_grad, 2, "shard_grad")]
 

@@ -21,7 +21,8 @@
 // under it. Four elements a lane: with 8 a lane's two 16-byte stores of the
 // master leave half-written lines behind each other and the write-through stores
 // fell to 3.1 TB/s (662 us at 125 M elements); with 2 the random words, shared
-// by 8 elements, are computed four times over (about 400 us).
+// by 8 elements, are computed four times over (about 400 us). Measured: 125 M
+// elements 312 us, 6.45 TB/s (a 1 GB copy: 6.55).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -47,7 +48,9 @@ using zero::state8::Key;
 using zero::state8::Words;
 using zero::state8::kBlock;
 
-constexpr int kThreads = 256;
+// Two waves a workgroup, four elements a lane. Measured on MI355X, 125 M
+// elements: 64 threads 328 us, 128 312 us, 256 318 us, 512 338 us.
+constexpr int kThreads = 128;
 
 constexpr int kEpt = zero::state8::kLaneElems;
 constexpr int64_t kChunk = int64_t(kThreads) * kEpt;
@@ -85,6 +88,22 @@ __device__ __forceinline__ float read_clip(const float* clip_scale) {
     return clip_scale != nullptr ? *clip_scale : 1.0f;
 }
 
+// The arrays from element `base` (a multiple of the block) on.
+__device__ __forceinline__ Arrays from(const Arrays& a, int64_t base) {
+    return Arrays{a.p + base, a.m + base, a.ms + base / kBlock, a.v + base, a.vs + base / kBlock, a.g + base, a.o + base};
+}
+
+// Elements of a workgroup's chunk at `base` that lie below n, and of a lane's
+// kEpt elements from t on.
+__device__ __forceinline__ int chunk_left(int64_t n, int64_t base) {
+    const int64_t left = n - base;
+    return left <= 0 ? 0 : (left < kChunk ? static_cast<int>(left) : static_cast<int>(kChunk));
+}
+__device__ __forceinline__ int lane_live(int left, uint32_t t) {
+    const int live = left - static_cast<int>(t);
+    return live <= 0 ? 0 : (live < kEpt ? live : kEpt);
+}
+
 // What a lane holds of its elements: those at or past n are zeros.
 struct Lane {
     float p[kEpt] = {};
@@ -93,40 +112,42 @@ struct Lane {
     int live = 0;                          // elements below n
 };
 
+// In everything below, the arrays start at the workgroup's chunk (the same
+// pointers in every lane) and t is the lane's first element in it, so that a
+// wave addresses an array by a scalar base and a 32-bit offset.
+//
 // VEC: every array allows accesses of kEpt elements. Lanes with fewer than
 // kEpt elements left, and all lanes where VEC does not hold, go one by one.
 template <bool VEC>
-__device__ __forceinline__ void load_state(Lane& l, const Arrays& a, int64_t n, int64_t i) {
-    const int64_t left = n - i;
-    l.live = left <= 0 ? 0 : (left < kEpt ? static_cast<int>(left) : kEpt);
+__device__ __forceinline__ void load_state(Lane& l, const Arrays& a, uint32_t t) {
     if (VEC && l.live == kEpt) {
-        const f32x4 x = zero::dev::ld_stream(reinterpret_cast<const f32x4*>(a.p + i));
-        l.m = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(a.m + i));
-        l.v = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(a.v + i));
+        const f32x4 x = zero::dev::ld_stream(reinterpret_cast<const f32x4*>(a.p + t));
+        l.m = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(a.m + t));
+        l.v = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(a.v + t));
 #pragma unroll
         for (int k = 0; k < kEpt; ++k) l.p[k] = x[k];
     } else {
 #pragma unroll
         for (int k = 0; k < kEpt; ++k) {
             if (k < l.live) {
-                l.p[k] = a.p[i + k];
-                l.m |= static_cast<uint32_t>(a.m[i + k]) << (8 * k);
-                l.v |= static_cast<uint32_t>(a.v[i + k]) << (8 * k);
+                l.p[k] = a.p[t + k];
+                l.m |= static_cast<uint32_t>(a.m[t + k]) << (8 * k);
+                l.v |= static_cast<uint32_t>(a.v[t + k]) << (8 * k);
             }
         }
     }
     if (l.live > 0) {
-        l.ms = a.ms[i / kBlock];
-        l.vs = a.vs[i / kBlock];
+        l.ms = a.ms[t / kBlock];
+        l.vs = a.vs[t / kBlock];
     }
 }
 
 template <bool VEC>
-__device__ __forceinline__ void load_grad(float (&g)[kEpt], const uint16_t* grad, int live, int64_t i) {
+__device__ __forceinline__ void load_grad(float (&g)[kEpt], const uint16_t* grad, int live, uint32_t t) {
 #pragma unroll
     for (int k = 0; k < kEpt; ++k) g[k] = 0.0f;
     if (VEC && live == kEpt) {
-        const u32x2 x = zero::dev::ld_stream(reinterpret_cast<const u32x2*>(grad + i));
+        const u32x2 x = zero::dev::ld_stream(reinterpret_cast<const u32x2*>(grad + t));
         g[0] = zero::dev::lo_bf16(x[0]);
         g[1] = zero::dev::hi_bf16(x[0]);
         g[2] = zero::dev::lo_bf16(x[1]);
@@ -134,15 +155,16 @@ __device__ __forceinline__ void load_grad(float (&g)[kEpt], const uint16_t* grad
     } else {
 #pragma unroll
         for (int k = 0; k < kEpt; ++k)
-            if (k < live) g[k] = zero::dev::bf16_to_f32(grad[i + k]);
+            if (k < live) g[k] = zero::dev::bf16_to_f32(grad[t + k]);
     }
 }
 
-// Updates a lane's elements from their clipped gradients and writes them back.
-// Every lane of the wave calls it (the block maxima cross lanes); a lane past n
-// brings zeros, which change no maximum.
+// Updates a lane's elements from their clipped gradients and writes them back;
+// `first` is the number of the chunk's first element. Every lane of the wave
+// calls it (the block maxima cross lanes); a lane past n brings zeros, which
+// change no maximum.
 template <bool VEC>
-__device__ __forceinline__ void update_and_store(Lane& l, const float (&g)[kEpt], const Arrays& a, int64_t i,
+__device__ __forceinline__ void update_and_store(Lane& l, const float (&g)[kEpt], const Arrays& a, uint32_t t,
                                                  int64_t first, const AdamScalars& c, Key key) {
     float m[kEpt], v[kEpt];
     zero::state8::decode4(l.m, l.ms, m);
@@ -152,34 +174,33 @@ __device__ __forceinline__ void update_and_store(Lane& l, const float (&g)[kEpt]
     const uint32_t ms = zero::state8::scale_byte(zero::state8::block_max(zero::state8::max_bits4(m)));
     const uint32_t vs = zero::state8::scale_byte(zero::state8::block_max(zero::state8::max_bits4(v)));
     if (l.live == 0) return;
-    const uint64_t e = static_cast<uint64_t>(first + i);
-    const Words words = zero::state8::group_words(e >> 3, key);
+    const Words words = zero::state8::group_words((static_cast<uint64_t>(first) >> 3) + (t >> 3), key);
     uint32_t rm[kEpt], rv[kEpt];
-    rm[0] = words.a + (static_cast<uint32_t>(e) & 7u) * words.b;
+    rm[0] = words.a + ((t & 4u) != 0 ? words.b << 2 : 0u);
 #pragma unroll
     for (int k = 1; k < kEpt; ++k) rm[k] = rm[k - 1] + words.b;
 #pragma unroll
     for (int k = 0; k < kEpt; ++k) rv[k] = rm[k] << 12;      // the word's low 20 bits, as a seed's high ones
     const uint32_t mw = zero::state8::encode4(m, ms, rm);
     const uint32_t vw = zero::state8::positive4(zero::state8::encode4(v, vs, rv), v, vs);
-    if (i % kBlock == 0) {                 // the block's first lane
-        a.ms[i / kBlock] = static_cast<uint8_t>(ms);
-        a.vs[i / kBlock] = static_cast<uint8_t>(vs);
+    if (t % kBlock == 0) {                 // the block's first lane
+        a.ms[t / kBlock] = static_cast<uint8_t>(ms);
+        a.vs[t / kBlock] = static_cast<uint8_t>(vs);
     }
     if (VEC && l.live == kEpt) {
-        zero::dev::st_stream(reinterpret_cast<f32x4*>(a.p + i), f32x4{l.p[0], l.p[1], l.p[2], l.p[3]});
-        zero::dev::st_stream(reinterpret_cast<uint32_t*>(a.m + i), mw);
-        zero::dev::st_stream(reinterpret_cast<uint32_t*>(a.v + i), vw);
-        zero::dev::st_stream(reinterpret_cast<u32x2*>(a.o + i),
-                             u32x2{zero::dev::pack_bf16(l.p[0], l.p[1]), zero::dev::pack_bf16(l.p[2], l.p[3])});
+        zero::dev::st_stream_at(a.p, 4 * t, f32x4{l.p[0], l.p[1], l.p[2], l.p[3]});
+        zero::dev::st_stream_at(a.m, t, mw);
+        zero::dev::st_stream_at(a.v, t, vw);
+        zero::dev::st_stream_at(a.o, 2 * t,
+                                u32x2{zero::dev::pack_bf16(l.p[0], l.p[1]), zero::dev::pack_bf16(l.p[2], l.p[3])});
     } else {
 #pragma unroll
         for (int k = 0; k < kEpt; ++k) {
             if (k < l.live) {
-                a.p[i + k] = l.p[k];
-                a.m[i + k] = static_cast<uint8_t>(mw >> (8 * k));
-                a.v[i + k] = static_cast<uint8_t>(vw >> (8 * k));
-                a.o[i + k] = static_cast<uint16_t>(zero::dev::f32_to_bf16(l.p[k]));
+                a.p[t + k] = l.p[k];
+                a.m[t + k] = static_cast<uint8_t>(mw >> (8 * k));
+                a.v[t + k] = static_cast<uint8_t>(vw >> (8 * k));
+                a.o[t + k] = static_cast<uint16_t>(zero::dev::f32_to_bf16(l.p[k]));
             }
         }
     }
@@ -187,18 +208,20 @@ __device__ __forceinline__ void update_and_store(Lane& l, const float (&g)[kEpt]
 
 // One workgroup's kChunk elements from `base` of arrays of n elements.
 template <bool VEC>
-__device__ __forceinline__ void update_chunk(const Arrays& a, int64_t n, int64_t base, int64_t first,
+__device__ __forceinline__ void update_chunk(const Arrays& whole, int64_t n, int64_t base, int64_t first,
                                              const AdamScalars& c, Key key, const float* clip_scale) {
-    const int64_t i = base + int64_t(threadIdx.x) * kEpt;
+    const Arrays a = from(whole, base);
+    const uint32_t t = threadIdx.x * kEpt;
     Lane l;
-    load_state<VEC>(l, a, n, i);
+    l.live = lane_live(chunk_left(n, base), t);
+    load_state<VEC>(l, a, t);
     float g[kEpt];
-    load_grad<VEC>(g, a.g, l.live, i);
+    load_grad<VEC>(g, a.g, l.live, t);
     const float clip = read_clip(clip_scale);   // after the loads are issued
     if (!isfinite(clip)) return;                // the same in every lane
 #pragma unroll
     for (int k = 0; k < kEpt; ++k) g[k] = g[k] * clip;
-    update_and_store<VEC>(l, g, a, i, first, c, key);
+    update_and_store<VEC>(l, g, a, t, first + base, c, key);
 }
 
 // The step's scalars and key: from the call, or from a schedule's state.
@@ -258,17 +281,25 @@ __global__ __launch_bounds__(kThreads) void adamw8_table_kernel(const Desc* __re
 struct Replicas {
     const uint16_t* p[ZERO_MAX_REPLICAS];
 };
-constexpr int kReplicaBatch = 8;           // replica loads in flight per lane
+// Replica loads in flight per lane (B). A full chip has waves enough to cover
+// the latency of two at a time, and keeps its streams in order: 164 M elements
+// of 8 replicas take 781 us with B = 2, 786 with 3, 809 with 4 or 8; 32 M of 64
+// replicas 745, 787 and 805. A window that the chip holds at once waits for
+// each load: 1 M elements of 8 replicas take 8.2 us with B = 2 and 7.0 with 8,
+// of 64 replicas 29.3 and 24.6 (4 M of 8: 22.5 and 21.3; 8 M: 42.8 and 42.6). A
+// batch of 8 loads its first replica again in place of each that it lacks, so
+// few replicas take B = 2 (120 M of 2: 354 us against 422).
+constexpr int kWideBatch = 8, kBatch = 2;
+inline bool wide_batch(int64_t n, int32_t n_replicas) {
+    return n <= (int64_t(1) << 22) && n_replicas > kWideBatch / 2;
+}
 
-template <bool VEC>
+template <bool VEC, int B>
 __device__ __forceinline__ void mean_grad(float (&g)[kEpt], const Replicas& reps, int n_rep, int64_t src_off,
-                                          int live, int64_t i) {
-    float acc[kEpt];
-#pragma unroll
-    for (int k = 0; k < kEpt; ++k) acc[k] = 0.0f;
-    const float count = static_cast<float>(n_rep);
+                                          int live, uint32_t t) {
+    float acc[kEpt] = {};
     if (VEC && live == kEpt) {
-        zero::dev::for_replicas<kReplicaBatch, u32x2>(reps.p, n_rep, src_off, i / kEpt, [&](u32x2 x) {
+        zero::dev::for_replicas<B, u32x2>(reps.p, n_rep, src_off, t / kEpt, [&](u32x2 x) {
             acc[0] = acc[0] + zero::dev::lo_bf16(x[0]);
             acc[1] = acc[1] + zero::dev::hi_bf16(x[0]);
             acc[2] = acc[2] + zero::dev::lo_bf16(x[1]);
@@ -276,74 +307,92 @@ __device__ __forceinline__ void mean_grad(float (&g)[kEpt], const Replicas& reps
         });
     } else if (live > 0) {
         for (int r = 0; r < n_rep; ++r) {
-            const uint16_t* p = reps.p[r] + src_off + i;
+            const uint16_t* p = reps.p[r] + src_off;
 #pragma unroll
             for (int k = 0; k < kEpt; ++k)
-                if (k < live) acc[k] = acc[k] + zero::dev::bf16_to_f32(p[k]);
+                if (k < live) acc[k] = acc[k] + zero::dev::bf16_to_f32(p[t + k]);
         }
     }
+    const float count = static_cast<float>(n_rep);
 #pragma unroll
     for (int k = 0; k < kEpt; ++k)
         g[k] = zero::dev::bf16_to_f32(zero::dev::f32_to_bf16(acc[k] / count));
 }
 
-template <bool VEC, typename Step>
-__global__ __launch_bounds__(kThreads) void reduce_adamw8_kernel(Replicas reps, int n_rep, int64_t src_off, Arrays a,
-                                                                 uint16_t* __restrict__ grad_out, int64_t n,
-                                                                 int64_t first, Step step,
+template <bool VEC, int B, typename Step>
+__global__ __launch_bounds__(kThreads) void reduce_adamw8_kernel(Replicas reps, int n_rep, int64_t src_off,
+                                                                 Arrays whole, uint16_t* __restrict__ grad_out,
+                                                                 int64_t n, int64_t first, Step step,
                                                                  const float* __restrict__ clip_scale) {
-    const int64_t i = workgroup() * kChunk + int64_t(threadIdx.x) * kEpt;
+    const int64_t base = workgroup() * kChunk;
+    const Arrays a = from(whole, base);
+    const uint32_t t = threadIdx.x * kEpt;
     Lane l;
-    load_state<VEC>(l, a, n, i);
+    l.live = lane_live(chunk_left(n, base), t);
+    load_state<VEC>(l, a, t);
     float g[kEpt];
-    mean_grad<VEC>(g, reps, n_rep, src_off, l.live, i);
+    mean_grad<VEC, B>(g, reps, n_rep, src_off + base, l.live, t);
     if (grad_out != nullptr) {
+        uint16_t* const out = grad_out + base;
         if (VEC && l.live == kEpt) {
-            zero::dev::st_stream(reinterpret_cast<u32x2*>(grad_out + i),
-                                 u32x2{zero::dev::pack_bf16(g[0], g[1]), zero::dev::pack_bf16(g[2], g[3])});
+            zero::dev::st_stream_at(out, 2 * t, u32x2{zero::dev::pack_bf16(g[0], g[1]), zero::dev::pack_bf16(g[2], g[3])});
         } else {
 #pragma unroll
             for (int k = 0; k < kEpt; ++k)
-                if (k < l.live) grad_out[i + k] = static_cast<uint16_t>(zero::dev::f32_to_bf16(g[k]));
+                if (k < l.live) out[t + k] = static_cast<uint16_t>(zero::dev::f32_to_bf16(g[k]));
         }
     }
     const float clip = read_clip(clip_scale);
     if (!isfinite(clip)) return;
 #pragma unroll
     for (int k = 0; k < kEpt; ++k) g[k] = g[k] * clip;
-    update_and_store<VEC>(l, g, a, i, first, step.scalars(), step.random_key());
+    update_and_store<VEC>(l, g, a, t, first + base, step.scalars(), step.random_key());
 }
 
 // ------------------------------------------------------------ conversions
+
+// A workgroup converts several chunks (rows), the loads of all of them issued first.
+// Measured on MI355X at 125 M elements: quantize with 1, 2, 3, 4, 8 rows 108,
+// 98, 102, 102, 105 us; dequantize 138, 116, 104, 103, 113 us.
+constexpr int kQuantizeRows = 2, kDequantizeRows = 4;
 
 // fp32 to codes and scales, rounded to nearest even.
 template <bool VEC>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const float* __restrict__ x, uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales, int64_t n, int second) {
-    const int64_t i = (workgroup() * kThreads + threadIdx.x) * kEpt;
-    const int64_t left = n - i;
-    const int live = left <= 0 ? 0 : (left < 4 ? static_cast<int>(left) : 4);
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (VEC && live == 4) {
-        const f32x4 q = zero::dev::ld_stream(reinterpret_cast<const f32x4*>(x + i));
+    const int64_t base = workgroup() * (kQuantizeRows * kChunk);
+    const uint32_t t = threadIdx.x * kEpt;
+    float v[kQuantizeRows][kEpt] = {};
+    int live[kQuantizeRows];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = q[k];
-    } else {
+    for (int r = 0; r < kQuantizeRows; ++r) {
+        const float* const from_x = x + base + r * kChunk;
+        live[r] = lane_live(chunk_left(n, base + r * kChunk), t);
+        if (VEC && live[r] == kEpt) {
+            const f32x4 q = zero::dev::ld_stream(reinterpret_cast<const f32x4*>(from_x + t));
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < live) v[k] = x[i + k];
+            for (int k = 0; k < kEpt; ++k) v[r][k] = q[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < kEpt; ++k)
+                if (k < live[r]) v[r][k] = from_x[t + k];
+        }
     }
-    const uint32_t byte = zero::state8::scale_byte(zero::state8::block_max(zero::state8::max_bits4(v)));
-    if (live == 0) return;
-    uint32_t w = zero::state8::nearest4(v, byte);
-    if (second) w = zero::state8::positive4(w, v, byte);
-    if (i % kBlock == 0) scales[i / kBlock] = static_cast<uint8_t>(byte);
-    if (VEC && live == 4) {
-        zero::dev::st_stream(reinterpret_cast<uint32_t*>(codes + i), w);
-    } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < live) codes[i + k] = static_cast<uint8_t>(w >> (8 * k));
+    for (int r = 0; r < kQuantizeRows; ++r) {
+        const uint32_t byte = zero::state8::scale_byte(zero::state8::block_max(zero::state8::max_bits4(v[r])));
+        if (live[r] == 0) continue;
+        uint32_t w = zero::state8::nearest4(v[r], byte);
+        if (second) w = zero::state8::positive4(w, v[r], byte);
+        uint8_t* const to = codes + base + r * kChunk;
+        if (t % kBlock == 0) scales[(base + r * kChunk) / kBlock + t / kBlock] = static_cast<uint8_t>(byte);
+        if (VEC && live[r] == kEpt) {
+            zero::dev::st_stream_at(to, t, w);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kEpt; ++k)
+                if (k < live[r]) to[t + k] = static_cast<uint8_t>(w >> (8 * k));
+        }
     }
 }
 
@@ -351,27 +400,36 @@ template <bool VEC>
 __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __restrict__ codes,
                                                               const uint8_t* __restrict__ scales,
                                                               float* __restrict__ out, int64_t n) {
-    const int64_t i = (workgroup() * kThreads + threadIdx.x) * kEpt;
-    const int64_t left = n - i;
-    const int live = left <= 0 ? 0 : (left < 4 ? static_cast<int>(left) : 4);
-    if (live == 0) return;
-    const uint32_t byte = scales[i / kBlock];
-    uint32_t w = 0;
-    if (VEC && live == 4) {
-        w = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(codes + i));
-    } else {
+    const int64_t base = workgroup() * (kDequantizeRows * kChunk);
+    const uint32_t t = threadIdx.x * kEpt;
+    uint32_t w[kDequantizeRows] = {}, byte[kDequantizeRows] = {};
+    int live[kDequantizeRows];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < live) w |= static_cast<uint32_t>(codes[i + k]) << (8 * k);
+    for (int r = 0; r < kDequantizeRows; ++r) {
+        const uint8_t* const from_c = codes + base + r * kChunk;
+        live[r] = lane_live(chunk_left(n, base + r * kChunk), t);
+        if (live[r] > 0) byte[r] = scales[(base + r * kChunk) / kBlock + t / kBlock];
+        if (VEC && live[r] == kEpt) {
+            w[r] = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(from_c + t));
+        } else {
+#pragma unroll
+            for (int k = 0; k < kEpt; ++k)
+                if (k < live[r]) w[r] |= static_cast<uint32_t>(from_c[t + k]) << (8 * k);
+        }
     }
-    float v[4];
-    zero::state8::decode4(w, byte, v);
-    if (VEC && live == 4) {
-        zero::dev::st_stream(reinterpret_cast<f32x4*>(out + i), f32x4{v[0], v[1], v[2], v[3]});
-    } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < live) out[i + k] = v[k];
+    for (int r = 0; r < kDequantizeRows; ++r) {
+        if (live[r] == 0) continue;
+        float v[kEpt];
+        zero::state8::decode4(w[r], byte[r], v);
+        float* const to = out + base + r * kChunk;
+        if (VEC && live[r] == kEpt) {
+            zero::dev::st_stream_at(to, 4 * t, f32x4{v[0], v[1], v[2], v[3]});
+        } else {
+#pragma unroll
+            for (int k = 0; k < kEpt; ++k)
+                if (k < live[r]) to[t + k] = v[k];
+        }
     }
 }
 
@@ -403,8 +461,8 @@ zero_status check_first(int64_t first, int64_t n, const char* who) {
     return ZERO_OK;
 }
 
-// No NULL array, no written array overlapping another array of the update
-// (n > 0). `extra`: another written span (p NULL for none).
+// "<a> overlaps <b>" for a written array of an update over n > 0 elements, or an
+// empty string.
 std::string array_clash(const Arrays& a, int64_t n) {
     const size_t nb = static_cast<size_t>(zero::state8::blocks_of(n)), b = static_cast<size_t>(n);
     const zero::Span wr[] = {{a.p, 4 * b, "master"},          {a.m, b, "exp_avg"}, {a.ms, nb, "exp_avg_scale"},
@@ -423,11 +481,11 @@ zero_status launch_flat(const Arrays& a, int64_t n, int64_t first, const Step& s
     if (st != ZERO_OK) return st;
     if (n == 0) return ZERO_OK;
     if (any_null(a)) return fail(ZERO_EINVAL, std::string(who) + ": NULL array");
-    const std::string clash = array_clash(a, n);
-    if (!clash.empty()) return fail(ZERO_EINVAL, std::string(who) + ": " + clash);
     dim3 grid;
     st = grid_for(n, kChunk, &grid, who);
     if (st != ZERO_OK) return st;
+    const std::string clash = array_clash(a, n);
+    if (!clash.empty()) return fail(ZERO_EINVAL, std::string(who) + ": " + clash);
     if (vector_ok(a))
         hipLaunchKernelGGL((adamw8_kernel<true, Step>), grid, dim3(kThreads), 0, stream, a, n, first, step, clip_scale);
     else
@@ -675,12 +733,11 @@ zero_status launch_reduce(const zero_plan* plan, int32_t rank, const uint16_t* c
     dim3 grid;
     st = grid_for(n, kChunk, &grid, who);
     if (st != ZERO_OK) return st;
-    if (vec)
-        hipLaunchKernelGGL((reduce_adamw8_kernel<true, Step>), grid, dim3(kThreads), 0, stream, table, n_replicas,
-                           src_off, a, grad_out, n, first + at, step, clip_scale);
-    else
-        hipLaunchKernelGGL((reduce_adamw8_kernel<false, Step>), grid, dim3(kThreads), 0, stream, table, n_replicas,
-                           src_off, a, grad_out, n, first + at, step, clip_scale);
+    const auto kernel = !vec ? reduce_adamw8_kernel<false, kBatch, Step>
+                             : (wide_batch(n, n_replicas) ? reduce_adamw8_kernel<true, kWideBatch, Step>
+                                                          : reduce_adamw8_kernel<true, kBatch, Step>);
+    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, table, n_replicas, src_off, a, grad_out, n, first + at,
+                       step, clip_scale);
     return zero::check_hip(hipGetLastError(), who);
 }
 
@@ -737,7 +794,7 @@ extern "C" zero_status zero_state8_quantize(const float* x, int64_t n, int32_t s
     const std::string clash = zero::first_overlap(wr, 2, rd, 1);
     if (!clash.empty()) return fail(ZERO_EINVAL, "zero_state8_quantize: " + clash);
     dim3 grid;
-    const zero_status st = grid_for(n, kChunk, &grid, who);
+    const zero_status st = grid_for(n, kQuantizeRows * kChunk, &grid, who);
     if (st != ZERO_OK) return st;
     if (aligned(x, 16) && aligned(codes, 4))
         hipLaunchKernelGGL(quantize_kernel<true>, grid, dim3(kThreads), 0, stream, x, codes, scales, n, second_moment);
@@ -760,7 +817,7 @@ extern "C" zero_status zero_state8_dequantize(const uint8_t* codes, const uint8_
     const std::string clash = zero::first_overlap(wr, 1, rd, 2);
     if (!clash.empty()) return fail(ZERO_EINVAL, "zero_state8_dequantize: " + clash);
     dim3 grid;
-    const zero_status st = grid_for(n, kChunk, &grid, who);
+    const zero_status st = grid_for(n, kDequantizeRows * kChunk, &grid, who);
     if (st != ZERO_OK) return st;
     if (aligned(out, 16) && aligned(codes, 4))
         hipLaunchKernelGGL(dequantize_kernel<true>, grid, dim3(kThreads), 0, stream, codes, scales, out, n);

@@ -45,7 +45,7 @@ namespace state8 {
 constexpr int kBlock = ZERO_STATE8_BLOCK;
 static_assert(kBlock == 128, "the lane groups below are laid out for blocks of 128");
 
-inline int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
+inline int64_t blocks_of(int64_t n) { return n / kBlock + (n % kBlock != 0); }
 
 // ------------------------------------------------------------ random words
 //
