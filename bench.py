@@ -80,6 +80,10 @@ def parse_args(argv=None):
                     help="count AdamW's step on the device (RankStep(device_step=True)): the "
                          "scheduled update kernels, the AdamW phase including the one-lane "
                          "advance; a comparison run, not the benchmark's line")
+    ap.add_argument("--state-bits", type=int, default=32, choices=(8, 32),
+                    help="hold AdamW's two moments in fp32 (the benchmark's line) or in 8 bits "
+                         "(RankStep(state_bits=8)); a comparison run, without the oracle's timing; "
+                         "not with the offload workload")
     ap.add_argument("--profile-extra", action="store_true",
                     help="with --profile-steps: first run each phase timed outside the step once "
                          "(the step's dispatches stay the run's last ones)")
@@ -122,7 +126,7 @@ class RankWorkload:
         "gpt2-small-fsdp2-pertensor": ("gpt2-small", 8, 7, 8, 0, True, "shard0"),
     }
 
-    def __init__(self, name: str, device, device_step: bool = False):
+    def __init__(self, name: str, device, device_step: bool = False, state_bits: int = 32):
         import torch
 
         import synth
@@ -152,10 +156,13 @@ class RankWorkload:
         self.per_tensor = name.endswith("-pertensor")
         if device_step and self.offload:
             raise SystemExit("bench.py: --device-step takes device state; not with the offload workload")
+        if state_bits == 8 and self.offload:
+            raise SystemExit("bench.py: --state-bits 8 takes device state; not with the offload workload")
+        self.state_bits = state_bits
         self.rs = RankStep(self.plan, rank, len(spans), self.hyper, self.max_norm, device,
                            gather=gather, offload=self.offload, offload_chunk=OFFLOAD_CHUNK,
                            host_threads=self.n_threads, per_param=self.per_tensor,
-                           device_step=device_step)
+                           device_step=device_step, state_bits=state_bits, seed=self.seed)
         rs = self.rs
         if self.offload:         # the fp32 master lives in host memory
             rs.master.copy_(torch.from_numpy(synth.normal_f32(S, self.seed, synth.KIND_MASTER, 0, 0,
@@ -323,6 +330,9 @@ class RankWorkload:
         rs = self.rs
         self.segs = rs.segments
         sl = [slice(soff, soff + ln) for (_, _, soff, ln) in self.segs]
+        self.elems_per_step = sum(x.stop - x.start for x in sl)
+        if self.state_bits == 8:        # no list call takes 8-bit moments
+            return
         lm = [t.clone() for t in rs.master_tensors]
         lmm = [torch.zeros_like(t) for t in rs.master_tensors]
         lv = [torch.zeros_like(t) for t in rs.master_tensors]
@@ -338,7 +348,6 @@ class RankWorkload:
             call_list(self.t_list)
         self.extra_phases = (list(getattr(self, "extra_phases", None) or [])
                              + [("adamw_list", adamw_list)])
-        self.elems_per_step = sum(x.stop - x.start for x in sl)
 
     def state_arrays(self):
         """The rank's fp32 master, m and v over its coalesced buffer, on the host
@@ -398,7 +407,7 @@ class RankWorkload:
         # 28 B/elem of state traffic is in host DRAM. The per-parameter update
         # covers the chunks' elements only (not the coalesced buffer's padding).
         b = {"clip": 8 * (self.n_ranks + max(len(self.windows), 1)) + 4,
-             "adamw": 4 * S if self.offload else 28 * self.elems_per_step}
+             "adamw": 4 * S if self.offload else adamw_bytes_per_element(self) * self.elems_per_step}
         if self.replicas:
             b["reduce"] = (2 * self.replicas + 2) * S
         else:
@@ -409,7 +418,7 @@ class RankWorkload:
             b["flatten"] = b["flatten_call"] = 4 * self.phi + 2 * (self.P - self.phi)
         if "gather" in b:
             b["gather_call"] = b["gather"]
-        if getattr(self, "per_tensor", False):
+        if getattr(self, "per_tensor", False) and getattr(self, "state_bits", 32) == 32:
             b["adamw_list"] = 28 * self.elems_per_step
         if getattr(self, "rt_table", None) is not None:
             b["reduce_tensors"] = (2 * self.replicas + 2) * S
@@ -424,7 +433,7 @@ class RankWorkload:
                if self.layout == "shard0" else "")
         upd = (f"ZeRO-Offload AdamW (fp32 state in host DRAM, {self.n_threads} host threads, "
                f"bf16 grads/params over PCIe in {OFFLOAD_CHUNK}-element chunks)"
-               if self.offload else "AdamW")
+               if self.offload else "AdamW" + moments_of(self))
         return (f"{self.workload.name} tensor list{lay}, N_d={self.n_ranks}, rank {self.rank} shard "
                 f"of {self.S} elements; step = {red} + clip {self.max_norm} + {upd}{g}")
 
@@ -432,7 +441,7 @@ class RankWorkload:
 class AllRanksWorkload:
     """Every rank of one data-parallel job, in turn on one GPU: reduce, AdamW, then gather."""
 
-    def __init__(self, name: str, device):
+    def __init__(self, name: str, device, state_bits: int = 32):
         import torch
 
         import synth
@@ -443,6 +452,7 @@ class AllRanksWorkload:
 
         # "-fused": each rank's reduce and AdamW in one pass (no clip between them)
         self.fused = name.endswith("-fused")
+        self.state_bits = state_bits
         w = synth.WORKLOADS[name[:-len("-fused")] if self.fused else name]
         self.name, self.workload, self.device = name, w, device
         self.n_ranks, self.rank, self.replicas = w.n_ranks, None, w.replicas
@@ -452,10 +462,14 @@ class AllRanksWorkload:
         self.P, self.S, self.phi = P, S, phi
         self.hyper = Hyper(lr=w.lr, beta1=w.beta1, beta2=w.beta2, eps=w.eps,
                            weight_decay=w.weight_decay)
-        views, self.arena = _staggered_arena(
-            [(P, torch.float32), (P, torch.float32), (P, torch.float32), (P, torch.int16),
-             (P, torch.int16)], device)
-        self.master, self.m, self.v, self.grad, self.param = views
+        moment = torch.float32 if state_bits == 32 else torch.uint8
+        specs = [(P, torch.float32), (P, moment), (P, moment), (P, torch.int16), (P, torch.int16)]
+        if state_bits == 8:      # the shards hold whole blocks: one scale array serves every rank
+            if S % zm.ZERO_STATE8_BLOCK:
+                raise ValueError("8-bit moments of all ranks need shards of whole blocks")
+            specs += [(zm.state8_blocks(P), torch.uint8)] * 2
+        views, self.arena = _staggered_arena(specs, device)
+        self.master, self.m, self.v, self.grad, self.param = views[:5]
         synth.device_normal_f32(self.master, self.seed, synth.KIND_MASTER, 0, 0, 0, phi,
                                 synth.MASTER_SIGMA)
         self.reps = staggered_replicas(self.replicas, P, device)
@@ -472,11 +486,20 @@ class AllRanksWorkload:
         self._reduce = [zb.prepare_grad_reduce_shard(self.plan, r, self.reps, 0, P,
                                                      self.grad[sl[r]], None, None, st)
                         for r in range(w.n_ranks)]
-        self._adamw = [zb.prepare_shard_adamw_step(self.master[sl[r]], self.m[sl[r]],
-                                                   self.v[sl[r]], self.grad[sl[r]],
-                                                   self.param[sl[r]], clip_scale=None, stream=st,
-                                                   **self.hyper.as_kwargs())
-                       for r in range(w.n_ranks)]
+        if state_bits == 8:
+            nb = S // zm.ZERO_STATE8_BLOCK
+            self.ms, self.vs = views[5:]
+            bl = [slice(r * nb, (r + 1) * nb) for r in range(w.n_ranks)]
+            self._adamw = [zb.prepare_shard_adamw8_step(
+                self.master[sl[r]], self.m[sl[r]], self.ms[bl[r]], self.v[sl[r]], self.vs[bl[r]],
+                self.grad[sl[r]], self.param[sl[r]], seed=self.seed, first_element=r * S, stream=st,
+                **self.hyper.as_kwargs()) for r in range(w.n_ranks)]
+        else:
+            self._adamw = [zb.prepare_shard_adamw_step(self.master[sl[r]], self.m[sl[r]],
+                                                       self.v[sl[r]], self.grad[sl[r]],
+                                                       self.param[sl[r]], clip_scale=None, stream=st,
+                                                       **self.hyper.as_kwargs())
+                           for r in range(w.n_ranks)]
         self._gt = zb.CopyTable.gather(self.plan, [self.param[s] for s in sl], self.tensors)
         self._gather = self._gt.prepare_run(st)
         # outside the step: one replica flattening its per-tensor gradients into a
@@ -509,20 +532,28 @@ class AllRanksWorkload:
 
         self.phases = [("reduce", reduce_all), ("adamw", adamw_all), ("gather", self._gather)]
         # AdamW-phase bytes per element and the kernel that phase runs
-        self.adamw_bpe, self.adamw_kernel = 28, "adamw_kernel"
+        self.adamw_bpe = adamw_bytes_per_element(self)
+        self.adamw_kernel = "adamw_kernel" if state_bits == 32 else "adamw8_kernel"
         if self.fused:
-            self._fused = [zb.prepare_reduce_adamw_step(
-                self.plan, r, self.reps, 0, P, self.master[sl[r]], self.m[sl[r]], self.v[sl[r]],
-                self.param[sl[r]], clip_scale=None, stream=st, **self.hyper.as_kwargs())
-                for r in range(w.n_ranks)]
+            if state_bits == 8:
+                self._fused = [zb.prepare_reduce_adamw8_step(
+                    self.plan, r, self.reps, 0, P, self.master[sl[r]], self.m[sl[r]], self.ms[bl[r]],
+                    self.v[sl[r]], self.vs[bl[r]], self.param[sl[r]], seed=self.seed,
+                    first_element=r * S, stream=st, **self.hyper.as_kwargs()) for r in range(w.n_ranks)]
+            else:
+                self._fused = [zb.prepare_reduce_adamw_step(
+                    self.plan, r, self.reps, 0, P, self.master[sl[r]], self.m[sl[r]], self.v[sl[r]],
+                    self.param[sl[r]], clip_scale=None, stream=st, **self.hyper.as_kwargs())
+                    for r in range(w.n_ranks)]
 
             def fused_all():
                 self.t += 1
                 for f in self._fused:
                     f(self.t)
             self.phases = [("adamw", fused_all), ("gather", self._gather)]
-            # R bf16 replicas read, master/m/v read and written, bf16 parameter written
-            self.adamw_bpe, self.adamw_kernel = 2 * self.replicas + 26, "reduce_adamw_kernel"
+            # R bf16 replicas read in place of the gradient
+            self.adamw_bpe += 2 * self.replicas - 2
+            self.adamw_kernel = "reduce_adamw_kernel" if state_bits == 32 else "reduce_adamw8_kernel"
         self.adamw_launches = w.n_ranks
         self.elems_per_step = P
 
@@ -534,12 +565,22 @@ class AllRanksWorkload:
                 "flatten_call": 4 * self.phi + 2 * (P - self.phi)}
 
     def describe(self):
-        update = (f"reduce of {self.replicas} bf16 replicas and AdamW in one pass per rank"
+        update = (f"reduce of {self.replicas} bf16 replicas and AdamW{moments_of(self)} in one pass per rank"
                   if self.fused else
-                  f"reduce of {self.replicas} bf16 replicas per rank + AdamW per shard")
+                  f"reduce of {self.replicas} bf16 replicas per rank + AdamW{moments_of(self)} per shard")
         return (f"{self.workload.name} tensor list, N_d={self.n_ranks}, all {self.n_ranks} ranks in "
                 f"turn ({self.S} elements each); step = {update} (no norm or clip) + gather of "
                 f"{len(self.workload.numels)} tensors")
+
+
+def adamw_bytes_per_element(wl) -> float:
+    """What AdamW reads and writes per element: the fp32 master, two moments (fp32, or a byte and
+    1/128 of a scale byte), the bf16 gradient and parameter."""
+    return 28 if getattr(wl, "state_bits", 32) == 32 else 16 + 4 / 128
+
+
+def moments_of(wl) -> str:
+    return "" if getattr(wl, "state_bits", 32) == 32 else " with 8-bit moments"
 
 
 def model_offsets(numels):
@@ -561,13 +602,16 @@ def padding_mask(plan, rank: int):
     return mask
 
 
-def make_workload(name: str, device, device_step: bool = False):
+def make_workload(name: str, device, device_step: bool = False, state_bits: int = 32):
     if name.startswith("gpt-1.3b"):
         if device_step:
             raise SystemExit("bench.py: --device-step applies to the one-rank workloads")
-        return AllRanksWorkload(name, device)
-    wl = RankWorkload(name, device, device_step)
-    if device_step:     # the scheduled kernels; the traffic entries are the plain kernel's
+        return AllRanksWorkload(name, device, state_bits)
+    wl = RankWorkload(name, device, device_step, state_bits)
+    if state_bits == 8:
+        wl.adamw_bpe = adamw_bytes_per_element(wl)
+        wl.adamw_kernel = "adamw8_table_kernel" if wl.per_tensor else "adamw8_kernel"
+    elif device_step:   # the scheduled kernels; the traffic entries are the plain kernel's
         wl.adamw_kernel = "adamw_table_sched_kernel" if wl.per_tensor else "adamw_sched_kernel"
     return wl
 
@@ -992,7 +1036,7 @@ def main(argv=None):
     if args.separate_arrays:
         step_module._staggered_arena = _separate_arrays
     print(f"[bench] setting up {args.workload}", file=sys.stderr, flush=True)
-    wl = make_workload(args.workload, device, args.device_step)
+    wl = make_workload(args.workload, device, args.device_step, args.state_bits)
     if args.profile_steps:
         if args.calibrate_copy:
             src = torch.ones(1 << 28, dtype=torch.float32, device=device)
@@ -1012,7 +1056,7 @@ def main(argv=None):
 
     m = measure(wl, steps, warmup)
     cpu = None
-    if args.cpu_baseline_seconds > 0:
+    if args.cpu_baseline_seconds > 0 and args.state_bits == 32:
         print("[bench] timing the oracle on the host", file=sys.stderr, flush=True)
         cpu = cpu_baseline(wl, args.cpu_baseline_seconds)
     ms_per_step, adamw_ms, adamw_each = m["ms_per_step"], m["adamw_ms"], m["adamw_each"]

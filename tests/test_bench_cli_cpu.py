@@ -120,3 +120,18 @@ def test_write_traffic_takes_bytes_per_launch(tmp_path, monkeypatch, workload, s
     assert e["fetch_scale"] == 2.0 and e["write_scale"] == 1.0
     assert e["bytes_per_launch"] == pytest.approx(28 * S, rel=1e-12)
     assert e["algorithmic_bytes"] == 28 * S
+
+
+def test_state_bits_option():
+    """--state-bits 8 is a comparison run: the line's default stays 32, other widths are refused, and
+    AdamW's bytes fall from 28 to 16 and 1/32 per element."""
+    sys.path.insert(0, ROOT)
+    import bench
+    assert bench.parse_args([]).state_bits == 32 and bench.parse_args(["--state-bits", "8"]).state_bits == 8
+    with pytest.raises(SystemExit):
+        bench.parse_args(["--state-bits", "16"])
+
+    class Stand:
+        state_bits = 8
+    assert bench.adamw_bytes_per_element(Stand) == 16 + 4 / 128 and "8-bit" in bench.moments_of(Stand)
+    assert bench.adamw_bytes_per_element(object()) == 28 and bench.moments_of(object()) == ""
