@@ -21,8 +21,8 @@
  *                           stepped in one launch
  *   zero_reduce_adamw_step  the reduce and the update in one pass, for a step
  *                           with no global norm between them
- *   zero_shard_adamw8_step, zero_mt8_table_*, zero_reduce_adamw8_step  the three
- *                           AdamW forms with the moments held in 8 bits
+ *   zero_shard_adamw8_step, zero_multi_tensor_adamw8_step, zero_mt8_table_*,
+ *   zero_reduce_adamw8_step  the AdamW forms with the moments held in 8 bits
  *   zero_state8_quantize, zero_state8_dequantize  those moments from and to fp32
  *   zero_gather_params      bf16 shards back to per-tensor parameters
  *                           (all-gather output layout, then un-flatten)
@@ -546,15 +546,30 @@ zero_status zero_shard_adamw8_step_scheduled(float* master, uint8_t* exp_avg, ui
                                              const zero_adamw_schedule* schedule, uint64_t seed,
                                              const float* clip_scale, hipStream_t stream);
 
-/* Many tensors, through a device table (zero_mt_table_*'s counterpart): each
- * tensor has its own arrays, and its own blocks, counted from its first
- * element. Tensor t's elements are numbered from first_element plus the
- * lengths of the tensors before it, each rounded up to a multiple of
- * ZERO_STATE8_BLOCK. Create, step, free, blocks and the caller's duties as
- * zero_mt_table_* (create: hipMalloc and a synchronous hipMemcpy on the
+/* Many tensors (zero_multi_tensor_adamw_step's and zero_mt_table_*'s
+ * counterparts): each tensor has its own arrays, and its own blocks, counted
+ * from its first element. Tensor t's elements are numbered from first_element
+ * plus the lengths of the tensors before it, each rounded up to a multiple of
+ * ZERO_STATE8_BLOCK; the results are zero_shard_adamw8_step's on each tensor.
+ * The list form takes the arrays with every call, 48 tensors a launch (the
+ * largest first, which changes no result). Errors: as
+ * zero_multi_tensor_adamw_step (ZERO_ERANGE for a tensor of 2^31 workgroups of
+ * 512 elements or more), and zero_shard_adamw8_step's on first_element.
+ * The table form is for fixed buffers. Create, step, free, blocks and the
+ * caller's duties as zero_mt_table_* (create: hipMalloc and a synchronous hipMemcpy on the
  * current device, once; 128 bytes per tensor and 4 per workgroup of 512
- * elements); the results are zero_shard_adamw8_step's on each tensor.
+ * elements).
  * Errors: as zero_mt_table_*, and zero_shard_adamw8_step's on first_element. */
+zero_status zero_multi_tensor_adamw8_step(float* const* masters, uint8_t* const* exp_avgs,
+                                          uint8_t* const* exp_avg_scales,
+                                          uint8_t* const* exp_avg_sqs,
+                                          uint8_t* const* exp_avg_sq_scales,
+                                          const uint16_t* const* grads, uint16_t* const* params_out,
+                                          const int64_t* numels, int32_t n_tensors,
+                                          int64_t first_element, int64_t step, double lr,
+                                          double beta1, double beta2, double eps,
+                                          double weight_decay, uint64_t seed,
+                                          const float* clip_scale, hipStream_t stream);
 typedef struct zero_mt8_table zero_mt8_table;
 zero_status zero_mt8_table_create(float* const* masters, uint8_t* const* exp_avgs,
                                   uint8_t* const* exp_avg_scales, uint8_t* const* exp_avg_sqs,

@@ -176,6 +176,7 @@ def test_non_finite_clip_skips(zm, coef):
     zm.zero_shard_adamw8_step(*d, to_dev_u16(g), out, 1, clip_scale=clip, **HP)
     table = zm.MultiTensor8Table(*[[x] for x in d], [to_dev_u16(g)], [out])
     table.step(1, clip_scale=clip, **HP)
+    zm.zero_multi_tensor_adamw8_step(*[[x] for x in d], [to_dev_u16(g)], [out], 1, clip_scale=clip, **HP)
     plan = zm.zero_partition_plan([n], 1, 1)
     grad_out = torch.zeros(n, dtype=torch.int16, device=dev())
     zm.zero_reduce_adamw8_step(plan, 0, [to_dev_u16(g)], 0, n, *d, out, 1, clip_scale=clip, shard_grad=grad_out, **HP)
@@ -211,7 +212,7 @@ def test_hyperparameter_corners(zm, case):
 
 def _ragged(zm, seed, misaligned):
     rng = np.random.default_rng(seed)
-    numels = [int(x) for x in np.exp(rng.uniform(0, np.log(20000), 30))] + [0, 1, 128, 129, 2048, 2049, 4096]
+    numels = [int(x) for x in np.exp(rng.uniform(0, np.log(20000), 70))] + [0, 1, 128, 129, 2048, 2049, 4096]
     states = [make_state(n, 1000 + k) if n else [np.zeros(0, np.float32)] + [np.zeros(0, np.uint8)] * 4
               for k, n in enumerate(numels)]
     grads = [make_grad(n, 2000 + k) for k, n in enumerate(numels)]
@@ -227,14 +228,18 @@ def _ragged(zm, seed, misaligned):
     return numels, states, grads, lists
 
 
+@pytest.mark.parametrize("form", ["list", "table"])
 @pytest.mark.parametrize("misaligned", [False, True])
-def test_table_step_matches_oracle_per_tensor(zm, misaligned):
+def test_many_tensors_match_oracle_per_tensor(zm, misaligned, form):
     numels, states, grads, lists = _ragged(zm, 30, misaligned)
     table = zm.MultiTensor8Table(*lists, first_element=256)
     assert table.blocks == sum(-(-n // 512) for n in numels)
     clip = torch.full((1,), 0.25, device=dev())
     for t in (1, 2):
-        table.step(t, seed=11, clip_scale=clip, **HP)
+        if form == "table":
+            table.step(t, seed=11, clip_scale=clip, **HP)
+        else:
+            zm.zero_multi_tensor_adamw8_step(*lists, t, seed=11, first_element=256, clip_scale=clip, **HP)
         first = 256
         for k, n in enumerate(numels):
             if n == 0:
@@ -267,6 +272,7 @@ def test_empty_table(zm):
     table = zm.MultiTensor8Table([], [], [], [], [], [], [])
     assert table.blocks == 0
     table.step(1, **HP)
+    zm.zero_multi_tensor_adamw8_step([], [], [], [], [], [], [], 1, **HP)
 
 
 @pytest.mark.parametrize("R,numels,n_ranks,align,rank,window,off", [

@@ -72,7 +72,7 @@ def _check_windows(state, out, held, windows, step, seed, first):
         assert sum(int(torch.count_nonzero(c)) for c in t.split(1 << 30)) == inside, "a code outside the windows changed"
 
 
-@pytest.mark.parametrize("form", ["flat", "table", "reduce"])
+@pytest.mark.parametrize("form", ["flat", "list", "table", "reduce"])
 def test_steps_past_2_32_elements(zm, form):
     n = (1 << 32) + 128 * 9 + 37
     _room(n * 10 + n // 64)
@@ -84,6 +84,8 @@ def test_steps_past_2_32_elements(zm, form):
     note(f"{form}, {n} elements")
     if form == "flat":
         zm.zero_shard_adamw8_step(*state, grad, out, 3, seed=4, first_element=first, **HP)
+    elif form == "list":
+        zm.zero_multi_tensor_adamw8_step(*[[t] for t in state], [grad], [out], 3, seed=4, first_element=first, **HP)
     elif form == "table":
         zm.MultiTensor8Table(*[[t] for t in state], [grad], [out], first_element=first).step(3, seed=4, **HP)
     else:

@@ -68,8 +68,12 @@ def _table(zm, rows, numels, first=0, n_tensors=None, null_list=None, out=True):
         lists[null_list] = None
     ns = (ctypes.c_int64 * max(T, 1))(*numels)
     h = ctypes.c_void_p()
-    st = zm._binding._mt8_create(*lists, ns, T if n_tensors is None else n_tensors, first,
-                                 ctypes.byref(h) if out else None)
+    count = T if n_tensors is None else n_tensors
+    listed = zm._binding._mt_adamw8(*lists, ns, count, first, 1, *HP, 0, None, None) if out else None
+    text = zm.zero_last_error()
+    st = zm._binding._mt8_create(*lists, ns, count, first, ctypes.byref(h) if out else None)
+    if out:                                             # the list form makes the same checks
+        assert listed == st and text.split(": ")[1:] == zm.zero_last_error().split(": ")[1:]
     if st == zm._binding.ZERO_OK:
         assert zm._binding._mt8_blocks(h) == 0
         assert zm._binding._mt8_step(h, 1, *HP, 0, None, None) == zm._binding.ZERO_OK     # nothing to do
@@ -92,6 +96,9 @@ def test_table_refusals(zm):
     assert _table(zm, [a, far], [1000, 1000], first=(1 << 63) - 1024) == R
     far[1] = far[0]
     assert _table(zm, [a, far], [1000, 1000]) == E and "overlaps" in zm.zero_last_error()
+    none = [None] * 8
+    assert zm._binding._mt_adamw8(*none, 0, 0, 0, *HP, 0, None, None) == E          # step < 1
+    assert zm._binding._mt_adamw8(*none, 0, 0, 1, *HP, 0, None, None) == zm._binding.ZERO_OK
     assert zm._binding._mt8_blocks(None) == -1
     assert zm._binding._mt8_step(None, 1, *HP, 0, None, None) == E
     assert zm._binding._mt8_step_sched(None, None, 0, None, None) == E

@@ -45,7 +45,8 @@ from ._binding import (LIB_PATH, ZERO_MAX_REPLICAS, AdamWSchedule, CopyTable,  #
                        zero_partition_plan_shard0, zero_host_adamw_step, zero_offload_adamw_step,
                        zero_multi_tensor_adamw_step,
                        zero_shard_adamw_step, zero_sqnorm_workspace_bytes, zero_status_string,
-                       ZERO_STATE8_BLOCK, MultiTensor8Table, state8_blocks, zero_reduce_adamw8_step,
+                       ZERO_STATE8_BLOCK, MultiTensor8Table, state8_blocks,
+                       zero_multi_tensor_adamw8_step, zero_reduce_adamw8_step,
                        zero_reduce_adamw8_step_scheduled, zero_shard_adamw8_step,
                        zero_shard_adamw8_step_scheduled, zero_state8_dequantize,
                        zero_state8_quantize)

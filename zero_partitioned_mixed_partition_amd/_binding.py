@@ -121,6 +121,8 @@ _adamw8 = _fn("zero_shard_adamw8_step", c_i32,
               [c_vp] * 7 + [c_i64, c_i64, c_i64, c_dbl, c_dbl, c_dbl, c_dbl, c_dbl, c_u64, c_vp, c_vp])
 _adamw8_sched = _fn("zero_shard_adamw8_step_scheduled", c_i32,
                     [c_vp] * 7 + [c_i64, c_i64, c_vp, c_u64, c_vp, c_vp])
+_mt_adamw8 = _fn("zero_multi_tensor_adamw8_step", c_i32,
+                 [c_vp] * 8 + [c_i32, c_i64, c_i64, c_dbl, c_dbl, c_dbl, c_dbl, c_dbl, c_u64, c_vp, c_vp])
 _mt8_create = _fn("zero_mt8_table_create", c_i32, [c_vp] * 8 + [c_i32, c_i64, ctypes.POINTER(c_vp)])
 _mt8_free = _fn("zero_mt8_table_free", None, [c_vp])
 _mt8_blocks = _fn("zero_mt8_table_blocks", c_i64, [c_vp])
@@ -1009,6 +1011,44 @@ def zero_shard_adamw8_step_scheduled(master, exp_avg, exp_avg_scale, exp_avg_sq,
                                         param_out, schedule, seed, first_element, clip_scale, stream)()
 
 
+def _state8_lists(lists):
+    """The seven pointer arrays and the element counts of a list of tensors."""
+    T = len(lists[0])
+    if any(len(x) != T for x in lists):
+        raise ValueError("the seven lists must have the same length")
+    rows = [_state8_ptrs(x[0].numel(), x) for x in zip(*lists)]
+    tabs = [(c_vp * max(T, 1))(*[row[k] for row in rows]) for k in range(7)]
+    return tabs, (c_i64 * max(T, 1))(*[t.numel() for t in lists[0]]), T
+
+
+def prepare_multi_tensor_adamw8_step(masters, exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_scales, grads,
+                                     params_out, lr: float, beta1: float, beta2: float, eps: float,
+                                     weight_decay: float, seed: int = 0, first_element: int = 0, clip_scale=None,
+                                     stream=None) -> Prepared:
+    """Lists of T device tensors, tensor t updated over masters[t].numel() elements. Call the result with the
+    step."""
+    lists = (masters, exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_scales, grads, params_out)
+    tabs, ns, T = _state8_lists(lists)
+    _need(clip_scale, 1, "clip_scale")
+    p = Prepared(_mt_adamw8, tabs + [ns, T, first_element, 1, lr, beta1, beta2, eps, weight_decay, _seed(seed),
+                                     _ptr(clip_scale, 4, "clip_scale"),
+                                     _stream(stream, masters[0]) if T else (stream or 0)],
+                 "zero_multi_tensor_adamw8_step", step_index=10)
+    p._keep = (lists, tabs, ns, clip_scale)
+    return p
+
+
+def zero_multi_tensor_adamw8_step(masters, exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_scales, grads,
+                                  params_out, step: int, lr: float, beta1: float, beta2: float, eps: float,
+                                  weight_decay: float, seed: int = 0, first_element: int = 0, clip_scale=None,
+                                  stream=None) -> None:
+    """zero_shard_adamw8_step over a ragged list of tensors (buffers that move from step to step; a fixed list
+    goes through MultiTensor8Table)."""
+    prepare_multi_tensor_adamw8_step(masters, exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_scales, grads,
+                                     params_out, lr, beta1, beta2, eps, weight_decay, seed, first_element,
+                                     clip_scale, stream)(step)
+
+
 class MultiTensor8Table:
     """Owner of a zero_mt8_table: a fixed list of per-parameter tensors with their moments in 8 bits,
     described once in device memory (on the current device), stepped in one launch. The tensors are held
@@ -1017,12 +1057,7 @@ class MultiTensor8Table:
     def __init__(self, masters, exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_scales, grads, params_out,
                  first_element: int = 0):
         lists = (masters, exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_scales, grads, params_out)
-        T = len(masters)
-        if any(len(x) != T for x in lists):
-            raise ValueError("the seven lists must have the same length")
-        rows = [_state8_ptrs(x[0].numel(), x) for x in zip(*lists)]
-        tabs = [(c_vp * max(T, 1))(*[row[k] for row in rows]) for k in range(7)]
-        ns = (c_i64 * max(T, 1))(*[t.numel() for t in masters])
+        tabs, ns, T = _state8_lists(lists)
         h = c_vp()
         _check(_mt8_create(*tabs, ns, T, first_element, ctypes.byref(h)), "zero_mt8_table_create")
         self._h = h

@@ -15,10 +15,11 @@
 // of 128.
 //
 // Bound: HBM. With the moments at a byte, the bytes fall from 28 to 16 while the
-// arithmetic grows, to about 90 vector issue slots an element (45 of them the
-// IEEE square root and two divisions), against the 100 that fit beside the
-// memory time; the conversions in one instruction each are what keeps the sum
-// under it. Four elements a lane: with 8 a lane's two 16-byte stores of the
+// arithmetic grows, to 79 vector instructions an element by the counters (some 45
+// issue slots of them the IEEE square root and two divisions), where the memory
+// time leaves room for about 97; the conversions in one instruction each are
+// what keeps the sum under it. (A square root and reciprocal of 1 ulp in their
+// place gain nothing: 316 us against 312.) Four elements a lane: with 8 a lane's two 16-byte stores of the
 // master leave half-written lines behind each other and the write-through stores
 // fell to 3.1 TB/s (662 us at 125 M elements); with 2 the random words, shared
 // by 8 elements, are computed four times over (about 400 us). Measured: 125 M
@@ -275,6 +276,35 @@ __global__ __launch_bounds__(kThreads) void adamw8_table_kernel(const Desc* __re
         update_chunk<false>(d.a, d.n, base, d.first, step.scalars(), step.random_key(), clip_scale);
 }
 
+// The list form, for buffers that move from step to step: the descriptors
+// travel in the kernel arguments, and a workgroup finds its tensor by a binary
+// search over the tensors' first workgroups.
+constexpr int kListTensors = 48;
+struct ListBatch {
+    Arrays a[kListTensors];
+    int64_t n[kListTensors];
+    int64_t first[kListTensors];
+    int32_t first_block[kListTensors + 1];
+    int32_t count;
+    uint64_t vec;                          // bit k: tensor k takes vector accesses
+};
+static_assert(sizeof(ListBatch) + sizeof(CallStep) + sizeof(float*) <= 4096, "kernel arguments are limited to 4 KB");
+
+__global__ __launch_bounds__(kThreads) void adamw8_list_kernel(ListBatch b, CallStep step,
+                                                               const float* __restrict__ clip_scale) {
+    const int32_t blk = static_cast<int32_t>(blockIdx.x);
+    int lo = 0, hi = b.count - 1;          // k with first_block[k] <= blk < first_block[k + 1]
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (b.first_block[mid] <= blk) lo = mid; else hi = mid - 1;
+    }
+    const int64_t base = static_cast<int64_t>(blk - b.first_block[lo]) * kChunk;
+    if ((b.vec >> lo) & 1u)
+        update_chunk<true>(b.a[lo], b.n[lo], base, b.first[lo], step.c, step.key, clip_scale);
+    else
+        update_chunk<false>(b.a[lo], b.n[lo], base, b.first[lo], step.c, step.key, clip_scale);
+}
+
 // The reduce and the update in one pass: the averaged gradient is the
 // reduce's (fp32 sum in replica order, one division by R, one rounding to
 // bf16), used where it is formed.
@@ -471,6 +501,16 @@ std::string array_clash(const Arrays& a, int64_t n) {
     return zero::first_overlap(wr, 6, rd, 1);
 }
 
+// The step's scalars and key of a call that counts the steps itself.
+zero_status call_step(int64_t step, double lr, double beta1, double beta2, double eps, double weight_decay,
+                      uint64_t seed, CallStep* out, const char* who) {
+    zero_status st = zero::adam::check_hyper(step, lr, beta1, beta2, eps, weight_decay, who);
+    if (st != ZERO_OK) return st;
+    st = zero::adam::step_scalars(step, lr, beta1, beta2, weight_decay, eps, &out->c, who);
+    out->key = zero::state8::step_key(seed, static_cast<uint64_t>(step));
+    return st;
+}
+
 bool any_null(const Arrays& a) { return !a.p || !a.m || !a.ms || !a.v || !a.vs || !a.g || !a.o; }
 
 template <typename Step>
@@ -503,12 +543,9 @@ extern "C" zero_status zero_shard_adamw8_step(float* master, uint8_t* exp_avg, u
     static const char* const who = "zero_shard_adamw8_step";
     zero::clear_error();
     if (n < 0) return zero::fail(ZERO_EINVAL, "zero_shard_adamw8_step: n < 0");
-    zero_status st = zero::adam::check_hyper(step, lr, beta1, beta2, eps, weight_decay, who);
-    if (st != ZERO_OK) return st;
     CallStep s{};
-    st = zero::adam::step_scalars(step, lr, beta1, beta2, weight_decay, eps, &s.c, who);
+    const zero_status st = call_step(step, lr, beta1, beta2, eps, weight_decay, seed, &s, who);
     if (st != ZERO_OK) return st;
-    s.key = zero::state8::step_key(seed, static_cast<uint64_t>(step));
     return launch_flat(Arrays{master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad, param_out}, n,
                        first_element, s, clip_scale, stream, who);
 }
@@ -528,7 +565,94 @@ extern "C" zero_status zero_shard_adamw8_step_scheduled(float* master, uint8_t* 
                        first_element, ScheduleStep{schedule->state, seed}, clip_scale, stream, who);
 }
 
-// ------------------------------------------------------------ device table
+// ------------------------------------------------------------ many tensors
+
+namespace {
+
+// The checks of a list, and one descriptor per non-empty tensor in list order
+// (first_block is the caller's to fill). Throws std::bad_alloc.
+zero_status describe_list(float* const* masters, uint8_t* const* exp_avgs, uint8_t* const* exp_avg_scales,
+                          uint8_t* const* exp_avg_sqs, uint8_t* const* exp_avg_sq_scales,
+                          const uint16_t* const* grads, uint16_t* const* params_out, const int64_t* numels,
+                          int32_t n_tensors, int64_t first_element, std::vector<Desc>* descs, const char* who) {
+    using zero::fail;
+    const std::string w(who);
+    if (n_tensors < 0) return fail(ZERO_EINVAL, w + ": n_tensors < 0");
+    if (n_tensors > 0 && (!masters || !exp_avgs || !exp_avg_scales || !exp_avg_sqs || !exp_avg_sq_scales || !grads ||
+                          !params_out || !numels))
+        return fail(ZERO_EINVAL, w + ": NULL array of pointers");
+    const zero_status st = check_first(first_element, 0, who);
+    if (st != ZERO_OK) return st;
+    int64_t first = first_element;
+    for (int32_t t = 0; t < n_tensors; ++t) {
+        const int64_t n = numels[t];
+        const std::string of = " of tensor " + std::to_string(t);
+        if (n < 0) return fail(ZERO_EINVAL, w + ": numel < 0" + of);
+        if (n == 0) continue;
+        if ((n - 1) / kChunk + 1 > 0x7FFFFFFF) return fail(ZERO_ERANGE, w + ": more than 2^31 workgroups" + of);
+        const int64_t padded = zero::state8::blocks_of(n) * kBlock;
+        if (padded > INT64_MAX - first) return fail(ZERO_ERANGE, w + ": first_element + n overflows" + of);
+        Desc d{};
+        d.a = Arrays{masters[t], exp_avgs[t], exp_avg_scales[t], exp_avg_sqs[t], exp_avg_sq_scales[t], grads[t],
+                     params_out[t]};
+        if (any_null(d.a)) return fail(ZERO_EINVAL, w + ": NULL array" + of);
+        const std::string clash = array_clash(d.a, n);
+        if (!clash.empty()) return fail(ZERO_EINVAL, w + ": " + clash + of);
+        d.n = n;
+        d.first = first;
+        d.vec = vector_ok(d.a);
+        descs->push_back(d);
+        first += padded;
+    }
+    return ZERO_OK;
+}
+
+}  // namespace
+
+extern "C" zero_status zero_multi_tensor_adamw8_step(float* const* masters, uint8_t* const* exp_avgs,
+                                                     uint8_t* const* exp_avg_scales, uint8_t* const* exp_avg_sqs,
+                                                     uint8_t* const* exp_avg_sq_scales, const uint16_t* const* grads,
+                                                     uint16_t* const* params_out, const int64_t* numels,
+                                                     int32_t n_tensors, int64_t first_element, int64_t step, double lr,
+                                                     double beta1, double beta2, double eps, double weight_decay,
+                                                     uint64_t seed, const float* clip_scale, hipStream_t stream) {
+    static const char* const who = "zero_multi_tensor_adamw8_step";
+    zero::clear_error();
+    CallStep s{};
+    zero_status st = call_step(step, lr, beta1, beta2, eps, weight_decay, seed, &s, who);
+    if (st != ZERO_OK) return st;
+    std::vector<Desc> descs;
+    try {
+        st = describe_list(masters, exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_scales, grads, params_out, numels,
+                           n_tensors, first_element, &descs, who);
+        if (st != ZERO_OK) return st;
+        // Largest first, as the 32-bit list: the many small tensors then share a launch.
+        std::stable_sort(descs.begin(), descs.end(), [](const Desc& x, const Desc& y) { return x.n > y.n; });
+    } catch (const std::bad_alloc&) {
+        return zero::fail(ZERO_ENOMEM, "zero_multi_tensor_adamw8_step: host allocation failed");
+    }
+    for (size_t at = 0; at < descs.size();) {
+        ListBatch b{};
+        while (at < descs.size() && b.count < kListTensors) {
+            const int k = b.count;
+            const int64_t end = b.first_block[k] + ((descs[at].n - 1) / kChunk + 1);
+            if (end > zero::kTableLaunchBlocks && k > 0) break;          // fewer than 2^32 work-items a launch
+            if (end > 0x7FFFFFFF) return zero::fail(ZERO_ERANGE, "zero_multi_tensor_adamw8_step: tensor too large");
+            b.a[k] = descs[at].a;
+            b.n[k] = descs[at].n;
+            b.first[k] = descs[at].first;
+            b.vec |= static_cast<uint64_t>(descs[at].vec != 0) << k;
+            b.first_block[k + 1] = static_cast<int32_t>(end);
+            ++b.count;
+            ++at;
+        }
+        hipLaunchKernelGGL(adamw8_list_kernel, dim3(static_cast<unsigned>(b.first_block[b.count])), dim3(kThreads), 0,
+                           stream, b, s, clip_scale);
+        st = zero::check_hip(hipGetLastError(), who);
+        if (st != ZERO_OK) return st;
+    }
+    return ZERO_OK;
+}
 
 struct zero_mt8_table {
     int device = -1;
@@ -549,40 +673,21 @@ extern "C" zero_status zero_mt8_table_create(float* const* masters, uint8_t* con
     const std::string w(who);
     if (!out) return fail(ZERO_EINVAL, w + ": NULL out");
     *out = nullptr;
-    if (n_tensors < 0) return fail(ZERO_EINVAL, w + ": n_tensors < 0");
-    if (n_tensors > 0 && (!masters || !exp_avgs || !exp_avg_scales || !exp_avg_sqs || !exp_avg_sq_scales || !grads ||
-                          !params_out || !numels))
-        return fail(ZERO_EINVAL, w + ": NULL array of pointers");
-    zero_status st = check_first(first_element, 0, who);
-    if (st != ZERO_OK) return st;
+    zero_status st = ZERO_OK;
     std::vector<Desc> descs;
     std::vector<uint32_t> index;
     zero_mt8_table* tab = nullptr;
     try {
-        int64_t blocks = 0, first = first_element;
-        for (int32_t t = 0; t < n_tensors; ++t) {
-            const int64_t n = numels[t];
-            const std::string of = " of tensor " + std::to_string(t);
-            if (n < 0) return fail(ZERO_EINVAL, w + ": numel < 0" + of);
-            if (n == 0) continue;
-            const int64_t wgs = (n - 1) / kChunk + 1;
+        st = describe_list(masters, exp_avgs, exp_avg_scales, exp_avg_sqs, exp_avg_sq_scales, grads, params_out, numels,
+                           n_tensors, first_element, &descs, who);
+        if (st != ZERO_OK) return st;
+        int64_t blocks = 0;
+        for (size_t k = 0; k < descs.size(); ++k) {
+            const int64_t wgs = (descs[k].n - 1) / kChunk + 1;
             if (blocks + wgs > 0x7FFFFFFF) return fail(ZERO_ERANGE, w + ": more than 2^31 workgroups in one list");
-            const int64_t padded = zero::state8::blocks_of(n) * kBlock;
-            if (padded > INT64_MAX - first) return fail(ZERO_ERANGE, w + ": first_element + n overflows" + of);
-            Desc d{};
-            d.a = Arrays{masters[t], exp_avgs[t], exp_avg_scales[t], exp_avg_sqs[t], exp_avg_sq_scales[t], grads[t],
-                         params_out[t]};
-            if (any_null(d.a)) return fail(ZERO_EINVAL, w + ": NULL array" + of);
-            const std::string clash = array_clash(d.a, n);
-            if (!clash.empty()) return fail(ZERO_EINVAL, w + ": " + clash + of);
-            d.n = n;
-            d.first = first;
-            d.first_block = blocks;
-            d.vec = vector_ok(d.a);
-            index.insert(index.end(), static_cast<size_t>(wgs), static_cast<uint32_t>(descs.size()));
-            descs.push_back(d);
+            descs[k].first_block = blocks;
+            index.insert(index.end(), static_cast<size_t>(wgs), static_cast<uint32_t>(k));
             blocks += wgs;
-            first += padded;
         }
         if (blocks > 0) index = zero::xcd_major_index(index);
         tab = new zero_mt8_table;
@@ -658,15 +763,12 @@ extern "C" zero_status zero_mt8_table_adamw8_step(const zero_mt8_table* table, i
     static const char* const who = "zero_mt8_table_adamw8_step";
     zero::clear_error();
     if (!table) return zero::fail(ZERO_EINVAL, "zero_mt8_table_adamw8_step: NULL table");
-    zero_status st = zero::adam::check_hyper(step, lr, beta1, beta2, eps, weight_decay, who);
-    if (st != ZERO_OK) return st;
     CallStep s{};
-    st = zero::adam::step_scalars(step, lr, beta1, beta2, weight_decay, eps, &s.c, who);
+    zero_status st = call_step(step, lr, beta1, beta2, eps, weight_decay, seed, &s, who);
     if (st != ZERO_OK) return st;
     if (table->blocks == 0) return ZERO_OK;
     st = check_table_device(table, who);
     if (st != ZERO_OK) return st;
-    s.key = zero::state8::step_key(seed, static_cast<uint64_t>(step));
     return launch_table(table, s, clip_scale, stream, who);
 }
 
@@ -752,12 +854,9 @@ extern "C" zero_status zero_reduce_adamw8_step(const zero_plan* plan, int32_t ra
                                                const float* clip_scale, hipStream_t stream) {
     static const char* const who = "zero_reduce_adamw8_step";
     zero::clear_error();
-    zero_status st = zero::adam::check_hyper(step, lr, beta1, beta2, eps, weight_decay, who);
-    if (st != ZERO_OK) return st;
     CallStep s{};
-    st = zero::adam::step_scalars(step, lr, beta1, beta2, weight_decay, eps, &s.c, who);
+    const zero_status st = call_step(step, lr, beta1, beta2, eps, weight_decay, seed, &s, who);
     if (st != ZERO_OK) return st;
-    s.key = zero::state8::step_key(seed, static_cast<uint64_t>(step));
     return launch_reduce(plan, rank, replicas, n_replicas, begin, count,
                          Arrays{master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, nullptr, param_out},
                          shard_grad, first_element, s, clip_scale, stream, who);
