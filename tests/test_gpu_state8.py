@@ -521,3 +521,26 @@ def test_captured_rank_step(zm):
         for x, y in zip(both[0].tensors, both[1].tensors):
             assert torch.equal(x, y)
     assert both[1].steps_applied() == 5
+
+
+@pytest.mark.parametrize("cut", [4096 - 64, 4096, 4096 + 128])
+def test_rank_step_windows_give_the_whole_steps_bits(zm, cut):
+    """Two bucket windows that meet inside the rank's shard, between blocks (one pass per window) and inside a
+    block (the two calls), against one window over the whole buffer."""
+    from zero_partitioned_mixed_partition_amd.step import Hyper, RankStep
+    plan = zm.zero_partition_plan([9000], 2, 128)                # S = 4608, rank 0
+    P, S = plan.padded_numel, plan.shard_numel
+    reps = [to_dev_u16(make_grad(P, 90 + k)) for k in range(2)]
+    state = make_state(S, 92)
+    results = []
+    for windows in ([(0, P, reps)], [(cut, P - cut, [r[cut:] for r in reps]), (0, cut, [r[:cut] for r in reps])]):
+        rs = RankStep(plan, 0, len(windows), Hyper(), 0.0, dev(), state_bits=8, seed=5)
+        assert rs._whole_blocks(windows) == (len(windows) == 1 or cut % 128 == 0)
+        for d, h in zip((rs.master, rs.exp_avg, rs.exp_avg_scale, rs.exp_avg_sq, rs.exp_avg_sq_scale), state):
+            d.copy_(torch.from_numpy(h))
+        for _ in range(2):
+            rs.step(windows)
+        torch.cuda.synchronize()
+        results.append([rs.master, rs.exp_avg, rs.exp_avg_scale, rs.exp_avg_sq, rs.exp_avg_sq_scale] + rs.tensors)
+    for x, y in zip(*results):
+        assert torch.equal(x, y)

@@ -255,6 +255,10 @@ def _stream(stream, tensor) -> int:
     if stream is not None:
         return int(stream)
     import torch
+    # the stream's handle without a Stream object around it (2 us less per call), where torch has the call
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None and tensor.device.index is not None:
+        return raw(tensor.device.index)
     return torch.cuda.current_stream(tensor.device).cuda_stream
 
 
@@ -941,16 +945,19 @@ def state8_blocks(n: int) -> int:
     return -(-n // ZERO_STATE8_BLOCK)
 
 
-_STATE8 = (("master", 4), ("exp_avg", 1), ("exp_avg_scale", 1), ("exp_avg_sq", 1), ("exp_avg_sq_scale", 1),
-           ("grad", 2), ("param_out", 2))
+_STATE8 = (("master", 4, False), ("exp_avg", 1, False), ("exp_avg_scale", 1, True), ("exp_avg_sq", 1, False),
+           ("exp_avg_sq_scale", 1, True), ("grad", 2, False), ("param_out", 2, False))
 
 
 def _state8_ptrs(n: int, tensors) -> List[int]:
-    """The pointers of an 8-bit update's seven tensors over n elements (None where the call takes none)."""
+    """The pointers of an 8-bit update's seven tensors over n elements (None where the call takes none). The
+    checks are _need's and _ptr's, called only where one fails: their calls cost more than the launch's arguments."""
     blocks = state8_blocks(n)
-    for t, (what, _) in zip(tensors, _STATE8):
-        _need(t, blocks if what.endswith("scale") else n, what)
-    return [_ptr(t, size, what) for t, (what, size) in zip(tensors, _STATE8)]
+    for t, (what, _, scale) in zip(tensors, _STATE8):
+        if t is not None and t.numel() < (blocks if scale else n):
+            _need(t, blocks if scale else n, what)
+    return [t.data_ptr() if t is not None and t.is_cuda and t.element_size() == size and t.is_contiguous()
+            else _ptr(t, size, what) for t, (what, size, _) in zip(tensors, _STATE8)]
 
 
 def _seed(seed: int) -> int:
@@ -1116,12 +1123,13 @@ class MultiTensor8Table:
 def _reduce8_args(plan: Plan, rank: int, replicas, begin: int, count: int, arrays, param_out, shard_grad,
                   clip_scale):
     """The arguments up to shard_grad of zero_reduce_adamw8_step; the state arrays are the rank's shard ([S])."""
+    S = plan.shard_numel
     for r in replicas:
         _need(r, count, "a replica")
-    _need(shard_grad, plan.shard_numel, "shard_grad")
+    _need(shard_grad, S, "shard_grad")
     _need(clip_scale, 1, "clip_scale")
     ptrs = (c_vp * max(len(replicas), 1))(*[_ptr(r, 2, "replica") for r in replicas])
-    state = _state8_ptrs(plan.shard_numel, (*arrays, None, param_out))
+    state = _state8_ptrs(S, (*arrays, None, param_out))
     return [plan.handle, rank, ptrs, len(replicas), begin, count] + state[:5] + [
         state[6], _ptr(shard_grad, 2, "shard_grad")]
 
@@ -1146,9 +1154,11 @@ def zero_reduce_adamw8_step(plan: Plan, rank: int, replicas: Sequence, begin: in
                             first_element: int = 0, clip_scale=None, shard_grad=None, stream=None) -> None:
     """The rank's averaged gradient and its 8-bit AdamW update in one pass: the bits of zero_grad_reduce_shard
     then zero_shard_adamw8_step. The window's part of the shard starts and ends at whole blocks of 128."""
-    prepare_reduce_adamw8_step(plan, rank, replicas, begin, count, master, exp_avg, exp_avg_scale, exp_avg_sq,
-                               exp_avg_sq_scale, param_out, lr, beta1, beta2, eps, weight_decay, seed,
-                               first_element, clip_scale, shard_grad, stream)(step)
+    args = _reduce8_args(plan, rank, replicas, begin, count,
+                         (master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale), param_out, shard_grad,
+                         clip_scale)
+    _check(_reduce_adamw8(*args, first_element, step, lr, beta1, beta2, eps, weight_decay, _seed(seed),
+                          _ptr(clip_scale, 4, "clip_scale"), _stream(stream, master)), "zero_reduce_adamw8_step")
 
 
 def prepare_reduce_adamw8_step_scheduled(plan: Plan, rank: int, replicas: Sequence, begin: int, count: int, master,
