@@ -24,6 +24,8 @@ Pinning status (what each function is checked against, outside itself):
   gather.py   flatten/gather round trip
   flatten.py  gather(flatten(x)) = x, padding zero, hand-worked case
   Shard(0)    torch.chunk's row cut, round trips, hand-worked case
+  state8.py   torch's e4m3 and e8m0 conversions, the mean over all draws, a
+              pure-Python count of the random words, the 32-bit step
 The fp32 evaluation order inside AdamW and the clip's 1e-6 guard are readings
 (the pages do not write the update out); they are pinned by the closed forms
 and the torch cross-check within tolerance, not bit for bit by the pages.
