@@ -515,7 +515,8 @@ zero_status zero_mt_table_adamw_step_scheduled(const zero_mt_table* table,
  * The update per element is zero_shard_adamw_step's, in its order, on the
  * decoded m and v: the new fp32 m and v update p, and then are encoded.
  * Accesses: any pointer alignment; with master 16-byte, codes 4-byte, grad and
- * param_out 8-byte aligned the vector path runs, with identical results.
+ * param_out 8-byte aligned (the usual case) a call is fastest; the results are
+ * the same at any.
  *
  * zero_shard_adamw8_step
  * master       device [n] fp32, updated in place.

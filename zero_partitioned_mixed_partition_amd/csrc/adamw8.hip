@@ -19,11 +19,11 @@
 // issue slots of them the IEEE square root and two divisions), where the memory
 // time leaves room for about 97; the conversions in one instruction each are
 // what keeps the sum under it. (A square root and reciprocal of 1 ulp in their
-// place gain nothing: 316 us against 312.) Four elements a lane: with 8 a lane's two 16-byte stores of the
-// master leave half-written lines behind each other and the write-through stores
-// fell to 3.1 TB/s (662 us at 125 M elements); with 2 the random words, shared
-// by 8 elements, are computed four times over (about 400 us). Measured: 125 M
-// elements 312 us, 6.45 TB/s (a 1 GB copy: 6.55).
+// place gain nothing: 316 us against 312.) Four elements a lane: with 8 a lane's
+// two 16-byte stores of the master leave half-written lines behind each other
+// and the write-through stores fell to 3.1 TB/s (662 us at 125 M elements); with
+// 2 the random words, shared by 8 elements, are computed four times over (about
+// 400 us). Measured: 125 M elements 312 us, 6.45 TB/s (a 1 GB copy: 6.55).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -113,18 +113,63 @@ struct Lane {
     int live = 0;                          // elements below n
 };
 
+// A lane's accesses of four elements. VEC: every array is aligned to them, and
+// stores write through. Otherwise the same widths at any alignment (the types
+// claim none beyond the element's, and the hardware takes them), with
+// non-temporal stores, whose lines the L2 completes. Measured on MI355X, 125 M
+// elements: 427 us with every array one element off (312 aligned), and 740
+// element by element.
+template <typename T> struct Four;         // the four elements of an access
+template <> struct Four<float> { typedef f32x4 type; };
+template <> struct Four<uint16_t> { typedef u32x2 type; };
+template <> struct Four<uint8_t> { typedef uint32_t type; };
+__device__ __forceinline__ f32x4 load_any(const float* p) {
+    typedef f32x4 any __attribute__((aligned(4)));
+    return __builtin_nontemporal_load(reinterpret_cast<const any*>(p));
+}
+__device__ __forceinline__ u32x2 load_any(const uint16_t* p) {
+    typedef u32x2 any __attribute__((aligned(2)));
+    return __builtin_nontemporal_load(reinterpret_cast<const any*>(p));
+}
+__device__ __forceinline__ uint32_t load_any(const uint8_t* p) {
+    typedef uint32_t any __attribute__((aligned(1)));
+    return __builtin_nontemporal_load(reinterpret_cast<const any*>(p));
+}
+__device__ __forceinline__ void store_any(float* p, f32x4 v) {
+    typedef f32x4 any __attribute__((aligned(4)));
+    __builtin_nontemporal_store(v, reinterpret_cast<any*>(p));
+}
+__device__ __forceinline__ void store_any(uint16_t* p, u32x2 v) {
+    typedef u32x2 any __attribute__((aligned(2)));
+    __builtin_nontemporal_store(v, reinterpret_cast<any*>(p));
+}
+__device__ __forceinline__ void store_any(uint8_t* p, uint32_t v) {
+    typedef uint32_t any __attribute__((aligned(1)));
+    __builtin_nontemporal_store(v, reinterpret_cast<any*>(p));
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ typename Four<T>::type load4(const T* p) {
+    if (VEC) return zero::dev::ld_stream(reinterpret_cast<const typename Four<T>::type*>(p));
+    return load_any(p);
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store4(T* base, uint32_t t, const typename Four<T>::type& v) {
+    if (VEC)
+        zero::dev::st_stream_at(base, sizeof(T) * t, v);
+    else
+        store_any(base + t, v);
+}
+
 // In everything below, the arrays start at the workgroup's chunk (the same
 // pointers in every lane) and t is the lane's first element in it, so that a
-// wave addresses an array by a scalar base and a 32-bit offset.
-//
-// VEC: every array allows accesses of kEpt elements. Lanes with fewer than
-// kEpt elements left, and all lanes where VEC does not hold, go one by one.
+// wave addresses an array by a scalar base and a 32-bit offset. Lanes with
+// fewer than kEpt elements left go one by one.
 template <bool VEC>
 __device__ __forceinline__ void load_state(Lane& l, const Arrays& a, uint32_t t) {
-    if (VEC && l.live == kEpt) {
-        const f32x4 x = zero::dev::ld_stream(reinterpret_cast<const f32x4*>(a.p + t));
-        l.m = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(a.m + t));
-        l.v = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(a.v + t));
+    if (l.live == kEpt) {
+        const f32x4 x = load4<VEC>(a.p + t);
+        l.m = load4<VEC>(a.m + t);
+        l.v = load4<VEC>(a.v + t);
 #pragma unroll
         for (int k = 0; k < kEpt; ++k) l.p[k] = x[k];
     } else {
@@ -147,8 +192,8 @@ template <bool VEC>
 __device__ __forceinline__ void load_grad(float (&g)[kEpt], const uint16_t* grad, int live, uint32_t t) {
 #pragma unroll
     for (int k = 0; k < kEpt; ++k) g[k] = 0.0f;
-    if (VEC && live == kEpt) {
-        const u32x2 x = zero::dev::ld_stream(reinterpret_cast<const u32x2*>(grad + t));
+    if (live == kEpt) {
+        const u32x2 x = load4<VEC>(grad + t);
         g[0] = zero::dev::lo_bf16(x[0]);
         g[1] = zero::dev::hi_bf16(x[0]);
         g[2] = zero::dev::lo_bf16(x[1]);
@@ -188,12 +233,12 @@ __device__ __forceinline__ void update_and_store(Lane& l, const float (&g)[kEpt]
         a.ms[t / kBlock] = static_cast<uint8_t>(ms);
         a.vs[t / kBlock] = static_cast<uint8_t>(vs);
     }
-    if (VEC && l.live == kEpt) {
-        zero::dev::st_stream_at(a.p, 4 * t, f32x4{l.p[0], l.p[1], l.p[2], l.p[3]});
-        zero::dev::st_stream_at(a.m, t, mw);
-        zero::dev::st_stream_at(a.v, t, vw);
-        zero::dev::st_stream_at(a.o, 2 * t,
-                                u32x2{zero::dev::pack_bf16(l.p[0], l.p[1]), zero::dev::pack_bf16(l.p[2], l.p[3])});
+    if (l.live == kEpt) {
+        store4<VEC>(a.p, t, f32x4{l.p[0], l.p[1], l.p[2], l.p[3]});
+        store4<VEC>(a.m, t, mw);
+        store4<VEC>(a.v, t, vw);
+        store4<VEC>(a.o, t, u32x2{zero::dev::pack_bf16(l.p[0], l.p[1]),
+                                              zero::dev::pack_bf16(l.p[2], l.p[3])});
     } else {
 #pragma unroll
         for (int k = 0; k < kEpt; ++k) {
@@ -328,13 +373,18 @@ template <bool VEC, int B>
 __device__ __forceinline__ void mean_grad(float (&g)[kEpt], const Replicas& reps, int n_rep, int64_t src_off,
                                           int live, uint32_t t) {
     float acc[kEpt] = {};
-    if (VEC && live == kEpt) {
-        zero::dev::for_replicas<B, u32x2>(reps.p, n_rep, src_off, t / kEpt, [&](u32x2 x) {
+    if (live == kEpt) {
+        const auto add = [&](u32x2 x) {
             acc[0] = acc[0] + zero::dev::lo_bf16(x[0]);
             acc[1] = acc[1] + zero::dev::hi_bf16(x[0]);
             acc[2] = acc[2] + zero::dev::lo_bf16(x[1]);
             acc[3] = acc[3] + zero::dev::hi_bf16(x[1]);
-        });
+        };
+        if (VEC) {
+            zero::dev::for_replicas<B, u32x2>(reps.p, n_rep, src_off, t / kEpt, add);
+        } else {
+            for (int r = 0; r < n_rep; ++r) add(load4<false>(reps.p[r] + src_off + t));
+        }
     } else if (live > 0) {
         for (int r = 0; r < n_rep; ++r) {
             const uint16_t* p = reps.p[r] + src_off;
@@ -364,8 +414,8 @@ __global__ __launch_bounds__(kThreads) void reduce_adamw8_kernel(Replicas reps, 
     mean_grad<VEC, B>(g, reps, n_rep, src_off + base, l.live, t);
     if (grad_out != nullptr) {
         uint16_t* const out = grad_out + base;
-        if (VEC && l.live == kEpt) {
-            zero::dev::st_stream_at(out, 2 * t, u32x2{zero::dev::pack_bf16(g[0], g[1]), zero::dev::pack_bf16(g[2], g[3])});
+        if (l.live == kEpt) {
+            store4<VEC>(out, t, u32x2{zero::dev::pack_bf16(g[0], g[1]), zero::dev::pack_bf16(g[2], g[3])});
         } else {
 #pragma unroll
             for (int k = 0; k < kEpt; ++k)
@@ -398,8 +448,8 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const float* __restr
     for (int r = 0; r < kQuantizeRows; ++r) {
         const float* const from_x = x + base + r * kChunk;
         live[r] = lane_live(chunk_left(n, base + r * kChunk), t);
-        if (VEC && live[r] == kEpt) {
-            const f32x4 q = zero::dev::ld_stream(reinterpret_cast<const f32x4*>(from_x + t));
+        if (live[r] == kEpt) {
+            const f32x4 q = load4<VEC>(from_x + t);
 #pragma unroll
             for (int k = 0; k < kEpt; ++k) v[r][k] = q[k];
         } else {
@@ -416,8 +466,8 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const float* __restr
         if (second) w = zero::state8::positive4(w, v[r], byte);
         uint8_t* const to = codes + base + r * kChunk;
         if (t % kBlock == 0) scales[(base + r * kChunk) / kBlock + t / kBlock] = static_cast<uint8_t>(byte);
-        if (VEC && live[r] == kEpt) {
-            zero::dev::st_stream_at(to, t, w);
+        if (live[r] == kEpt) {
+            store4<VEC>(to, t, w);
         } else {
 #pragma unroll
             for (int k = 0; k < kEpt; ++k)
@@ -439,8 +489,8 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __r
         const uint8_t* const from_c = codes + base + r * kChunk;
         live[r] = lane_live(chunk_left(n, base + r * kChunk), t);
         if (live[r] > 0) byte[r] = scales[(base + r * kChunk) / kBlock + t / kBlock];
-        if (VEC && live[r] == kEpt) {
-            w[r] = zero::dev::ld_stream(reinterpret_cast<const uint32_t*>(from_c + t));
+        if (live[r] == kEpt) {
+            w[r] = load4<VEC>(from_c + t);
         } else {
 #pragma unroll
             for (int k = 0; k < kEpt; ++k)
@@ -453,8 +503,8 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __r
         float v[kEpt];
         zero::state8::decode4(w[r], byte[r], v);
         float* const to = out + base + r * kChunk;
-        if (VEC && live[r] == kEpt) {
-            zero::dev::st_stream_at(to, 4 * t, f32x4{v[0], v[1], v[2], v[3]});
+        if (live[r] == kEpt) {
+            store4<VEC>(to, t, f32x4{v[0], v[1], v[2], v[3]});
         } else {
 #pragma unroll
             for (int k = 0; k < kEpt; ++k)
