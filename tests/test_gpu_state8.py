@@ -152,6 +152,29 @@ def test_every_code_and_scale_as_input(zm):
         check(d + [out], oracle.adamw8_step(*state, g, 2, seed=5, **HP), f"gradients {scale}")
 
 
+@pytest.mark.parametrize("coef", [1.0, 0.7312345, 3.0e-5])
+def test_encoding_over_every_exponent(zm, coef):
+    """With both betas 0 the moments are g and g^2 of the clipped gradient: 2^20 elements whose exponents spread over
+    60 binades below their block's largest and whose blocks lie anywhere in bf16's range (some blocks subnormal,
+    some with squares that overflow), so that every normal and subnormal code is met, and cut to zero."""
+    rng = np.random.default_rng(11)
+    n = 1 << 20
+    sign, mant = rng.integers(0, 2, n), rng.integers(0, 128, n)
+    top = np.repeat(rng.integers(1, 255, n // 128), 128)
+    expo = np.maximum(top - rng.integers(0, 60, n) * (rng.random(n) < 0.9), 0)
+    g = (sign << 15 | expo << 7 | mant).astype(np.uint16)
+    state = [np.zeros(n, np.float32)] + [np.zeros(k, np.uint8) for k in (n, n // 128) * 2]
+    hp = dict(HP, beta1=0.0, beta2=0.0)
+    clip = torch.full((1,), coef, dtype=torch.float32, device=dev())
+    d, out = to_dev(state), torch.zeros(n, dtype=torch.int16, device=dev())
+    zm.zero_shard_adamw8_step(*d, to_dev_u16(g), out, 1, seed=13, clip_scale=clip, **hp)
+    want = oracle.adamw8_step(*state, g, 1, seed=13, clip=np.float32(coef), **hp)
+    check(d + [out], want, f"coefficient {coef}")
+    seen = np.bincount(want[1] & 0x7F, minlength=128)
+    note(f"codes of the first moment met: {np.count_nonzero(seen)}")
+    assert (seen[:0x70] > 0).all()                      # every code below the top binade, whose share a coefficient sets
+
+
 def test_non_finite_gradients_make_their_blocks_nan(zm):
     n = 128 * 6 + 5
     state, g = make_state(n, 12), make_grad(n, 13)

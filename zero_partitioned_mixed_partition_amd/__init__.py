@@ -31,6 +31,7 @@ clip, AdamW, gather) on one stream, e.g. for GPT-2 small over 8 ranks:
     rs.step([(0, plan.padded_numel, replica_buffers)]) # rs.tensors: new parameters
 
 RankStep(..., offload=True) keeps the fp32 state in host memory (ZeRO-Offload).
+RankStep(..., state_bits=8) holds the two moments in 8 bits on the device.
 """
 from ._binding import (LIB_PATH, ZERO_MAX_REPLICAS, AdamWSchedule, CopyTable,  # noqa: F401
                        MultiTensorTable, Plan, ReduceTable,

@@ -21,7 +21,8 @@
 // r, subnormal codes included. r uniform is stochastic rounding. gfx950
 // converts so in one instruction (scale, add the seed's high 20 bits, cut,
 // place the byte), to nearest even in another, and back in a third; the GPU
-// tests compare all three with this formula over every code and scale.
+// tests compare all three with this formula: decoding for every code and scale,
+// encoding over every exponent of a block, subnormal codes included.
 //
 // Why stochastic. With beta2 = 0.999 the second moment moves by about 0.1% a
 // step, against code steps of 6-12%: rounding to nearest would return the old
