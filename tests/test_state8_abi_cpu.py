@@ -202,3 +202,71 @@ def test_rank_step_options(zm):
         thirty_two.moments()
     per = step.RankStep(plan, 1, 1, step.Hyper(), 0.0, torch.device("cpu"), state_bits=8, per_param=True)
     assert per.first_element == 128 * 11 and per.exp_avg_scale_tensors[0].numel() == 10
+
+
+class _Stand:
+    """What the binding asks of a device tensor; the address is never dereferenced."""
+
+    def __init__(self, n, size, device, address):
+        self.n, self.size, self.dev, self.address = n, size, device, address
+        self.is_cuda = True
+        self.device = torch.device("cuda", device)
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        return self.size
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.dev
+
+    def data_ptr(self):
+        return self.address
+
+
+def _stands(devices):
+    sizes = (4, 1, 1, 1, 1, 2, 2)
+    return [_Stand(3 if k in (2, 4) else 300, size, dev, 0x1000000 * (k + 1))
+            for k, (size, dev) in enumerate(zip(sizes, devices))]
+
+
+def test_tensors_of_another_device_are_refused(zm, monkeypatch):
+    """The default stream's handle is the same on every device: a call for another device's tensors, or one that
+    mixes devices, would run on the current one with their addresses."""
+    hyper = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    plan = zm.zero_partition_plan([300], 1, 1)
+    cases = [([1] * 7, "the current device is 0")]
+    for k in range(1, 7):
+        cases.append(([int(j == k) for j in range(7)], "the call runs on device 0"))
+    for devices, text in cases:
+        t = _stands(devices)
+        with pytest.raises(ValueError, match=text):
+            zm.zero_shard_adamw8_step(*t, 1, stream=0, **hyper)
+        with pytest.raises(ValueError, match=text):
+            zm.MultiTensor8Table(*[[x] for x in t])
+        with pytest.raises(ValueError, match=text):
+            zm.zero_multi_tensor_adamw8_step(*[[x] for x in t], 1, stream=0, **hyper)
+        with pytest.raises(ValueError, match=text):
+            zm.zero_reduce_adamw8_step(plan, 0, [t[5]], 0, 300, *t[:5], t[6], 1, stream=0, **hyper)
+    here = _stands([0] * 7)
+    far = _Stand(300, 4, 1, 0x9000000)
+    with pytest.raises(ValueError, match="clip_scale lies on device 1"):
+        zm.zero_shard_adamw8_step(*here, 1, clip_scale=far, stream=0, **hyper)
+    with pytest.raises(ValueError, match="clip_scale lies on device 1"):
+        zm.zero_multi_tensor_adamw8_step(*[[x] for x in here], 1, clip_scale=far, stream=0, **hyper)
+    with pytest.raises(ValueError, match="shard_grad lies on device 1"):
+        zm.zero_reduce_adamw8_step(plan, 0, [here[5]], 0, 300, *here[:5], here[6], 1, stream=0,
+                                   shard_grad=_Stand(300, 2, 1, 0x9000000), **hyper)
+    with pytest.raises(ValueError, match="the current device is 0"):
+        zm.zero_state8_quantize(far, here[1], here[2])
+    with pytest.raises(ValueError, match="scales lies on device 1"):
+        zm.zero_state8_quantize(here[0], here[1], _Stand(3, 1, 1, 0x9000000))
+    with pytest.raises(ValueError, match="the current device is 0"):
+        zm.zero_state8_dequantize(here[1], here[2], far)
+    with pytest.raises(ValueError, match="codes lies on device 1"):
+        zm.zero_state8_dequantize(_Stand(300, 1, 1, 0x9000000), here[2], here[0])

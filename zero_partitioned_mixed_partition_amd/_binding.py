@@ -949,15 +949,45 @@ _STATE8 = (("master", 4, False), ("exp_avg", 1, False), ("exp_avg_scale", 1, Tru
            ("exp_avg_sq_scale", 1, True), ("grad", 2, False), ("param_out", 2, False))
 
 
+def _on_device(t, dev: int, size: int, what: str) -> int:
+    """_ptr of a tensor that has to lie on device `dev`."""
+    if t is not None and t.get_device() == dev and t.element_size() == size and t.is_contiguous():
+        return t.data_ptr()
+    p = _ptr(t, size, what)
+    if t is not None:
+        raise ValueError(f"{what} lies on device {t.get_device()}, the call runs on device {dev}")
+    return p
+
+
+def _call_device(t, size: int, what: str) -> int:
+    """The device of a call whose first tensor is t: the current one. The default stream's handle is the same on
+    every device, so a call for another device's tensors would run on the current one with their addresses."""
+    dev = t.get_device()
+    if dev < 0:
+        _ptr(t, size, what)
+    import torch
+    current = torch.cuda.current_device()
+    if dev != current:
+        raise ValueError(f"{what} lies on device {dev}, the current device is {current}")
+    return dev
+
+
 def _state8_ptrs(n: int, tensors) -> List[int]:
     """The pointers of an 8-bit update's seven tensors over n elements (None where the call takes none). The
-    checks are _need's and _ptr's, called only where one fails: their calls cost more than the launch's arguments."""
+    checks are _need's and _on_device's, called only where one fails: their calls cost more than the launch's
+    arguments."""
     blocks = state8_blocks(n)
     for t, (what, _, scale) in zip(tensors, _STATE8):
         if t is not None and t.numel() < (blocks if scale else n):
             _need(t, blocks if scale else n, what)
-    return [t.data_ptr() if t is not None and t.is_cuda and t.element_size() == size and t.is_contiguous()
-            else _ptr(t, size, what) for t, (what, size, _) in zip(tensors, _STATE8)]
+    dev = _call_device(tensors[0], 4, "master")
+    return [t.data_ptr() if t is not None and t.get_device() == dev and t.element_size() == size and t.is_contiguous()
+            else _on_device(t, dev, size, what) for t, (what, size, _) in zip(tensors, _STATE8)]
+
+
+def _clip_ptr(clip_scale, t) -> int:
+    """The clip coefficient's address, on the device of tensor t."""
+    return 0 if clip_scale is None else _on_device(clip_scale, t.get_device(), 4, "clip_scale")
 
 
 def _seed(seed: int) -> int:
@@ -976,7 +1006,7 @@ def prepare_shard_adamw8_step(master, exp_avg, exp_avg_scale, exp_avg_sq, exp_av
     _need(clip_scale, 1, "clip_scale")
     p = Prepared(_adamw8, _state8_ptrs(n, tensors) +
                  [n, first_element, 1, lr, beta1, beta2, eps, weight_decay, _seed(seed),
-                  _ptr(clip_scale, 4, "clip_scale"), _stream(stream, master)],
+                  _clip_ptr(clip_scale, master), _stream(stream, master)],
                  "zero_shard_adamw8_step", step_index=9)
     p._keep = (tensors, clip_scale)
     return p
@@ -993,7 +1023,7 @@ def zero_shard_adamw8_step(master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_s
     _need(clip_scale, 1, "clip_scale")
     _check(_adamw8(*_state8_ptrs(n, (master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad, param_out)),
                    n, first_element, step, lr, beta1, beta2, eps, weight_decay, _seed(seed),
-                   _ptr(clip_scale, 4, "clip_scale"), _stream(stream, master)), "zero_shard_adamw8_step")
+                   _clip_ptr(clip_scale, master), _stream(stream, master)), "zero_shard_adamw8_step")
 
 
 def prepare_shard_adamw8_step_scheduled(master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad,
@@ -1004,8 +1034,8 @@ def prepare_shard_adamw8_step_scheduled(master, exp_avg, exp_avg_scale, exp_avg_
     tensors = (master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, grad, param_out)
     _need(clip_scale, 1, "clip_scale")
     p = Prepared(_adamw8_sched, _state8_ptrs(n, tensors) +
-                 [n, first_element, schedule.handle, _seed(seed), _ptr(clip_scale, 4, "clip_scale"),
-                  _stream(stream, master)], "zero_shard_adamw8_step_scheduled")
+                 [n, first_element, schedule.handle, _seed(seed),
+                  _clip_ptr(clip_scale, master), _stream(stream, master)], "zero_shard_adamw8_step_scheduled")
     p._keep = (tensors, schedule, clip_scale)
     return p
 
@@ -1038,7 +1068,7 @@ def prepare_multi_tensor_adamw8_step(masters, exp_avgs, exp_avg_scales, exp_avg_
     tabs, ns, T = _state8_lists(lists)
     _need(clip_scale, 1, "clip_scale")
     p = Prepared(_mt_adamw8, tabs + [ns, T, first_element, 1, lr, beta1, beta2, eps, weight_decay, _seed(seed),
-                                     _ptr(clip_scale, 4, "clip_scale"),
+                                     _clip_ptr(clip_scale, masters[0]) if T else 0,
                                      _stream(stream, masters[0]) if T else (stream or 0)],
                  "zero_multi_tensor_adamw8_step", step_index=10)
     p._keep = (lists, tabs, ns, clip_scale)
@@ -1086,6 +1116,9 @@ class MultiTensor8Table:
     def blocks(self) -> int:
         return int(_mt8_blocks(self._h))
 
+    def _clip_ptr(self, clip_scale) -> int:
+        return _clip_ptr(clip_scale, self._keep[0][0]) if self._keep[0] else 0
+
     def _stream_of(self, stream) -> int:
         if stream is not None:
             return int(stream)
@@ -1096,7 +1129,7 @@ class MultiTensor8Table:
         """zero_mt8_table_adamw8_step with its arguments marshalled once; call the result with the step."""
         _need(clip_scale, 1, "clip_scale")
         p = Prepared(_mt8_step, [self._h, 1, lr, beta1, beta2, eps, weight_decay, _seed(seed),
-                                 _ptr(clip_scale, 4, "clip_scale"), self._stream_of(stream)],
+                                 self._clip_ptr(clip_scale), self._stream_of(stream)],
                      "zero_mt8_table_adamw8_step", step_index=1)
         p._keep = (self, clip_scale)
         return p
@@ -1105,13 +1138,13 @@ class MultiTensor8Table:
              seed: int = 0, clip_scale=None, stream=None) -> None:
         _need(clip_scale, 1, "clip_scale")
         _check(_mt8_step(self._h, step, lr, beta1, beta2, eps, weight_decay, _seed(seed),
-                         _ptr(clip_scale, 4, "clip_scale"), self._stream_of(stream)), "zero_mt8_table_adamw8_step")
+                         self._clip_ptr(clip_scale), self._stream_of(stream)), "zero_mt8_table_adamw8_step")
 
     def prepare_step_scheduled(self, schedule: AdamWSchedule, seed: int = 0, clip_scale=None,
                                stream=None) -> Prepared:
         """zero_mt8_table_adamw8_step_scheduled with its arguments marshalled once."""
         _need(clip_scale, 1, "clip_scale")
-        p = Prepared(_mt8_step_sched, [self._h, schedule.handle, _seed(seed), _ptr(clip_scale, 4, "clip_scale"),
+        p = Prepared(_mt8_step_sched, [self._h, schedule.handle, _seed(seed), self._clip_ptr(clip_scale),
                                        self._stream_of(stream)], "zero_mt8_table_adamw8_step_scheduled")
         p._keep = (self, schedule, clip_scale)
         return p
@@ -1128,10 +1161,11 @@ def _reduce8_args(plan: Plan, rank: int, replicas, begin: int, count: int, array
         _need(r, count, "a replica")
     _need(shard_grad, S, "shard_grad")
     _need(clip_scale, 1, "clip_scale")
-    ptrs = (c_vp * max(len(replicas), 1))(*[_ptr(r, 2, "replica") for r in replicas])
     state = _state8_ptrs(S, (*arrays, None, param_out))
+    dev = arrays[0].get_device()
+    ptrs = (c_vp * max(len(replicas), 1))(*[_on_device(r, dev, 2, "replica") for r in replicas])
     return [plan.handle, rank, ptrs, len(replicas), begin, count] + state[:5] + [
-        state[6], _ptr(shard_grad, 2, "shard_grad")]
+        state[6], _on_device(shard_grad, dev, 2, "shard_grad")]
 
 
 def prepare_reduce_adamw8_step(plan: Plan, rank: int, replicas: Sequence, begin: int, count: int, master, exp_avg,
@@ -1142,7 +1176,7 @@ def prepare_reduce_adamw8_step(plan: Plan, rank: int, replicas: Sequence, begin:
     arrays = (master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale)
     args = _reduce8_args(plan, rank, replicas, begin, count, arrays, param_out, shard_grad, clip_scale)
     p = Prepared(_reduce_adamw8, args + [first_element, 1, lr, beta1, beta2, eps, weight_decay, _seed(seed),
-                                         _ptr(clip_scale, 4, "clip_scale"), _stream(stream, master)],
+                                         _clip_ptr(clip_scale, master), _stream(stream, master)],
                  "zero_reduce_adamw8_step", step_index=14)
     p._keep = (args, plan, replicas, arrays, param_out, shard_grad, clip_scale)
     return p
@@ -1158,7 +1192,7 @@ def zero_reduce_adamw8_step(plan: Plan, rank: int, replicas: Sequence, begin: in
                          (master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale), param_out, shard_grad,
                          clip_scale)
     _check(_reduce_adamw8(*args, first_element, step, lr, beta1, beta2, eps, weight_decay, _seed(seed),
-                          _ptr(clip_scale, 4, "clip_scale"), _stream(stream, master)), "zero_reduce_adamw8_step")
+                          _clip_ptr(clip_scale, master), _stream(stream, master)), "zero_reduce_adamw8_step")
 
 
 def prepare_reduce_adamw8_step_scheduled(plan: Plan, rank: int, replicas: Sequence, begin: int, count: int, master,
@@ -1169,7 +1203,7 @@ def prepare_reduce_adamw8_step_scheduled(plan: Plan, rank: int, replicas: Sequen
     arrays = (master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale)
     args = _reduce8_args(plan, rank, replicas, begin, count, arrays, param_out, shard_grad, clip_scale)
     p = Prepared(_reduce_adamw8_sched, args + [first_element, schedule.handle, _seed(seed),
-                                               _ptr(clip_scale, 4, "clip_scale"), _stream(stream, master)],
+                                               _clip_ptr(clip_scale, master), _stream(stream, master)],
                  "zero_reduce_adamw8_step_scheduled")
     p._keep = (args, plan, replicas, arrays, param_out, shard_grad, schedule, clip_scale)
     return p
@@ -1190,8 +1224,9 @@ def zero_state8_quantize(x, codes, scales, second_moment: bool = False, stream=N
     n = x.numel()
     _need(codes, n, "codes")
     _need(scales, state8_blocks(n), "scales")
-    _check(_quantize8(_ptr(x, 4, "x"), n, int(second_moment), _ptr(codes, 1, "codes"), _ptr(scales, 1, "scales"),
-                      _stream(stream, x)), "zero_state8_quantize")
+    dev = _call_device(x, 4, "x")
+    _check(_quantize8(_on_device(x, dev, 4, "x"), n, int(second_moment), _on_device(codes, dev, 1, "codes"),
+                      _on_device(scales, dev, 1, "scales"), _stream(stream, x)), "zero_state8_quantize")
 
 
 def zero_state8_dequantize(codes, scales, out, stream=None) -> None:
@@ -1199,5 +1234,6 @@ def zero_state8_dequantize(codes, scales, out, stream=None) -> None:
     n = out.numel()
     _need(codes, n, "codes")
     _need(scales, state8_blocks(n), "scales")
-    _check(_dequantize8(_ptr(codes, 1, "codes"), _ptr(scales, 1, "scales"), n, _ptr(out, 4, "out"),
-                        _stream(stream, out)), "zero_state8_dequantize")
+    dev = _call_device(out, 4, "out")
+    _check(_dequantize8(_on_device(codes, dev, 1, "codes"), _on_device(scales, dev, 1, "scales"), n,
+                        _on_device(out, dev, 4, "out"), _stream(stream, out)), "zero_state8_dequantize")
