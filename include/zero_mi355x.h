@@ -488,9 +488,8 @@ zero_status zero_mt_table_adamw_step_scheduled(const zero_mt_table* table,
  * infinity), a scale byte an e8m0 power of two: value = e4m3(code) *
  * 2^(byte - 127): 3 bits of mantissa down to 2^-13 of the block's largest, the
  * least code at 2^-17 to 2^-16 of it. Byte 255 stands for a block that held an
- * infinity or NaN:
- * it reads as NaN throughout (its codes are written as 0). All-zero bytes are
- * zeros, so cleared arrays are the moments of a new run.
+ * infinity or NaN: it reads as NaN throughout (its codes are written as 0).
+ * All-zero bytes are zeros, so cleared arrays are the moments of a new run.
  * Encoding a block. E = the biased exponent field of the largest magnitude;
  * byte = 255 if E = 255, else max(E - 7, 0) (that magnitude then lies in
  * [2^7, 2^8) in code units and never saturates). In the steps, y = |x| *
@@ -520,7 +519,8 @@ zero_status zero_mt_table_adamw_step_scheduled(const zero_mt_table* table,
  *
  * zero_shard_adamw8_step
  * master       device [n] fp32, updated in place.
- * exp_avg, exp_avg_sq  device [n] codes, updated in place.
+ * exp_avg, exp_avg_sq  device [n] codes, updated in place (exp_avg_sq's values
+ *              are not negative).
  * exp_avg_scale, exp_avg_sq_scale  device [ceil(n / 128)] bytes, in place.
  * grad, param_out, n, step, lr, beta1, beta2, eps, weight_decay, clip_scale:
  *              as zero_shard_adamw_step (a non-finite coefficient skips the
@@ -554,13 +554,14 @@ zero_status zero_shard_adamw8_step_scheduled(float* master, uint8_t* exp_avg, ui
  * ZERO_STATE8_BLOCK; the results are zero_shard_adamw8_step's on each tensor.
  * The list form takes the arrays with every call, 48 tensors a launch (the
  * largest first, which changes no result). Errors: as
- * zero_multi_tensor_adamw_step (ZERO_ERANGE for a tensor of 2^31 workgroups of
- * 512 elements or more), and zero_shard_adamw8_step's on first_element.
+ * zero_multi_tensor_adamw_step (ZERO_ERANGE for a tensor of 1.7e10 elements or
+ * more, which one launch does not hold), and zero_shard_adamw8_step's on
+ * first_element.
  * The table form is for fixed buffers. Create, step, free, blocks and the
- * caller's duties as zero_mt_table_* (create: hipMalloc and a synchronous hipMemcpy on the
- * current device, once; 128 bytes per tensor and 4 per workgroup of 512
- * elements).
- * Errors: as zero_mt_table_*, and zero_shard_adamw8_step's on first_element. */
+ * caller's duties as zero_mt_table_* (create: hipMalloc and a synchronous
+ * hipMemcpy on the current device, once; 128 bytes per tensor and 4 per
+ * workgroup of 512 elements; a longer list than one launch holds takes
+ * several). Errors: as zero_mt_table_*, and zero_shard_adamw8_step's on first_element. */
 zero_status zero_multi_tensor_adamw8_step(float* const* masters, uint8_t* const* exp_avgs,
                                           uint8_t* const* exp_avg_scales,
                                           uint8_t* const* exp_avg_sqs,

@@ -96,6 +96,12 @@ def test_table_refusals(zm):
     assert _table(zm, [a, far], [1000, 1000], first=(1 << 63) - 1024) == R
     far[1] = far[0]
     assert _table(zm, [a, far], [1000, 1000]) == E and "overlaps" in zm.zero_last_error()
+    # past one launch of the list form (the table takes several): refused before any launch
+    big = [0x100000000000 * (k + 1) for k in range(7)]
+    lists = [(ctypes.c_void_p * 2)(big[k], a[k]) for k in range(7)]
+    ns = (ctypes.c_int64 * 2)(512 * (1 << 25), 10)
+    assert zm._binding._mt_adamw8(*lists, ns, 2, 0, 1, *HP, 0, None, None) == R
+    assert "too large for one launch" in zm.zero_last_error()
     none = [None] * 8
     assert zm._binding._mt_adamw8(*none, 0, 0, 0, *HP, 0, None, None) == E          # step < 1
     assert zm._binding._mt_adamw8(*none, 0, 0, 1, *HP, 0, None, None) == zm._binding.ZERO_OK

@@ -681,13 +681,15 @@ extern "C" zero_status zero_multi_tensor_adamw8_step(float* const* masters, uint
     } catch (const std::bad_alloc&) {
         return zero::fail(ZERO_ENOMEM, "zero_multi_tensor_adamw8_step: host allocation failed");
     }
+    constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / kThreads - 1;      // fewer than 2^32 work-items a launch
+    if (!descs.empty() && (descs[0].n - 1) / kChunk + 1 > kMaxBlocks)
+        return zero::fail(ZERO_ERANGE, "zero_multi_tensor_adamw8_step: a tensor too large for one launch");
     for (size_t at = 0; at < descs.size();) {
         ListBatch b{};
         while (at < descs.size() && b.count < kListTensors) {
             const int k = b.count;
             const int64_t end = b.first_block[k] + ((descs[at].n - 1) / kChunk + 1);
-            if (end > zero::kTableLaunchBlocks && k > 0) break;          // fewer than 2^32 work-items a launch
-            if (end > 0x7FFFFFFF) return zero::fail(ZERO_ERANGE, "zero_multi_tensor_adamw8_step: tensor too large");
+            if (end > kMaxBlocks) break;
             b.a[k] = descs[at].a;
             b.n[k] = descs[at].n;
             b.first[k] = descs[at].first;
