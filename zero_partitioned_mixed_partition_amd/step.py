@@ -304,25 +304,49 @@ class RankStep:
                     [(c, s, True) for c, s in zip(self.exp_avg_sq_tensors, self.exp_avg_sq_scale_tensors)])
         return ([(self.exp_avg, self.exp_avg_scale, False)], [(self.exp_avg_sq, self.exp_avg_sq_scale, True)])
 
+    def _hand_over(self, stream, tensors) -> None:
+        """Before calls on `stream` (a handle; None: the current stream) with tensors of the current stream's: the
+        stream waits for the current one (whose queued work may still use their memory), and their memory is
+        handed out again only after what the stream holds when they are freed."""
+        if stream is None:
+            return
+        current = torch.cuda.current_stream(self.device)
+        if int(stream) == current.cuda_stream:
+            return
+        side = (torch.cuda.ExternalStream(int(stream), device=self.device) if int(stream)
+                else torch.cuda.default_stream(self.device))
+        side.wait_stream(current)
+        for x in tensors:
+            x.record_stream(side)
+
     def load_moments(self, exp_avg, exp_avg_sq, stream=None) -> None:
         """Sets the 8-bit moments from fp32 ones, rounded to nearest (a fp32 checkpoint): a device tensor of
-        shard_numel elements each, or with per_param a list of one per segment."""
+        shard_numel elements each, or with per_param a list of one per segment. `stream` first waits for the
+        current stream, which made them; they may be dropped once the call returns."""
+        sets = []
         for given, held in zip((exp_avg, exp_avg_sq), self._moment_sets()):
             given = list(given) if self.per_param else [given]
             if len(given) != len(held) or any(x.numel() != c.numel() for x, (c, _, _) in zip(given, held)):
                 raise ValueError("the moments differ in length from the rank's")
+            if any(x.device.type != self.device.type for x in given):
+                raise ValueError("the moments must be device tensors")
+            sets.append((given, held))
+        self._hand_over(stream, [x for given, _ in sets for x in given])
+        for given, held in sets:
             for x, (codes, scales, second) in zip(given, held):
                 zb.zero_state8_quantize(x, codes, scales, second, stream)
 
     def moments(self, stream=None):
-        """The 8-bit moments as new fp32 tensors (exp_avg, exp_avg_sq), laid out as load_moments takes them."""
-        out = []
-        for held in self._moment_sets():
-            values = [torch.empty(c.numel(), dtype=torch.float32, device=self.device) for c, _, _ in held]
+        """The 8-bit moments as new fp32 tensors (exp_avg, exp_avg_sq), laid out as load_moments takes them. They
+        are the current stream's tensors, written on `stream` after its queued work: a reader on another stream
+        than `stream` waits for it."""
+        sets = self._moment_sets()
+        out = [[torch.empty(c.numel(), dtype=torch.float32, device=self.device) for c, _, _ in held] for held in sets]
+        self._hand_over(stream, [x for values in out for x in values])
+        for values, held in zip(out, sets):
             for x, (codes, scales, _) in zip(values, held):
                 zb.zero_state8_dequantize(codes, scales, x, stream)
-            out.append(values if self.per_param else values[0])
-        return tuple(out)
+        return tuple(values if self.per_param else values[0] for values in out)
 
     def _mt_table(self) -> zb.MultiTensorTable:
         """The per-parameter state's device table (the gradient and the parameter
