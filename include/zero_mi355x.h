@@ -500,11 +500,14 @@ zero_status zero_mt_table_adamw_step_scheduled(const zero_mt_table* table,
  * to the nearest code, ties to even. In the second moment a positive x has a
  * code of at least 1 (never rounded to zero).
  * Random words. Element e of step t of a run with `seed` has a 32-bit word
- * that depends on (seed, t, e) only, all arithmetic unsigned:
- *   z = seed + t * 0x6A09E667F3BCC909;  z = (z ^ z >> 32) * 0xBB67AE8584CAA73B;
+ * that depends on (seed, t, e) only; elements are counted in windows of 2^28,
+ * each with a key of its own. All arithmetic unsigned:
+ *   w = e / 2^28, q = e % 2^28 / 8, j = e % 8;
+ *   z = seed + t * 0x6A09E667F3BCC909 + w * 0xA54FF53A5F1D36F1;
+ *   z = (z ^ z >> 32) * 0xBB67AE8584CAA73B;
  *   z = (z ^ z >> 29) * 0x3C6EF372FE94F82B;  z ^= z >> 32;          (64 bits)
- *   q = e / 8, j = e % 8;  a = (low(q) ^ low(z)) * 0xA54FF53B;  a ^= a >> 16;
- *   a = (a + high(q) + high(z)) * 0x510E527F;  a ^= a >> 15;
+ *   a = (q ^ low(z)) * 0xA54FF53B;           a ^= a >> 16;
+ *   a = (a + high(z)) * 0x510E527F;          a ^= a >> 15;
  *   b = a * 0x9B05688D;  b = (b ^ b >> 16) | 1;  word = a + j * b   (32 bits)
  * The first moment's r is word >> 12, the second's word & 0xFFFFF.
  * first_element (a multiple of ZERO_STATE8_BLOCK, >= 0) is the number e of the

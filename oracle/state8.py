@@ -17,6 +17,7 @@ import numpy as np
 from .adamw import adamw_step
 
 BLOCK = 128
+WINDOW = 1 << 28
 _WIDE = (1 << 64) - 1
 
 
@@ -52,9 +53,9 @@ def decode(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
     return out.reshape(-1)[:len(codes)]
 
 
-def words(n: int, first: int, seed: int, step: int) -> np.ndarray:
-    """The 32-bit random words of elements first .. first + n - 1."""
-    z = (seed + step * 0x6A09E667F3BCC909) & _WIDE
+def words(n: int, first: int, seed: int, step: int, window: int = 0) -> np.ndarray:
+    """The 32-bit random words of elements first .. first + n - 1 of one window's stream."""
+    z = (seed + step * 0x6A09E667F3BCC909 + window * 0xA54FF53A5F1D36F1) & _WIDE
     z = ((z ^ (z >> 32)) * 0xBB67AE8584CAA73B) & _WIDE
     z = ((z ^ (z >> 29)) * 0x3C6EF372FE94F82B) & _WIDE
     z ^= z >> 32
@@ -69,6 +70,18 @@ def words(n: int, first: int, seed: int, step: int) -> np.ndarray:
     b = (a * u(0x9B05688D)) & low
     b = (b ^ (b >> u(16))) | u(1)
     return ((a + j * b) & low).astype(np.uint32)
+
+
+def element_words(n: int, first: int, seed: int, step: int) -> np.ndarray:
+    """The random words of elements first .. first + n - 1 of a step: each window of 2^28 elements has a
+    stream of its own, numbered from the window's start."""
+    parts, end = [], first + n
+    while first < end:
+        window, at = divmod(first, WINDOW)
+        count = min(end - first, WINDOW - at)
+        parts.append(words(count, at, seed, step, window) if window else words(count, at, seed, step))
+        first += count
+    return np.concatenate(parts) if parts else np.zeros(0, np.uint32)
 
 
 def encode(x: np.ndarray, second: bool, draw: np.ndarray = None):
@@ -112,7 +125,7 @@ def adamw8_step(master, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, gr
     with np.errstate(invalid="ignore", over="ignore", divide="ignore", under="ignore"):
         p, m, v, bits = adamw_step(master, decode(exp_avg, exp_avg_scale), decode(exp_avg_sq, exp_avg_sq_scale),
                                    grad_bits, step, lr, beta1, beta2, eps, weight_decay, clip)
-    w = words(n, first_element, seed, step)
+    w = element_words(n, first_element, seed, step)
     mc, ms = encode(m, False, w >> np.uint32(12))
     vc, vs = encode(v, True, w & np.uint32(0xFFFFF))
     return p, mc, ms, vc, vs, bits

@@ -45,7 +45,6 @@ using zero::dev::u32x2;
 using zero::dev::u32x4;
 using zero::adam::AdamState;
 using AdamScalars = zero::adam::StepScalars;
-using zero::state8::Key;
 using zero::state8::Words;
 using zero::state8::kBlock;
 
@@ -206,12 +205,12 @@ __device__ __forceinline__ void load_grad(float (&g)[kEpt], const uint16_t* grad
 }
 
 // Updates a lane's elements from their clipped gradients and writes them back;
-// `first` is the number of the chunk's first element. Every lane of the wave
-// calls it (the block maxima cross lanes); a lane past n brings zeros, which
-// change no maximum.
+// `first` is the number of the chunk's first element, `base` the step's part of
+// the random words' keys. Every lane of the wave calls it (the block maxima cross
+// lanes); a lane past n brings zeros, which change no maximum.
 template <bool VEC>
 __device__ __forceinline__ void update_and_store(Lane& l, const float (&g)[kEpt], const Arrays& a, uint32_t t,
-                                                 int64_t first, const AdamScalars& c, Key key) {
+                                                 int64_t first, const AdamScalars& c, uint64_t base) {
     float m[kEpt], v[kEpt];
     zero::state8::decode4(l.m, l.ms, m);
     zero::state8::decode4(l.v, l.vs, v);
@@ -220,7 +219,7 @@ __device__ __forceinline__ void update_and_store(Lane& l, const float (&g)[kEpt]
     const uint32_t ms = zero::state8::scale_byte(zero::state8::block_max(zero::state8::max_bits4(m)));
     const uint32_t vs = zero::state8::scale_byte(zero::state8::block_max(zero::state8::max_bits4(v)));
     if (l.live == 0) return;
-    const Words words = zero::state8::group_words((static_cast<uint64_t>(first) >> 3) + (t >> 3), key);
+    const Words words = zero::state8::words_at(zero::dev::first_lane(first), t, kChunk, base);
     uint32_t rm[kEpt], rv[kEpt];
     rm[0] = words.a + ((t & 4u) != 0 ? words.b << 2 : 0u);
 #pragma unroll
@@ -255,7 +254,7 @@ __device__ __forceinline__ void update_and_store(Lane& l, const float (&g)[kEpt]
 // One workgroup's kChunk elements from `base` of arrays of n elements.
 template <bool VEC>
 __device__ __forceinline__ void update_chunk(const Arrays& whole, int64_t n, int64_t base, int64_t first,
-                                             const AdamScalars& c, Key key, const float* clip_scale) {
+                                             const AdamScalars& c, uint64_t words, const float* clip_scale) {
     const Arrays a = from(whole, base);
     const uint32_t t = threadIdx.x * kEpt;
     Lane l;
@@ -267,22 +266,23 @@ __device__ __forceinline__ void update_chunk(const Arrays& whole, int64_t n, int
     if (!isfinite(clip)) return;                // the same in every lane
 #pragma unroll
     for (int k = 0; k < kEpt; ++k) g[k] = g[k] * clip;
-    update_and_store<VEC>(l, g, a, t, first + base, c, key);
+    update_and_store<VEC>(l, g, a, t, first + base, c, words);
 }
 
-// The step's scalars and key: from the call, or from a schedule's state.
+// The step's scalars and its part of the random words' keys: from the call, or
+// from a schedule's state.
 struct CallStep {
     AdamScalars c;
-    Key key;
+    uint64_t base;
     __device__ __forceinline__ AdamScalars scalars() const { return c; }
-    __device__ __forceinline__ Key random_key() const { return key; }
+    __device__ __forceinline__ uint64_t words() const { return base; }
 };
 struct ScheduleStep {
     const AdamState* state;
     uint64_t seed;
     __device__ __forceinline__ AdamScalars scalars() const { return state->next; }
-    __device__ __forceinline__ Key random_key() const {
-        return zero::state8::step_key(seed, static_cast<uint64_t>(state->applied + 1));
+    __device__ __forceinline__ uint64_t words() const {
+        return zero::state8::step_base(seed, static_cast<uint64_t>(state->applied + 1));
     }
 };
 
@@ -293,7 +293,7 @@ __device__ __forceinline__ int64_t workgroup() {
 template <bool VEC, typename Step>
 __global__ __launch_bounds__(kThreads) void adamw8_kernel(Arrays a, int64_t n, int64_t first, Step step,
                                                           const float* __restrict__ clip_scale) {
-    update_chunk<VEC>(a, n, workgroup() * kChunk, first, step.scalars(), step.random_key(), clip_scale);
+    update_chunk<VEC>(a, n, workgroup() * kChunk, first, step.scalars(), step.words(), clip_scale);
 }
 
 // Many tensors: one 128-byte descriptor per non-empty tensor and, per
@@ -316,9 +316,9 @@ __global__ __launch_bounds__(kThreads) void adamw8_table_kernel(const Desc* __re
     const Desc d = table[index[zero::dev::xcd_major_entry(blk0, per)]];
     const int64_t base = (blk - d.first_block) * kChunk;
     if (d.vec)
-        update_chunk<true>(d.a, d.n, base, d.first, step.scalars(), step.random_key(), clip_scale);
+        update_chunk<true>(d.a, d.n, base, d.first, step.scalars(), step.words(), clip_scale);
     else
-        update_chunk<false>(d.a, d.n, base, d.first, step.scalars(), step.random_key(), clip_scale);
+        update_chunk<false>(d.a, d.n, base, d.first, step.scalars(), step.words(), clip_scale);
 }
 
 // The list form, for buffers that move from step to step: the descriptors
@@ -345,9 +345,9 @@ __global__ __launch_bounds__(kThreads) void adamw8_list_kernel(ListBatch b, Call
     }
     const int64_t base = static_cast<int64_t>(blk - b.first_block[lo]) * kChunk;
     if ((b.vec >> lo) & 1u)
-        update_chunk<true>(b.a[lo], b.n[lo], base, b.first[lo], step.c, step.key, clip_scale);
+        update_chunk<true>(b.a[lo], b.n[lo], base, b.first[lo], step.c, step.base, clip_scale);
     else
-        update_chunk<false>(b.a[lo], b.n[lo], base, b.first[lo], step.c, step.key, clip_scale);
+        update_chunk<false>(b.a[lo], b.n[lo], base, b.first[lo], step.c, step.base, clip_scale);
 }
 
 // The reduce and the update in one pass: the averaged gradient is the
@@ -426,7 +426,7 @@ __global__ __launch_bounds__(kThreads) void reduce_adamw8_kernel(Replicas reps, 
     if (!isfinite(clip)) return;
 #pragma unroll
     for (int k = 0; k < kEpt; ++k) g[k] = g[k] * clip;
-    update_and_store<VEC>(l, g, a, t, first + base, step.scalars(), step.random_key());
+    update_and_store<VEC>(l, g, a, t, first + base, step.scalars(), step.words());
 }
 
 // ------------------------------------------------------------ conversions
@@ -557,7 +557,7 @@ zero_status call_step(int64_t step, double lr, double beta1, double beta2, doubl
     zero_status st = zero::adam::check_hyper(step, lr, beta1, beta2, eps, weight_decay, who);
     if (st != ZERO_OK) return st;
     st = zero::adam::step_scalars(step, lr, beta1, beta2, weight_decay, eps, &out->c, who);
-    out->key = zero::state8::step_key(seed, static_cast<uint64_t>(step));
+    out->base = zero::state8::step_base(seed, static_cast<uint64_t>(step));
     return st;
 }
 
