@@ -522,12 +522,15 @@ bool vector_ok(const Arrays& a) {
            aligned(a.o, 2 * kEpt);
 }
 
-// Rows of workgroups: a grid dimension holds fewer than 2^32 work-items.
+// The grid of one array's call: rows of workgroups, since a grid dimension holds
+// fewer than 2^32 work-items. At most 2^48 elements, whose rows and bytes fit.
+constexpr int64_t kMaxElements = int64_t(1) << 48;
 zero_status grid_for(int64_t items, int64_t per_workgroup, dim3* grid, const char* who) {
     constexpr int64_t kMaxRow = (int64_t(1) << 32) / kThreads - 1;
+    static_assert(kMaxElements / kChunk / kMaxRow < 0xFFFF, "rows of the largest call");
+    if (items > kMaxElements) return zero::fail(ZERO_ERANGE, std::string(who) + ": more than 2^48 elements");
     const int64_t blocks = (items - 1) / per_workgroup + 1;
     const int64_t rows = (blocks + kMaxRow - 1) / kMaxRow;
-    if (rows > 0xFFFF) return zero::fail(ZERO_ERANGE, std::string(who) + ": n too large for one dispatch");
     *grid = dim3(static_cast<unsigned>((blocks + rows - 1) / rows), static_cast<unsigned>(rows));
     return ZERO_OK;
 }
@@ -865,6 +868,9 @@ zero_status launch_reduce(const zero_plan* plan, int32_t rank, const uint16_t* c
         return fail(ZERO_EINVAL, w + ": the window's part of the shard [" + std::to_string(at) + ", " +
                                      std::to_string(at + n) + ") must start and end at multiples of " +
                                      std::to_string(kBlock) + " elements or the shard's end");
+    dim3 grid;
+    st = grid_for(n, kChunk, &grid, who);
+    if (st != ZERO_OK) return st;
     a.g = replicas[0];
     if (any_null(a)) return fail(ZERO_EINVAL, w + (replicas[0] ? ": NULL state array" : ": NULL replica"));
     Replicas table{};
@@ -884,9 +890,6 @@ zero_status launch_reduce(const zero_plan* plan, int32_t rank, const uint16_t* c
     if (!clash.empty()) return fail(ZERO_EINVAL, w + ": " + clash);
     bool vec = vector_ok(a) && (grad_out == nullptr || aligned(grad_out, 2 * kEpt));
     for (int32_t k = 0; k < n_replicas; ++k) vec = vec && aligned(replicas[k] + src_off, 2 * kEpt);
-    dim3 grid;
-    st = grid_for(n, kChunk, &grid, who);
-    if (st != ZERO_OK) return st;
     const auto kernel = !vec ? reduce_adamw8_kernel<false, kBatch, Step>
                              : (wide_batch(n, n_replicas) ? reduce_adamw8_kernel<true, kWideBatch, Step>
                                                           : reduce_adamw8_kernel<true, kBatch, Step>);
@@ -939,14 +942,14 @@ extern "C" zero_status zero_state8_quantize(const float* x, int64_t n, int32_t s
     if (n < 0) return fail(ZERO_EINVAL, "zero_state8_quantize: n < 0");
     if (n == 0) return ZERO_OK;
     if (!x || !codes || !scales) return fail(ZERO_EINVAL, "zero_state8_quantize: NULL array");
+    dim3 grid;
+    const zero_status st = grid_for(n, kQuantizeRows * kChunk, &grid, who);
+    if (st != ZERO_OK) return st;
     const size_t b = static_cast<size_t>(n);
     const zero::Span wr[] = {{codes, b, "codes"}, {scales, static_cast<size_t>(zero::state8::blocks_of(n)), "scales"}};
     const zero::Span rd[] = {{x, 4 * b, "x"}};
     const std::string clash = zero::first_overlap(wr, 2, rd, 1);
     if (!clash.empty()) return fail(ZERO_EINVAL, "zero_state8_quantize: " + clash);
-    dim3 grid;
-    const zero_status st = grid_for(n, kQuantizeRows * kChunk, &grid, who);
-    if (st != ZERO_OK) return st;
     if (aligned(x, 16) && aligned(codes, 4))
         hipLaunchKernelGGL(quantize_kernel<true>, grid, dim3(kThreads), 0, stream, x, codes, scales, n, second_moment);
     else
@@ -962,14 +965,14 @@ extern "C" zero_status zero_state8_dequantize(const uint8_t* codes, const uint8_
     if (n < 0) return fail(ZERO_EINVAL, "zero_state8_dequantize: n < 0");
     if (n == 0) return ZERO_OK;
     if (!codes || !scales || !out) return fail(ZERO_EINVAL, "zero_state8_dequantize: NULL array");
+    dim3 grid;
+    const zero_status st = grid_for(n, kDequantizeRows * kChunk, &grid, who);
+    if (st != ZERO_OK) return st;
     const size_t b = static_cast<size_t>(n);
     const zero::Span wr[] = {{out, 4 * b, "out"}};
     const zero::Span rd[] = {{codes, b, "codes"}, {scales, static_cast<size_t>(zero::state8::blocks_of(n)), "scales"}};
     const std::string clash = zero::first_overlap(wr, 1, rd, 2);
     if (!clash.empty()) return fail(ZERO_EINVAL, "zero_state8_dequantize: " + clash);
-    dim3 grid;
-    const zero_status st = grid_for(n, kDequantizeRows * kChunk, &grid, who);
-    if (st != ZERO_OK) return st;
     if (aligned(out, 16) && aligned(codes, 4))
         hipLaunchKernelGGL(dequantize_kernel<true>, grid, dim3(kThreads), 0, stream, codes, scales, out, n);
     else
