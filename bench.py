@@ -331,16 +331,18 @@ class RankWorkload:
         self.segs = rs.segments
         sl = [slice(soff, soff + ln) for (_, _, soff, ln) in self.segs]
         self.elems_per_step = sum(x.stop - x.start for x in sl)
-        if self.state_bits == 8:        # no list call takes 8-bit moments
-            return
         lm = [t.clone() for t in rs.master_tensors]
-        lmm = [torch.zeros_like(t) for t in rs.master_tensors]
-        lv = [torch.zeros_like(t) for t in rs.master_tensors]
-        self._list_state = (lm, lmm, lv)
+        held = [rs.exp_avg_tensors, rs.exp_avg_sq_tensors]
+        prepare, extra = zb.prepare_multi_tensor_adamw_step, {}
+        if self.state_bits == 8:
+            held = [rs.exp_avg_tensors, rs.exp_avg_scale_tensors, rs.exp_avg_sq_tensors, rs.exp_avg_sq_scale_tensors]
+            prepare, extra = zb.prepare_multi_tensor_adamw8_step, {"seed": self.seed,
+                                                                   "first_element": rs.first_element}
+        self._list_state = [lm] + [[torch.zeros_like(t) for t in ts] for ts in held]
         st = torch.cuda.current_stream(device).cuda_stream
-        call_list = zb.prepare_multi_tensor_adamw_step(
-            lm, lmm, lv, [rs.grad[x] for x in sl], [rs.param_shards[self.rank][x] for x in sl],
-            clip_scale=rs.scale, stream=st, **self.hyper.as_kwargs())
+        call_list = prepare(*self._list_state, [rs.grad[x] for x in sl],
+                            [rs.param_shards[self.rank][x] for x in sl],
+                            clip_scale=rs.scale, stream=st, **extra, **self.hyper.as_kwargs())
         self.t_list = 0
 
         def adamw_list():
@@ -418,8 +420,8 @@ class RankWorkload:
             b["flatten"] = b["flatten_call"] = 4 * self.phi + 2 * (self.P - self.phi)
         if "gather" in b:
             b["gather_call"] = b["gather"]
-        if getattr(self, "per_tensor", False) and getattr(self, "state_bits", 32) == 32:
-            b["adamw_list"] = 28 * self.elems_per_step
+        if getattr(self, "per_tensor", False):
+            b["adamw_list"] = adamw_bytes_per_element(self) * self.elems_per_step
         if getattr(self, "rt_table", None) is not None:
             b["reduce_tensors"] = (2 * self.replicas + 2) * S
         return b
@@ -579,6 +581,21 @@ def adamw_bytes_per_element(wl) -> float:
     return 28 if getattr(wl, "state_bits", 32) == 32 else 16 + 4 / 128
 
 
+def dtype_of(wl) -> str:
+    """The line's type: what AdamW computes in, and what its moments are held in where that differs."""
+    return "f32" if getattr(wl, "state_bits", 32) == 32 else "f32 (moments held in e4m3)"
+
+
+def adamw_kernel_of(state_bits: int, per_tensor: bool, device_step: bool) -> str:
+    """The kernel of a one-rank workload's AdamW phase. The scheduled 8-bit kernels are instantiations of the plain
+    ones."""
+    if state_bits == 8:
+        return ("adamw8_table_kernel" if per_tensor else "adamw8_kernel") + ("<ScheduleStep>" if device_step else "")
+    if device_step:
+        return "adamw_table_sched_kernel" if per_tensor else "adamw_sched_kernel"
+    return "adamw_kernel"
+
+
 def moments_of(wl) -> str:
     return "" if getattr(wl, "state_bits", 32) == 32 else " with 8-bit moments"
 
@@ -610,9 +627,8 @@ def make_workload(name: str, device, device_step: bool = False, state_bits: int 
     wl = RankWorkload(name, device, device_step, state_bits)
     if state_bits == 8:
         wl.adamw_bpe = adamw_bytes_per_element(wl)
-        wl.adamw_kernel = "adamw8_table_kernel" if wl.per_tensor else "adamw8_kernel"
-    elif device_step:   # the scheduled kernels; the traffic entries are the plain kernel's
-        wl.adamw_kernel = "adamw_table_sched_kernel" if wl.per_tensor else "adamw_sched_kernel"
+    if state_bits == 8 or device_step:      # the traffic entries are the plain 32-bit kernel's
+        wl.adamw_kernel = adamw_kernel_of(state_bits, wl.per_tensor, device_step)
     return wl
 
 
@@ -1078,7 +1094,7 @@ def main(argv=None):
         "higher_is_better": True,
         "scaling": "weak",
         "vs_baseline": None,
-        "dtype": "f32",
+        "dtype": dtype_of(wl),
         "data": "synthetic",
         "config": {"workload": wl.describe(), "name": wl.name, "params": wl.phi,
                    "shard_elems": wl.S, "n_ranks": wl.n_ranks, "replicas": wl.replicas,

@@ -135,3 +135,21 @@ def test_state_bits_option():
         state_bits = 8
     assert bench.adamw_bytes_per_element(Stand) == 16 + 4 / 128 and "8-bit" in bench.moments_of(Stand)
     assert bench.adamw_bytes_per_element(object()) == 28 and bench.moments_of(object()) == ""
+
+
+def test_an_8_bit_line_names_its_type_and_kernel():
+    """A --state-bits 8 line says what the moments are held in, and names the kernel of its AdamW phase, the
+    scheduled one with --device-step; the other lines keep theirs."""
+    sys.path.insert(0, ROOT)
+    import bench
+
+    class Stand:
+        state_bits = 8
+    assert "e4m3" in bench.dtype_of(Stand) and bench.dtype_of(object()) == "f32"
+    names = {(bits, per, dev): bench.adamw_kernel_of(bits, per, dev)
+             for bits in (8, 32) for per in (False, True) for dev in (False, True)}
+    assert names == {(32, False, False): "adamw_kernel", (32, True, False): "adamw_kernel",
+                     (32, False, True): "adamw_sched_kernel", (32, True, True): "adamw_table_sched_kernel",
+                     (8, False, False): "adamw8_kernel", (8, True, False): "adamw8_table_kernel",
+                     (8, False, True): "adamw8_kernel<ScheduleStep>",
+                     (8, True, True): "adamw8_table_kernel<ScheduleStep>"}
