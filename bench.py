@@ -718,7 +718,7 @@ def time_phases(wl, reps: int):
 
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "adamw_traffic.json")
 ADAMW_SOURCES = [os.path.join(ROOT, "zero_partitioned_mixed_partition_amd", "csrc", f)
-                 for f in ("adamw.hip", "device_common.hpp")]
+                 for f in ("adamw.hip", "device_common.hpp", "schedule.hpp", "schedule_device.hpp")]
 
 
 def adamw_flushed(wl, reps: int):

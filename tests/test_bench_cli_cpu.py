@@ -153,3 +153,22 @@ def test_an_8_bit_line_names_its_type_and_kernel():
                      (8, False, False): "adamw8_kernel", (8, True, False): "adamw8_table_kernel",
                      (8, False, True): "adamw8_kernel<ScheduleStep>",
                      (8, True, True): "adamw8_table_kernel<ScheduleStep>"}
+
+
+def test_the_traffic_digest_covers_the_kernels_sources():
+    """Every local header that adamw.hip's kernels are compiled from is hashed (internal.hpp and the C header
+    declare host functions), and the committed entries are tied to that digest."""
+    import re
+    sys.path.insert(0, ROOT)
+    import bench
+    csrc = os.path.join(ROOT, "zero_partitioned_mixed_partition_amd", "csrc")
+    seen, todo = set(), ["adamw.hip"]
+    while todo:
+        name = todo.pop()
+        if name in seen or name in ("internal.hpp", "zero_mi355x.h"):
+            continue
+        seen.add(name)
+        todo += re.findall(r'#include "([^"]+)"', open(os.path.join(csrc, name)).read())
+    assert seen == {os.path.basename(f) for f in bench.ADAMW_SOURCES}
+    for e in json.load(open(bench.TRAFFIC_FILE))["runs"]:
+        assert e["source_sha256"] == bench.kernel_source_digest(), e["workload"]
