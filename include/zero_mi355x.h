@@ -498,7 +498,9 @@ zero_status zero_mt_table_adamw_step_scheduled(const zero_mt_table* table,
  * and the sign in bit 7: stochastic rounding, so that a moment that moves by
  * less than a code's step still moves in the mean. zero_state8_quantize rounds
  * to the nearest code, ties to even. In the second moment a positive x has a
- * code of at least 1 (never rounded to zero).
+ * code of at least 1 (never rounded to zero): one below the block's least code
+ * (2^-17 to 2^-16 of its largest) reads as that code, and its element takes
+ * smaller steps than with fp32 moments; the mean is kept from that code on.
  * Random words. Element e of step t of a run with `seed` has a 32-bit word
  * that depends on (seed, t, e) only; elements are counted in windows of 2^28,
  * each with a key of its own. All arithmetic unsigned:

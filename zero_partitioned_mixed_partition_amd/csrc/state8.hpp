@@ -27,10 +27,13 @@
 // Why stochastic. With beta2 = 0.999 the second moment moves by about 0.1% a
 // step, against code steps of 6-12%: rounding to nearest would return the old
 // code for ever. The stochastic rounding moves it by one code now and then and
-// keeps its mean right.
+// keeps its mean right, at the least code and above.
 //
 // A positive second moment never rounds to zero (its code is at least 1): with
-// v = 0 beside a surviving m, m / (sqrt(v) + eps) would be a step of m / eps.
+// v = 0 beside a surviving m, m / (sqrt(v) + eps) would be a step of m / eps. The
+// price: a v below the least code, 2^-17 to 2^-16 of its block's largest, reads
+// as that code while the block's scale stays, and its element's steps are smaller
+// by the root of the ratio.
 #pragma once
 
 #include <hip/hip_runtime.h>
