@@ -426,7 +426,7 @@ def prepare_reduce_adamw_step(plan: Plan, rank: int, replicas: Sequence, begin: 
                                  _ptr(shard_grad, 2, "shard_grad"), 1, lr, beta1, beta2, eps,
                                  weight_decay, _ptr(clip_scale, 4, "clip_scale"),
                                  _stream(stream, master)], "zero_reduce_adamw_step", step_index=11)
-    p._keep = (ptrs, replicas, master, exp_avg, exp_avg_sq, param_out, shard_grad, clip_scale)
+    p._keep = (plan, ptrs, list(replicas), master, exp_avg, exp_avg_sq, param_out, shard_grad, clip_scale)
     return p
 
 
@@ -461,7 +461,8 @@ def prepare_reduce_adamw_step_scheduled(plan: Plan, rank: int, replicas: Sequenc
                                        _ptr(shard_grad, 2, "shard_grad"), schedule.handle,
                                        _ptr(clip_scale, 4, "clip_scale"), _stream(stream, master)],
                  "zero_reduce_adamw_step_scheduled")
-    p._keep = (ptrs, replicas, master, exp_avg, exp_avg_sq, param_out, shard_grad, schedule, clip_scale)
+    p._keep = (plan, ptrs, list(replicas), master, exp_avg, exp_avg_sq, param_out, shard_grad, schedule,
+               clip_scale)
     return p
 
 
@@ -512,7 +513,7 @@ def prepare_multi_tensor_adamw_step(masters, exp_avgs, exp_avg_sqs, grads, param
     p = Prepared(_mt_adamw, tabs + [ns, T, 1, lr, beta1, beta2, eps, weight_decay,
                                     _ptr(clip_scale, 4, "clip_scale"), st],
                  "zero_multi_tensor_adamw_step", step_index=7)
-    p._keep = (lists, tabs, ns, clip_scale)
+    p._keep = ([list(x) for x in lists], tabs, ns, clip_scale)
     return p
 
 
@@ -546,7 +547,7 @@ class MultiTensorTable:
         _check(_mt_create(*tabs, ns, T, ctypes.byref(h)), "zero_mt_table_create")
         self._h = h
         self._free = _mt_free          # held by the instance for interpreter exit
-        self._keep = lists
+        self._keep = [list(x) for x in lists]
         self.device = masters[0].device if T else None
 
     def __del__(self):
@@ -867,7 +868,7 @@ def prepare_grad_reduce_shard(plan: Plan, rank: int, replicas: Sequence, begin: 
     p = Prepared(_reduce, [plan.handle, rank, ptrs, len(replicas), begin, count,
                            _ptr(shard_grad, 2, "shard_grad"), _ptr(sqnorm_out, 8, "sqnorm_out"), ws,
                            wsb, _stream(stream, shard_grad)], "zero_grad_reduce_shard")
-    p._keep = (ptrs, replicas, shard_grad, sqnorm_out, workspace)
+    p._keep = (plan, ptrs, list(replicas), shard_grad, sqnorm_out, workspace)
     return p
 
 
@@ -925,7 +926,7 @@ def prepare_gather_params(plan: Plan, shards: Sequence, tensors: Sequence, strea
     ref = next((x for x in list(shards) + list(tensors) if x is not None), None)
     p = Prepared(_gather, [plan.handle, sp, tp, _stream(stream, ref) if ref is not None else 0],
                  "zero_gather_params")
-    p._keep = (sp, tp, shards, tensors)
+    p._keep = (plan, sp, tp, list(shards), list(tensors))
     return p
 
 
@@ -934,7 +935,7 @@ def prepare_flatten_params(plan: Plan, tensors: Sequence, flat, stream) -> Prepa
     tp = (c_vp * max(len(tensors), 1))(*[_ptr(t, 2, "tensor") for t in tensors])
     p = Prepared(_flatten, [plan.handle, tp, _ptr(flat, 2, "flat"), _stream(stream, flat)],
                  "zero_flatten_params")
-    p._keep = (tp, tensors, flat)
+    p._keep = (plan, tp, list(tensors), flat)
     return p
 
 
@@ -1071,7 +1072,7 @@ def prepare_multi_tensor_adamw8_step(masters, exp_avgs, exp_avg_scales, exp_avg_
                                      _clip_ptr(clip_scale, masters[0]) if T else 0,
                                      _stream(stream, masters[0]) if T else (stream or 0)],
                  "zero_multi_tensor_adamw8_step", step_index=10)
-    p._keep = (lists, tabs, ns, clip_scale)
+    p._keep = ([list(x) for x in lists], tabs, ns, clip_scale)
     return p
 
 
@@ -1099,7 +1100,7 @@ class MultiTensor8Table:
         _check(_mt8_create(*tabs, ns, T, first_element, ctypes.byref(h)), "zero_mt8_table_create")
         self._h = h
         self._free = _mt8_free         # held by the instance for interpreter exit
-        self._keep = lists
+        self._keep = [list(x) for x in lists]
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -1178,7 +1179,7 @@ def prepare_reduce_adamw8_step(plan: Plan, rank: int, replicas: Sequence, begin:
     p = Prepared(_reduce_adamw8, args + [first_element, 1, lr, beta1, beta2, eps, weight_decay, _seed(seed),
                                          _clip_ptr(clip_scale, master), _stream(stream, master)],
                  "zero_reduce_adamw8_step", step_index=14)
-    p._keep = (args, plan, replicas, arrays, param_out, shard_grad, clip_scale)
+    p._keep = (args, plan, list(replicas), arrays, param_out, shard_grad, clip_scale)
     return p
 
 
@@ -1205,7 +1206,7 @@ def prepare_reduce_adamw8_step_scheduled(plan: Plan, rank: int, replicas: Sequen
     p = Prepared(_reduce_adamw8_sched, args + [first_element, schedule.handle, _seed(seed),
                                                _clip_ptr(clip_scale, master), _stream(stream, master)],
                  "zero_reduce_adamw8_step_scheduled")
-    p._keep = (args, plan, replicas, arrays, param_out, shard_grad, schedule, clip_scale)
+    p._keep = (args, plan, list(replicas), arrays, param_out, shard_grad, schedule, clip_scale)
     return p
 
 
