@@ -628,7 +628,9 @@ zero_status zero_reduce_adamw8_step_scheduled(const zero_plan* plan, int32_t ran
  * a positive x at code 1 or more. The written arrays must not overlap one
  * another or x. zero_state8_dequantize: the values, out device [n] fp32 (exact
  * but for fp32 subnormals, which round to nearest); out must not overlap the
- * codes or the scales.
+ * codes or the scales. Quantizing dequantized values need not give the same
+ * bytes: a block whose largest is a power of two that stochastic rounding
+ * reached gets the next scale, and codes below its normal ones lose a bit.
  * Errors: ZERO_EINVAL (n < 0; with n > 0, null pointers or overlapping arrays,
  * named in zero_last_error()); ZERO_ERANGE for n past 2^48; ZERO_EHIP. */
 zero_status zero_state8_quantize(const float* x, int64_t n, int32_t second_moment, uint8_t* codes,

@@ -59,3 +59,25 @@ def test_a_block_of_large_and_tiny_second_moments_over_steps():
             assert np.allclose(taken, np.broadcast_to(want, taken.shape), rtol=1e-5, atol=2.0 ** -27)
             assert (taken < 1e-3).all()
         last = least
+
+
+@pytest.mark.parametrize("second", [False, True])
+def test_what_a_trip_through_fp32_keeps(second):
+    """Stochastically rounded moments decoded and encoded again, to nearest: blocks keep their bytes unless their
+    largest was rounded up to 2^8 code units. Those get the next scale; each value moves by at most half the new
+    scale's step below the normal codes (2^-10 units), and a second moment by at most the new least code."""
+    rng = np.random.default_rng(2)
+    n = 128 * 4000
+    x = (rng.standard_normal(n) * 1e-3).astype(np.float32)
+    x = x * x if second else x
+    codes, scales = state8.encode(x, second, rng.integers(0, 1 << 20, n))
+    values = state8.decode(codes, scales)
+    again, scales2 = state8.encode(values, second)
+    full = ((codes.reshape(-1, 128) & 0x7F).max(axis=1) == 0x78)            # 2^8
+    assert 0 < full.sum() < len(full) // 10
+    assert np.array_equal(scales2, scales + full)
+    same = codes.reshape(-1, 128)[~full] & 0x7F
+    assert np.array_equal(again.reshape(-1, 128)[~full] & 0x7F, same)
+    moved = np.abs(state8.decode(again, scales2).astype(np.float64) - values).reshape(-1, 128)[full]
+    unit = np.ldexp(1.0, scales2.astype(np.int64) - 127)[full][:, None]
+    assert (moved <= unit * (2.0 ** -9 if second else 2.0 ** -10)).all()

@@ -95,6 +95,8 @@ class RankStep:
     # 1,060.7 us per 164 M-element shard against 1,162.1 us for reduce then
     # AdamW; with 64 replicas over Llama-3-8B's six bucket windows it takes
     # 3.32 ms per step against 3.10-3.19 ms, so wider windows keep the two calls.
+    # (Both with fp32 moments; 8-bit ones take the same rule, which was not
+    # measured for them.)
     FUSE_MAX_REPLICAS = 8
 
     def __init__(self, plan: zb.Plan, rank: int, n_windows: int, hyper: Hyper, max_norm: float,
@@ -339,7 +341,8 @@ class RankStep:
     def moments(self, stream=None):
         """The 8-bit moments as new fp32 tensors (exp_avg, exp_avg_sq), laid out as load_moments takes them. They
         are the current stream's tensors, written on `stream` after its queued work: a reader on another stream
-        than `stream` waits for it."""
+        than `stream` waits for it. (load_moments of them may give a block whose largest was rounded up to a power
+        of two the next scale: an 8-bit run's exact state is its codes and scales.)"""
         sets = self._moment_sets()
         out = [[torch.empty(c.numel(), dtype=torch.float32, device=self.device) for c, _, _ in held] for held in sets]
         self._hand_over(stream, [x for values in out for x in values])
