@@ -848,11 +848,15 @@ def zero_shard_adamw_step_scheduled(master, exp_avg, exp_avg_sq, grad, param_out
 
 
 class Prepared:
+    _device = None      # the device that has to be current, of calls that nothing else ties to theirs
+
     def __init__(self, fn, args, where: str, step_index: Optional[int] = None):
         self._fn, self._args, self._where, self._step_index = fn, list(args), where, step_index
 
     def __call__(self, step: Optional[int] = None) -> None:
         args = self._args
+        if self._device is not None:
+            _same_device(self._device, self._where)
         if self._step_index is not None:
             args = list(args)
             args[self._step_index] = step
@@ -960,16 +964,23 @@ def _on_device(t, dev: int, size: int, what: str) -> int:
     return p
 
 
-def _call_device(t, size: int, what: str) -> int:
-    """The device of a call whose first tensor is t: the current one. The default stream's handle is the same on
-    every device, so a call for another device's tensors would run on the current one with their addresses."""
-    dev = t.get_device()
-    if dev < 0:
-        _ptr(t, size, what)
+def _same_device(dev: int, what: str) -> None:
+    """Refuses device dev unless it is the current one. The default stream's handle is the same on every device, so
+    a call for another device's tensors would run on the current one with their addresses."""
     import torch
     current = torch.cuda.current_device()
     if dev != current:
         raise ValueError(f"{what} lies on device {dev}, the current device is {current}")
+
+
+def _call_device(t, size: int, what: str) -> int:
+    """The device of a call whose first tensor is t: the current one."""
+    dev = t.get_device()
+    if dev < 0:
+        _ptr(t, size, what)
+    import torch
+    if dev != torch.cuda.current_device():
+        _same_device(dev, what)
     return dev
 
 
@@ -1010,6 +1021,7 @@ def prepare_shard_adamw8_step(master, exp_avg, exp_avg_scale, exp_avg_sq, exp_av
                   _clip_ptr(clip_scale, master), _stream(stream, master)],
                  "zero_shard_adamw8_step", step_index=9)
     p._keep = (tensors, clip_scale)
+    p._device = master.get_device()
     return p
 
 
@@ -1073,6 +1085,7 @@ def prepare_multi_tensor_adamw8_step(masters, exp_avgs, exp_avg_scales, exp_avg_
                                      _stream(stream, masters[0]) if T else (stream or 0)],
                  "zero_multi_tensor_adamw8_step", step_index=10)
     p._keep = ([list(x) for x in lists], tabs, ns, clip_scale)
+    p._device = masters[0].get_device() if T else None
     return p
 
 
@@ -1180,6 +1193,7 @@ def prepare_reduce_adamw8_step(plan: Plan, rank: int, replicas: Sequence, begin:
                                          _clip_ptr(clip_scale, master), _stream(stream, master)],
                  "zero_reduce_adamw8_step", step_index=14)
     p._keep = (args, plan, list(replicas), arrays, param_out, shard_grad, clip_scale)
+    p._device = master.get_device()
     return p
 
 
