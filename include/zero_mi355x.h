@@ -24,6 +24,10 @@
  *   zero_shard_adamw8_step, zero_multi_tensor_adamw8_step, zero_mt8_table_*,
  *   zero_reduce_adamw8_step  the AdamW forms with the moments held in 8 bits
  *   zero_state8_quantize, zero_state8_dequantize  those moments from and to fp32
+ *   zero_orthogonalize      a stack of matrices, orthogonalised by Newton-Schulz
+ *                           steps
+ *   zero_muon_step, zero_muon_table_*  Muon's update of weight matrices: momentum,
+ *                           orthogonalisation, weight update and bf16 emit
  *   zero_gather_params      bf16 shards back to per-tensor parameters
  *                           (all-gather output layout, then un-flatten)
  *   zero_flatten_params     per-tensor bf16 buffers into the padded flat buffer
@@ -637,6 +641,114 @@ zero_status zero_state8_quantize(const float* x, int64_t n, int32_t second_momen
                                  uint8_t* scales, hipStream_t stream);
 zero_status zero_state8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n,
                                    float* out, hipStream_t stream);
+
+/* ------------------------------------------------------------------ Muon: orthogonalised updates
+ *
+ * [ZF] "Execution Flow for ZeRO-1", steps 3-4 (the rank updates its fp32 master
+ * weights and emits 16-bit parameters), with Muon's update in place of AdamW's:
+ * a weight matrix moves along its orthogonalised momentum. The state is the fp32
+ * master and one fp32 momentum. The other parameters of a model (vectors,
+ * embeddings) keep AdamW.
+ *
+ * Orthogonalising. G is rows x cols, row-major; a tall one is taken transposed,
+ * so that X has no more rows than columns:
+ *   X = G / (|G| + eps), |G| the Frobenius norm (its squares summed in fp64)
+ *   for each step (a, b, c):  A = X X^T,  X <- a X + (b A + c A^2) X
+ * Each step is an odd polynomial of the singular values; (3.4445, -4.7750,
+ * 2.0315) five times takes those from 1/500 of the norm up to between 0.7 and
+ * 1.2. A zero matrix gives zeros (with eps = 0 too); one that holds an infinity
+ * or NaN gives NaN throughout, and no other matrix of the call is touched by it.
+ * Precision: products of fp16 values (scaled by powers of two) summed in fp32,
+ * the first X of fp32 inputs held in two fp16 parts where it is multiplied; about
+ * 2e-3 of the result's Frobenius norm off the exact steps, as much as rounding
+ * it to bf16. Singular values below about 1e-5 of the norm, and directions
+ * that G does not have, come out as noise of up to 0.02; elements below 3e-10
+ * (a norm far below eps) as zeros or noise of that size. Deterministic: no atomics.
+ *
+ * coefficients host [3 * n_steps] doubles, (a, b, c) of each step.
+ * n_steps      1..32.
+ * eps          >= 0.
+ * workspace    device, 256-byte aligned, zero_muon_workspace_bytes(count, rows,
+ *              cols) bytes or more (0 where the arguments are refused or there is nothing to do):
+ *              8 bytes an element and 6 per element of the smaller side's
+ *              square, both padded to whole tiles. It needs no initialisation, its
+ *              contents on return are unspecified, and calls that may run at the
+ *              same time need separate ones.
+ * Sides: the shorter up to 65,536, the longer up to 2^22.
+ *
+ * zero_orthogonalize: `count` matrices one after the other.
+ * x            device [count * rows * cols], bf16 or fp32 by x_type.
+ * out          device [count * rows * cols] bf16, rounded to nearest even once.
+ *              Must not overlap x or the workspace.
+ * Errors: ZERO_EINVAL (an unknown x_type, a negative count or side, bad steps
+ * or eps, coefficients that let singular values grow past 2^20; with something
+ * to do, null pointers, a workspace not 256-byte aligned, overlapping arrays,
+ * named in zero_last_error()); ZERO_ERANGE (a side past its limit, or more
+ * workgroups than one launch holds); ZERO_ENOSPACE; ZERO_ENOMEM; ZERO_EHIP.
+ *
+ * zero_muon_step: the update of `count` matrices one after the other. Per
+ * element, each operation one IEEE fp32 operation, in this order, the scalars
+ * computed in fp64 and rounded once:
+ *   g = fp32(grad) * clip
+ *   momentum = mu * momentum + g
+ *   u = nesterov ? g + mu * momentum : momentum
+ *   o = the element of u's orthogonalised matrix, in bf16 as zero_orthogonalize
+ *       returns it
+ *   p = p * (1 - lr * weight_decay)
+ *   p = p - (lr * scale) * o
+ *   param_out = bf16_rne(p)
+ * master, momentum  device fp32, updated in place.
+ * grad         device bf16, read only.
+ * param_out    device bf16, written. The written arrays and the workspace must
+ *              not overlap one another or grad.
+ * mu           in [0, 1).
+ * scale        factor of the rate, usually a function of the sides: 0.2 *
+ *              sqrt(max(rows, cols)) gives the update an AdamW step's root mean square.
+ * clip_scale   device float, nullable (NULL means 1). A non-finite value skips
+ *              the update: nothing of the caller's is written.
+ * Errors: as zero_orthogonalize; ZERO_EINVAL (lr < 0, mu outside [0, 1),
+ * non-finite scalars). */
+#define ZERO_MATRIX_BF16 0
+#define ZERO_MATRIX_F32 1
+size_t zero_muon_workspace_bytes(int64_t count, int64_t rows, int64_t cols);
+zero_status zero_orthogonalize(const void* x, int32_t x_type, uint16_t* out, int64_t count, int64_t rows,
+                               int64_t cols, const double* coefficients, int32_t n_steps, double eps,
+                               void* workspace, size_t workspace_bytes, hipStream_t stream);
+zero_status zero_muon_step(float* master, float* momentum, const uint16_t* grad, uint16_t* param_out,
+                           int64_t count, int64_t rows, int64_t cols, double lr, double mu,
+                           int32_t nesterov, double weight_decay, double scale,
+                           const double* coefficients, int32_t n_steps, double eps,
+                           const float* clip_scale, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
+/* zero_muon_step over a list of matrices of any shapes, described once in
+ * device memory (as zero_mt_table_*): every product is one launch over all of
+ * them. The results are zero_muon_step's on each matrix, up to the choice of how the
+ * steps are grouped (below its stated precision), which follows the whole list.
+ * Create: host arrays of n_matrices pointers, sides and scales; a matrix without
+ * elements is left out. hipMalloc and a synchronous hipMemcpy on the current
+ * device, once (128 bytes a matrix and 4 per workgroup). The table keeps the pointers,
+ * not the data: the caller keeps the buffers alive and in place. The written
+ * arrays must not overlap one another or a gradient.
+ * Step: with the table's device current (ZERO_EINVAL otherwise); workspace of
+ * zero_muon_table_workspace_bytes(table) bytes or more. An empty list enqueues nothing.
+ * Free: releases the device memory (hipFree, which waits for the device); no
+ * step using the table may still be running. Accepts NULL.
+ * Matrices: those with elements, or -1 for NULL.
+ * Errors: as zero_muon_step, the first overlap named in zero_last_error();
+ * ZERO_EINVAL for a NULL out or a negative n_matrices; ZERO_ENOMEM; ZERO_EHIP. */
+typedef struct zero_muon_table zero_muon_table;
+zero_status zero_muon_table_create(float* const* masters, float* const* momenta,
+                                   const uint16_t* const* grads, uint16_t* const* params_out,
+                                   const int64_t* rows, const int64_t* cols, const double* scales,
+                                   int32_t n_matrices, zero_muon_table** out);
+void zero_muon_table_free(zero_muon_table* table);
+size_t zero_muon_table_workspace_bytes(const zero_muon_table* table);
+int32_t zero_muon_table_matrices(const zero_muon_table* table);
+zero_status zero_muon_table_step(const zero_muon_table* table, double lr, double mu, int32_t nesterov,
+                                 double weight_decay, const double* coefficients, int32_t n_steps,
+                                 double eps, const float* clip_scale, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------ gather
  *

@@ -26,6 +26,8 @@ Pinning status (what each function is checked against, outside itself):
   Shard(0)    torch.chunk's row cut, round trips, hand-worked case
   state8.py   torch's e4m3 and e8m0 conversions, the mean over all draws, a
               pure-Python count of the random words, the 32-bit step
+  muon.py     the same steps through the singular values, a diagonal matrix
+              step by step, orthogonal invariance
 The fp32 evaluation order inside AdamW and the clip's 1e-6 guard are readings
 (the pages do not write the update out); they are pinned by the closed forms
 and the torch cross-check within tolerance, not bit for bit by the pages.
@@ -38,6 +40,7 @@ from .gather import gather_params, gather_params_shard0  # noqa: F401
 from .plan import Plan, Shard0Plan, memory_bytes, partition_plan, partition_plan_shard0  # noqa: F401
 from .reduce import reduce_shard  # noqa: F401
 from .sqnorm import SqnormAccumulator, sqnorm, sqnorm_fsum  # noqa: F401
+from . import muon  # noqa: F401
 from . import state8  # noqa: F401
 from .state8 import adamw8_step  # noqa: F401
 from .step import rank_step  # noqa: F401

@@ -12,6 +12,8 @@ The entry points mirror the C ABI in include/zero_mi355x.h one for one:
     zero_shard_adamw8_step  the AdamW update with both moments in 8 bits (also
                             MultiTensor8Table, zero_reduce_adamw8_step)
     zero_state8_quantize    fp32 moments -> 8 bits, and zero_state8_dequantize back
+    zero_orthogonalize      matrices orthogonalised by Newton-Schulz steps
+    zero_muon_step          Muon's update of weight matrices (also MuonTable)
     zero_gather_params      bf16 shards -> per-tensor parameters
     zero_flatten_params     per-tensor buffers -> padded flat buffer
     zero_host_adamw_step    the same update on the host CPU (ZeRO-Offload)
@@ -50,4 +52,7 @@ from ._binding import (LIB_PATH, ZERO_MAX_REPLICAS, AdamWSchedule, CopyTable,  #
                        zero_multi_tensor_adamw8_step, zero_reduce_adamw8_step,
                        zero_reduce_adamw8_step_scheduled, zero_shard_adamw8_step,
                        zero_shard_adamw8_step_scheduled, zero_state8_dequantize,
-                       zero_state8_quantize)
+                       zero_state8_quantize,
+                       MUON_COEFFICIENTS, ZERO_MATRIX_BF16, ZERO_MATRIX_F32, MuonTable, muon_scale,
+                       muon_workspace, prepare_muon_step, zero_muon_step, zero_muon_workspace_bytes,
+                       zero_orthogonalize)

@@ -8,6 +8,7 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import List, Optional, Sequence, Tuple
 
@@ -137,6 +138,18 @@ _reduce_adamw8_sched = _fn("zero_reduce_adamw8_step_scheduled", c_i32,
                            [c_i64, c_vp, c_u64, c_vp, c_vp])
 _quantize8 = _fn("zero_state8_quantize", c_i32, [c_vp, c_i64, c_i32, c_vp, c_vp, c_vp])
 _dequantize8 = _fn("zero_state8_dequantize", c_i32, [c_vp, c_vp, c_i64, c_vp, c_vp])
+_muon_ws = _fn("zero_muon_workspace_bytes", c_sz, [c_i64, c_i64, c_i64])
+_orth = _fn("zero_orthogonalize", c_i32,
+            [c_vp, c_i32, c_vp, c_i64, c_i64, c_i64, ctypes.POINTER(c_dbl), c_i32, c_dbl, c_vp, c_sz, c_vp])
+_muon = _fn("zero_muon_step", c_i32,
+            [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_dbl, c_dbl, c_i32, c_dbl, c_dbl, ctypes.POINTER(c_dbl), c_i32,
+             c_dbl, c_vp, c_vp, c_sz, c_vp])
+_muont_create = _fn("zero_muon_table_create", c_i32, [c_vp] * 7 + [c_i32, ctypes.POINTER(c_vp)])
+_muont_free = _fn("zero_muon_table_free", None, [c_vp])
+_muont_ws = _fn("zero_muon_table_workspace_bytes", c_sz, [c_vp])
+_muont_count = _fn("zero_muon_table_matrices", c_i32, [c_vp])
+_muont_step = _fn("zero_muon_table_step", c_i32,
+                  [c_vp, c_dbl, c_dbl, c_i32, c_dbl, ctypes.POINTER(c_dbl), c_i32, c_dbl, c_vp, c_vp, c_sz, c_vp])
 _rt_blocks = _fn("zero_reduce_table_blocks", c_i64, [c_vp])
 _rt_free = _fn("zero_reduce_table_free", None, [c_vp])
 _status_string = _fn("zero_status_string", ctypes.c_char_p, [c_i32])
@@ -1252,3 +1265,225 @@ def zero_state8_dequantize(codes, scales, out, stream=None) -> None:
     dev = _call_device(out, 4, "out")
     _check(_dequantize8(_on_device(codes, dev, 1, "codes"), _on_device(scales, dev, 1, "scales"), n,
                         _on_device(out, dev, 4, "out"), _stream(stream, out)), "zero_state8_dequantize")
+
+
+# --------------------------------------------------------------------------- Muon
+
+ZERO_MATRIX_BF16, ZERO_MATRIX_F32 = 0, 1
+
+# (a, b, c) of each Newton-Schulz step: the usual five, which bring singular values to between 0.7 and 1.2.
+MUON_COEFFICIENTS = ((3.4445, -4.7750, 2.0315),) * 5
+
+
+def muon_scale(rows: int, cols: int) -> float:
+    """The usual factor of Muon's rate: an orthogonalised update times it has the root mean square of an AdamW
+    step, 0.2."""
+    return 0.2 * math.sqrt(max(rows, cols))
+
+
+def zero_muon_workspace_bytes(count: int, rows: int, cols: int) -> int:
+    return int(_muon_ws(count, rows, cols))
+
+
+def muon_workspace(count: int, rows: int, cols: int, device) -> "object":
+    """A device workspace for zero_orthogonalize and zero_muon_step on `count` matrices of rows x cols."""
+    import torch
+    return torch.empty(zero_muon_workspace_bytes(count, rows, cols), dtype=torch.uint8, device=device)
+
+
+def _steps(coefficients):
+    """Host array of the steps' (a, b, c), and their number. The usual ones are marshalled once."""
+    if coefficients is MUON_COEFFICIENTS:
+        return _usual_steps
+    flat = []
+    for step in coefficients:
+        a, b, c = step
+        flat += [float(a), float(b), float(c)]
+    return (c_dbl * max(len(flat), 1))(*flat), len(flat) // 3
+
+
+_usual_steps = ((c_dbl * 15)(*[x for step in MUON_COEFFICIENTS for x in step]), 5)
+
+
+def _stack_count(t, rows: int, cols: int) -> int:
+    """How many matrices of rows x cols tensor t holds."""
+    if rows < 0 or cols < 0:
+        raise ValueError("a side is negative")
+    n = t.numel()
+    if rows * cols == 0:
+        if n:
+            raise ValueError(f"a tensor of {n} elements is no stack of {rows} x {cols} matrices")
+        return 0
+    if n % (rows * cols):
+        raise ValueError(f"a tensor of {n} elements is no stack of {rows} x {cols} matrices")
+    return n // (rows * cols)
+
+
+def _own_workspace(nbytes: int, t, stream):
+    """A workspace for one call on `stream` (a handle; None: the current stream), from torch's allocator."""
+    import torch
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+    if stream is not None and nbytes:
+        current = torch.cuda.current_stream(t.device)
+        if int(stream) != current.cuda_stream:
+            side = (torch.cuda.ExternalStream(int(stream), device=t.device) if int(stream)
+                    else torch.cuda.default_stream(t.device))
+            side.wait_stream(current)          # whose queued work may still use the memory
+            ws.record_stream(side)
+    return ws
+
+
+def _matrix_type(x) -> int:
+    import torch
+    if x.dtype in (torch.bfloat16, torch.int16, torch.uint16):
+        return ZERO_MATRIX_BF16
+    if x.dtype == torch.float32:
+        return ZERO_MATRIX_F32
+    raise ValueError(f"x must hold bf16 or fp32 values, not {x.dtype}")
+
+
+def _bf16_or_bits(t, what: str) -> None:
+    import torch
+    if t.dtype == torch.float16:
+        raise ValueError(f"{what} must hold bf16 values, not {t.dtype}")
+
+
+def zero_orthogonalize(x, out, rows: int, cols: int, coefficients=MUON_COEFFICIENTS, eps: float = 1e-7,
+                       workspace=None, stream=None) -> None:
+    """Each rows x cols matrix of the stack x (bf16 or fp32) orthogonalised by Newton-Schulz steps into out (bf16).
+    coefficients: (a, b, c) of each step. workspace: muon_workspace(count, rows, cols, device), or None for one of
+    the call's own; calls that may run at the same time need separate ones."""
+    count = _stack_count(x, rows, cols)
+    kind = _matrix_type(x)
+    _bf16_or_bits(out, "out")
+    _need(out, x.numel(), "out")
+    if count == 0:
+        return
+    dev = _call_device(x, 4 if kind else 2, "x")
+    steps, n_steps = _steps(coefficients)
+    if workspace is None:
+        workspace = _own_workspace(zero_muon_workspace_bytes(count, rows, cols), x, stream)
+    _check(_orth(_on_device(x, dev, 4 if kind else 2, "x"), kind, _on_device(out, dev, 2, "out"), count, rows, cols,
+                 steps, n_steps, eps, _on_device(workspace, dev, 1, "workspace"), workspace.numel(),
+                 _stream(stream, x)), "zero_orthogonalize")
+
+
+def _muon_ptrs(n: int, tensors, dev: int) -> List[int]:
+    """The pointers of an update's master, momentum, gradient and parameters over n elements."""
+    out = []
+    for t, size, what in zip(tensors, (4, 4, 2, 2), ("master", "momentum", "grad", "param_out")):
+        _need(t, n, what)
+        if size == 2:
+            _bf16_or_bits(t, what)
+        out.append(_on_device(t, dev, size, what))
+    return out
+
+
+def prepare_muon_step(master, momentum_buffer, grad, param_out, rows: int, cols: int, lr: float, momentum: float = 0.95,
+                      nesterov: bool = True, weight_decay: float = 0.0, scale: Optional[float] = None,
+                      coefficients=MUON_COEFFICIENTS, eps: float = 1e-7, clip_scale=None, workspace=None,
+                      stream=None) -> "Prepared":
+    """zero_muon_step with its arguments marshalled once. It holds its workspace (made here where none is given)."""
+    count = _stack_count(master, rows, cols)
+    dev = _call_device(master, 4, "master")
+    ptrs = _muon_ptrs(master.numel(), (master, momentum_buffer, grad, param_out), dev)
+    _need(clip_scale, 1, "clip_scale")
+    steps, n_steps = _steps(coefficients)
+    if workspace is None:
+        workspace = _own_workspace(zero_muon_workspace_bytes(count, rows, cols), master, stream)
+    p = Prepared(_muon, ptrs + [count, rows, cols, lr, momentum, int(nesterov), weight_decay,
+                                muon_scale(rows, cols) if scale is None else scale, steps, n_steps, eps,
+                                _clip_ptr(clip_scale, master), _on_device(workspace, dev, 1, "workspace"),
+                                workspace.numel(), _stream(stream, master)], "zero_muon_step")
+    p._keep = (master, momentum_buffer, grad, param_out, clip_scale, workspace, steps)
+    p._device = dev
+    return p
+
+
+def zero_muon_step(master, momentum_buffer, grad, param_out, rows: int, cols: int, lr: float, momentum: float = 0.95,
+                   nesterov: bool = True, weight_decay: float = 0.0, scale: Optional[float] = None,
+                   coefficients=MUON_COEFFICIENTS, eps: float = 1e-7, clip_scale=None, workspace=None,
+                   stream=None) -> None:
+    """Muon's update of a stack of rows x cols weight matrices: master and momentum_buffer (fp32) in place, grad
+    (bf16) read, param_out (bf16) written. scale: factor of lr (None: muon_scale(rows, cols)). workspace:
+    muon_workspace(count, rows, cols, device), or None for one of the call's own."""
+    prepare_muon_step(master, momentum_buffer, grad, param_out, rows, cols, lr, momentum, nesterov, weight_decay,
+                      scale, coefficients, eps, clip_scale, workspace, stream)()
+
+
+class MuonTable:
+    """Owner of a zero_muon_table: a fixed list of weight matrices of any shapes with their momenta, described once in
+    device memory (on the current device) and stepped together. The tensors are held here, so their
+    buffers outlive the table; so is the workspace, which is made at the first step (one table's steps follow each
+    other in any case: they update the same weights). shapes: (rows, cols) of each; scales: factors of
+    lr (None: muon_scale of each)."""
+
+    def __init__(self, masters, momentum_buffers, grads, params_out, shapes, scales=None):
+        lists = (masters, momentum_buffers, grads, params_out)
+        T = len(shapes)
+        if any(len(x) != T for x in lists) or (scales is not None and len(scales) != T):
+            raise ValueError("the lists must have the same length")
+        shapes = [(int(r), int(c)) for r, c in shapes]
+        if scales is None:
+            scales = [muon_scale(r, c) for r, c in shapes]
+        rows = []
+        for k, (r, c) in enumerate(shapes):
+            if r < 0 or c < 0:
+                raise ValueError("a side is negative")
+            rows.append(_muon_ptrs(r * c, [x[k] for x in lists], _call_device(masters[k], 4, "master")))
+        tabs = [(c_vp * max(T, 1))(*[row[k] for row in rows]) for k in range(4)]
+        sides = [(c_i64 * max(T, 1))(*[s[k] for s in shapes]) for k in range(2)]
+        h = c_vp()
+        _check(_muont_create(*tabs, *sides, (c_dbl * max(T, 1))(*[float(x) for x in scales]), T, ctypes.byref(h)),
+               "zero_muon_table_create")
+        self._h = h
+        self._free = _muont_free       # held by the instance for interpreter exit
+        self._keep = [list(x) for x in lists]
+        self._workspace = None
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        free = getattr(self, "_free", None)
+        if h is not None and h.value and free is not None:
+            free(h)
+            h.value = None
+
+    @property
+    def handle(self) -> c_vp:
+        return self._h
+
+    @property
+    def matrices(self) -> int:
+        """The matrices that have elements."""
+        return int(_muont_count(self._h))
+
+    @property
+    def workspace_bytes(self) -> int:
+        return int(_muont_ws(self._h))
+
+    def prepare_step(self, lr: float, momentum: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0,
+                     coefficients=MUON_COEFFICIENTS, eps: float = 1e-7, clip_scale=None, workspace=None,
+                     stream=None) -> "Prepared":
+        """zero_muon_table_step with its arguments marshalled once."""
+        _need(clip_scale, 1, "clip_scale")
+        steps, n_steps = _steps(coefficients)
+        if not self.matrices:
+            ptrs = [0, 0, 0, 0 if stream is None else int(stream)]
+        else:
+            first = self._keep[0][0]
+            dev = first.get_device()
+            if workspace is None:
+                if self._workspace is None:
+                    self._workspace = _own_workspace(self.workspace_bytes, first, stream)
+                workspace = self._workspace
+            ptrs = [_clip_ptr(clip_scale, first), _on_device(workspace, dev, 1, "workspace"), workspace.numel(),
+                    _stream(stream, first)]
+        p = Prepared(_muont_step, [self._h, lr, momentum, int(nesterov), weight_decay, steps, n_steps, eps] + ptrs,
+                     "zero_muon_table_step")
+        p._keep = (self, clip_scale, workspace, steps)
+        return p
+
+    def step(self, lr: float, momentum: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0,
+             coefficients=MUON_COEFFICIENTS, eps: float = 1e-7, clip_scale=None, workspace=None, stream=None) -> None:
+        """One update of every matrix of the list."""
+        self.prepare_step(lr, momentum, nesterov, weight_decay, coefficients, eps, clip_scale, workspace, stream)()

@@ -1,0 +1,133 @@
+// The products and the workspace of an orthogonalisation (muon_plan.hpp).
+#include "muon_plan.hpp"
+
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+namespace zero {
+namespace muon {
+
+namespace {
+
+// The power of two e for which values up to `bound` are held as value * 2^e: the largest lies in (2^13, 2^14], a
+// factor of 4 below fp16's largest for what roundings add.
+int exponent_for(double bound) { return 14 - static_cast<int>(std::ceil(std::log2(std::max(bound, 1e-6)))); }
+
+float pow2(int e) { return static_cast<float>(std::ldexp(1.0, e)); }
+
+constexpr int kSamples = 2048;
+
+// The largest |f(x)| over [0, top], by samples, with a margin for what lies between them.
+template <typename F>
+double largest(double top, F f) {
+    double most = 0.0;
+    for (int i = 0; i <= kSamples; ++i) most = std::max(most, std::fabs(f(top * i / kSamples)));
+    return most * 1.02;
+}
+
+}  // namespace
+
+zero_status check_coefficients(const double* coefficients, int32_t n_steps, const char* who) {
+    const std::string w(who);
+    if (n_steps < 1 || n_steps > kMaxSteps)
+        return fail(ZERO_EINVAL, w + ": n_steps must be 1.." + std::to_string(kMaxSteps));
+    if (!coefficients) return fail(ZERO_EINVAL, w + ": NULL coefficients");
+    for (int32_t i = 0; i < 3 * n_steps; ++i)
+        if (!std::isfinite(coefficients[i])) return fail(ZERO_EINVAL, w + ": a coefficient is not finite");
+    return ZERO_OK;
+}
+
+double program_cost(int32_t n_steps, bool pairs, double m, double n) {
+    const int32_t two = n_steps < 2 ? 0 : pairs ? n_steps / 2 : 1, one = n_steps - 2 * two;
+    return m * m * (two * (3 * n + 5 * m) + one * (3 * n + m));
+}
+
+zero_status make_program(const double* coefficients, int32_t n_steps, bool pairs, bool low, std::vector<Product>* out,
+                         const char* who) {
+    out->clear();
+    int eX = 14;             // the first X: kappa * 2^-14 times what is held
+    double top = 1.0;        // bound of the eigenvalues of A, X X^T of a matrix of norm 1
+    int32_t from = kT0, to = kT1;
+    for (int32_t at = 0; at < n_steps;) {
+        const bool pair = at + 1 < n_steps && (pairs || at == 0), first = at == 0;
+        const double a = coefficients[3 * at], b = coefficients[3 * at + 1], c = coefficients[3 * at + 2];
+        auto poly = [&](double x) { return a + x * (b + x * c); };
+        auto product = [&](Kind kind, int32_t lhs, int32_t rhs, int32_t o, double alpha) {
+            Product p{};
+            p.kind = kind;
+            p.lhs = lhs, p.rhs = rhs, p.out = o, p.add = kNone, p.out_t = kNone;
+            p.alpha = static_cast<float>(alpha);
+            out->push_back(p);
+            return &out->back();
+        };
+        auto polynomial = [&](double a0, double b0, double c0, int32_t from_s, int32_t to_s, int eA, int eC) {
+            Product* p = product(Kind::kSquare, from_s, from_s, to_s, c0 * pow2(eC - 2 * eA));
+            p->add = from_s;
+            p->beta = static_cast<float>(b0 * pow2(eC - eA));
+            p->diag = static_cast<float>(a0 * pow2(eC));
+        };
+        const int eA = exponent_for(top), eC = exponent_for(largest(top, poly));
+        product(Kind::kGram, kX, kX, kS0, pow2(eA - 2 * eX))->kappa_power = first ? 2 : 0;
+        polynomial(a, b, c, kS0, kS1, eA, eC);
+        int32_t q = kS1;
+        int eQ = eC;
+        double next = largest(top, [&](double x) { return x * poly(x) * poly(x); });
+        if (pair) {
+            const double a1 = coefficients[3 * at + 3], b1 = coefficients[3 * at + 4], c1 = coefficients[3 * at + 5];
+            auto poly1 = [&](double x) { return a1 + x * (b1 + x * c1); };
+            auto after = [&](double x) { return x * poly(x) * poly(x); };       // the eigenvalue after the first step
+            const int eT = exponent_for(largest(top, [&](double x) { return x * poly(x); }));
+            const int eA1 = exponent_for(next), eC1 = exponent_for(largest(next, poly1));
+            eQ = exponent_for(largest(top, [&](double x) { return poly(x) * poly1(after(x)); }));
+            product(Kind::kSquare, kS1, kS0, kS2, pow2(eT - eC - eA));
+            product(Kind::kSquare, kS2, kS1, kS0, pow2(eA1 - eT - eC));
+            polynomial(a1, b1, c1, kS0, kS2, eA1, eC1);
+            product(Kind::kSquare, kS2, kS1, kS0, pow2(eQ - eC1 - eC));
+            q = kS0;
+            next = largest(top, [&](double x) {
+                const double y = after(x), p1 = poly1(y);
+                return y * p1 * p1;
+            });
+        }
+        if (!(next <= std::ldexp(1.0, 40)))
+            return fail(ZERO_EINVAL, std::string(who) + ": these coefficients let singular values grow past 2^20");
+        at += pair ? 2 : 1;
+        const bool last = at == n_steps;
+        const int eN = exponent_for(std::sqrt(next));
+        Product* p = product(last ? Kind::kFinal : Kind::kApply, q, from, last ? kNone : kX,
+                             pow2((last ? 0 : eN) - eQ - eX));
+        p->out_t = last ? kNone : to;
+        p->with_low = first && low;
+        p->kappa_power = first ? 1 : 0;
+        std::swap(from, to);
+        eX = eN;
+        top = next;
+    }
+    return ZERO_OK;
+}
+
+void shape(Desc* d, int64_t rows, int64_t cols, int64_t tile) {
+    const int64_t numel = rows * cols;
+    d->rows = static_cast<int32_t>(rows);
+    d->cols = static_cast<int32_t>(cols);
+    d->M = static_cast<int32_t>(pad(std::min(rows, cols), tile));
+    d->N = static_cast<int32_t>(pad(std::max(rows, cols), tile));
+    d->chunk = std::max(kChunk, pad((numel + kMaxChunks - 1) / kMaxChunks, kChunk));
+    d->chunks = static_cast<int32_t>((numel + d->chunk - 1) / d->chunk);
+}
+
+int64_t grid_count(const Desc& d, int grid, int64_t tile) {
+    const int64_t m = d.M / tile, n = d.N / tile;
+    return grid == kByChunk ? d.chunks : grid == kByTile ? m * n : m * (m + 1) / 2;
+}
+
+int64_t area_bytes(const Desc& d) {
+    const int64_t m = d.M, n = d.N;
+    return pad(2 * (4 * m * n + 3 * m * m), 256);
+}
+
+int64_t head_bytes(int64_t partials, int64_t matrices) { return pad(8 * partials + 4 * matrices, 256); }
+
+}  // namespace muon
+}  // namespace zero

@@ -1,0 +1,116 @@
+// What an orthogonalisation by Newton-Schulz steps computes, as a list of
+// matrix products, and where its matrices lie in the workspace (host C++, no
+// device code).
+//
+// G is a matrix of m x n, m <= n (a tall matrix is taken transposed). With
+// X = G / (|G| + eps) and per step (a, b, c)
+//   A = X X^T,   C = a I + b A + c A^2,   X <- C X,
+// every A and C is a polynomial of the first A, so they commute and are
+// symmetric: products of two of them are computed on the tiles at and below
+// the diagonal and mirrored. Two steps can share one pass over X:
+//   A' = C A C (the next step's A),   X <- (C' C) X,
+// which takes three m^3 products more and one m^2 n product with its X X^T less.
+//
+// In flops, r = n / m: a step alone 3 r + 1 times m^3 (A r, its square 1, the
+// apply 2 r), a pair 3 r + 5 against 6 r + 2. Five steps in pairs 9 r + 11,
+// with one pair only 12 r + 8, one by one 15 r + 5.
+#pragma once
+
+#include <cstdint>
+#include <vector>
+
+#include "internal.hpp"
+
+namespace zero {
+namespace muon {
+
+// A matrix's arrays in the workspace, all fp16, both sides padded to whole tiles with zeros (M >= m, N >= n).
+enum Buffer : int32_t {
+    kX = 0,      // [M][N]: X
+    kT0 = 1,     // [N][M]: X transposed, and
+    kT1 = 2,     // [N][M]: the one being written while the other is read
+    kS0 = 3,     // [M][M]: three square ones for A, C and their products
+    kS1 = 4,
+    kS2 = 5,
+    kLow = 6,    // [N][M]: what rounding the transposed first X to fp16 left (fp32 inputs)
+    kNone = 7,
+};
+
+enum class Kind : int32_t {
+    kGram,      // square output, the sum runs over N
+    kSquare,    // square output, the sum runs over M
+    kApply,     // X and its transpose, the sum runs over M
+    kFinal,     // as kApply, into the caller's array
+};
+
+// out = alpha * kappa^kappa_power * lhs rhs^T + beta * add + diag * I, where an
+// apply's rhs is a transposed X. Values are held scaled by powers of two, so
+// that fp16 keeps its 11 bits from the largest to 2^-27 of it; the factors hold
+// the differences.
+struct Product {
+    Kind kind;
+    int32_t lhs, rhs, add, out, out_t;
+    int32_t with_low;        // the rhs is kT0 + kLow
+    int32_t kappa_power;
+    float alpha, beta, diag;
+};
+
+// The most steps one call takes.
+constexpr int kMaxSteps = 32;
+
+// The products of n_steps steps. `pairs`: steps in pairs, else one pair and single steps. `low`: the first X has a
+// low part. ZERO_EINVAL for steps that let the largest singular value grow past 2^20. Throws std::bad_alloc.
+zero_status make_program(const double* coefficients, int32_t n_steps, bool pairs, bool low, std::vector<Product>* out,
+                         const char* who);
+
+// ZERO_EINVAL for NULL or non-finite coefficients, or n_steps outside [1, kMaxSteps].
+zero_status check_coefficients(const double* coefficients, int32_t n_steps, const char* who);
+
+// Multiplications of one matrix's program, in units of the padded sides' products, for choosing between the two.
+double program_cost(int32_t n_steps, bool pairs, double m, double n);
+
+// ------------------------------------------------------------ sizes
+
+constexpr int64_t kMaxShort = int64_t(1) << 16;    // the longer and the shorter side at most
+constexpr int64_t kMaxLong = int64_t(1) << 22;
+
+// Elements of one workgroup of the momentum pass, and at most so many workgroups (partial sums) a matrix.
+constexpr int64_t kChunk = 8192;
+constexpr int64_t kMaxChunks = 1024;
+
+// One matrix as the kernels see it. Device tables hold an array of these.
+struct alignas(128) Desc {
+    const void* src;          // the gradient (bf16), or the orthogonalisation's input
+    float* momentum;          // NULL for an orthogonalisation
+    float* master;
+    uint16_t* out;            // parameters, or the orthogonalised matrix
+    int64_t ws;               // byte offset of its arrays in the workspace
+    int64_t chunk;            // elements of one workgroup of the momentum pass
+    double scale;             // of its update
+    int32_t rows, cols;       // the caller's
+    int32_t M, N;             // the padded short and long side
+    int32_t first_partial;    // its first partial sum
+    int32_t chunks;
+    int32_t first[3];         // its first workgroup in the momentum pass, the packing and apply, the square products
+    int32_t id;
+};
+static_assert(sizeof(Desc) == 128, "one 128-byte descriptor per matrix");
+
+enum Grid : int32_t { kByChunk = 0, kByTile = 1, kByPair = 2 };
+
+inline int64_t pad(int64_t x, int64_t tile) { return (x + tile - 1) / tile * tile; }
+
+// Fills in M, N, chunk and chunks of a matrix of rows x cols.
+void shape(Desc* d, int64_t rows, int64_t cols, int64_t tile);
+
+// Workgroups of a matrix in each grid.
+int64_t grid_count(const Desc& d, int grid, int64_t tile);
+
+// Bytes of a matrix's arrays (kLow at the end, where the input is fp32).
+int64_t area_bytes(const Desc& d);
+
+// Bytes at the workspace's start: the partial sums and a factor per matrix.
+int64_t head_bytes(int64_t partials, int64_t matrices);
+
+}  // namespace muon
+}  // namespace zero
