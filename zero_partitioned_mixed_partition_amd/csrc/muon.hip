@@ -19,6 +19,7 @@
 #include <cmath>
 #include <new>
 #include <string>
+#include <type_traits>
 #include <vector>
 
 #include "device_common.hpp"
@@ -32,6 +33,8 @@ namespace {
 
 using zero::muon::Desc;
 using zero::muon::Kind;
+using zero::muon::kGrids;
+using zero::muon::stride;
 using zero::muon::Product;
 
 typedef _Float16 f16;
@@ -40,20 +43,20 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256;
-constexpr int kTile = 128;        // a workgroup's tile of a product, and the padding's unit
-constexpr int kDepth = 64;        // K elements of one LDS stage
+using zero::muon::kPack;
 
 // The matrices of one call: a device table of descriptors, or (table NULL) a stack of equal matrices described by its
 // first.
 struct Matrices {
     const Desc* table;
-    const uint32_t* index[3];     // per grid, the descriptor of each workgroup
+    const uint32_t* index[kGrids];    // per grid, the descriptor of each workgroup
     Desc base;
     int64_t src_bytes;            // from one matrix of a stack to the next
     int64_t numel;
     int64_t area;
-    uint32_t per[3];              // workgroups of one matrix of a stack, per grid
-    uint32_t total[3];
+    int64_t tile;                 // of the products: the sides are padded to it
+    uint32_t per[kGrids];         // workgroups of one matrix of a stack, per grid
+    uint32_t total[kGrids];
     double* partials;
     float* kappa;
     char* ws;
@@ -89,17 +92,74 @@ struct MomentumScalars {
 
 __device__ __forceinline__ bool skipped(const float* clip) { return clip != nullptr && !isfinite(*clip); }
 
-__device__ __forceinline__ float gradient(const Desc& d, int64_t i, float clip) {
-    return zero::dev::bf16_to_f32(static_cast<const uint16_t*>(d.src)[i]) * clip;
+// Four consecutive values; the arrays are aligned to their elements only.
+struct __attribute__((packed, aligned(4))) F32x4 {
+    float v[4];
+};
+struct __attribute__((packed, aligned(2))) U16x4 {
+    uint16_t v[4];
+};
+
+// Reads n <= 4 values at element i as fp32 (the rest 0), four at once where n is 4.
+__device__ __forceinline__ void read4(const float* p, int64_t i, int n, float* out) {
+    if (n == 4) {
+        const F32x4 x = *reinterpret_cast<const F32x4*>(p + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[k] = x.v[k];
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[k] = k < n ? p[i + k] : 0.0f;
+    }
+}
+__device__ __forceinline__ void read4(const uint16_t* p, int64_t i, int n, float* out) {
+    if (n == 4) {
+        const U16x4 x = *reinterpret_cast<const U16x4*>(p + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[k] = zero::dev::bf16_to_f32(x.v[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[k] = k < n ? zero::dev::bf16_to_f32(p[i + k]) : 0.0f;
+    }
 }
 
-// The matrix to orthogonalise at element i. kSource: 0 bf16, 1 fp32, 2 momentum (already updated) and gradient.
-template <int kSource>
-__device__ __forceinline__ float input(const Desc& d, int64_t i, const MomentumScalars& s, float clip) {
-    if constexpr (kSource == 0) return zero::dev::bf16_to_f32(static_cast<const uint16_t*>(d.src)[i]);
-    if constexpr (kSource == 1) return static_cast<const float*>(d.src)[i];
-    const float buf = d.momentum[i];
-    return s.nesterov ? gradient(d, i, clip) + s.mu * buf : buf;
+// Writes n <= 4 values at element i, four at once where n is 4.
+__device__ __forceinline__ void write4(float* p, int64_t i, int n, const float* v) {
+    if (n == 4) {
+        *reinterpret_cast<F32x4*>(p + i) = F32x4{{v[0], v[1], v[2], v[3]}};
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < n) p[i + k] = v[k];
+    }
+}
+__device__ __forceinline__ void write4(uint16_t* p, int64_t i, int n, const uint16_t* v) {
+    if (n == 4) {
+        *reinterpret_cast<U16x4*>(p + i) = U16x4{{v[0], v[1], v[2], v[3]}};
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < n) p[i + k] = v[k];
+    }
+}
+
+// The matrix to orthogonalise at elements i to i + n - 1. kSource: 0 bf16, 1 fp32, 2 momentum and gradient (kUpdate:
+// the momentum is moved on and written first).
+template <int kSource, bool kUpdate>
+__device__ __forceinline__ void input4(const Desc& d, int64_t i, int n, const MomentumScalars& s, float clip, float* u) {
+    if constexpr (kSource == 0) read4(static_cast<const uint16_t*>(d.src), i, n, u);
+    if constexpr (kSource == 1) read4(static_cast<const float*>(d.src), i, n, u);
+    if constexpr (kSource == 2) {
+        float buf[4], g[4] = {};
+        read4(d.momentum, i, n, buf);
+        if (kUpdate || s.nesterov) read4(static_cast<const uint16_t*>(d.src), i, n, g);
+        if constexpr (kUpdate) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) buf[k] = s.mu * buf[k] + g[k] * clip;
+            write4(d.momentum, i, n, buf);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[k] = s.nesterov ? g[k] * clip + s.mu * buf[k] : buf[k];
+    }
 }
 
 // Momentum and squared norm: each workgroup takes one chunk of one matrix.
@@ -113,41 +173,62 @@ __global__ __launch_bounds__(kThreads) void momentum_kernel(Matrices m, Momentum
     const int64_t n = static_cast<int64_t>(d.rows) * d.cols;
     const int64_t lo = d.chunk * c, hi = lo + d.chunk < n ? lo + d.chunk : n;
     double sum = 0.0;
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
-        if constexpr (kSource == 2) d.momentum[i] = s.mu * d.momentum[i] + gradient(d, i, clip);
-        const double u = input<kSource>(d, i, s, clip);
-        sum += u * u;
-    }
+    auto add = [&](int64_t i, int count) {
+        float u[4];
+        input4<kSource, true>(d, i, count, s, clip, u);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < count) sum += static_cast<double>(u[k]) * u[k];
+    };
+    int64_t i = lo + 4 * threadIdx.x;
+#pragma unroll 2
+    for (; i + 4 <= hi; i += 4 * kThreads) add(i, 4);
+    if (i < hi) add(i, static_cast<int>(hi - i));
     sum = zero::dev::block_sum<kThreads>(sum, lds);
     if (threadIdx.x == 0) m.partials[d.first_partial + static_cast<int64_t>(c)] = sum;
 }
 
 __device__ __forceinline__ f16* buffer(const Matrices& m, const Desc& d, int32_t which) {
-    const int64_t mn = static_cast<int64_t>(d.M) * d.N, mm = static_cast<int64_t>(d.M) * d.M;
+    const int64_t x = static_cast<int64_t>(d.M) * stride(d.N), xt = static_cast<int64_t>(d.N) * stride(d.M),
+                  mm = static_cast<int64_t>(d.M) * stride(d.M);
     f16* const at = reinterpret_cast<f16*>(m.ws + d.ws);
     switch (which) {
         case zero::muon::kX: return at;
-        case zero::muon::kT0: return at + mn;
-        case zero::muon::kT1: return at + 2 * mn;
-        case zero::muon::kS0: return at + 3 * mn;
-        case zero::muon::kS1: return at + 3 * mn + mm;
-        case zero::muon::kS2: return at + 3 * mn + 2 * mm;
-        default: return at + 3 * mn + 3 * mm;
+        case zero::muon::kT0: return at + x;
+        case zero::muon::kT1: return at + x + xt;
+        case zero::muon::kLow: return at + x + 2 * xt;
+        case zero::muon::kS0: return at + x + 3 * xt;
+        case zero::muon::kS1: return at + x + 3 * xt + mm;
+        default: return at + x + 3 * xt + 2 * mm;
     }
 }
 
-// Packs a 128 x 128 tile of the padded matrix: u * 2^(13 - e), where |u| lies in [2^e, 2^(e + 1)), as fp16 in both
-// orders, and with kLowPart what the rounding left. X is 2^-14 kappa times what is held.
+// Packs a 64 x 64 tile of the padded matrix: u * 2^(13 - e), where |u| lies in [2^e, 2^(e + 1)), as fp16 in both
+// orders, and with kLowPart what the rounding left. X is 2^-14 kappa times what is held. A thread holds 4 x 4 values;
+// the other order goes through LDS, so that both are written in rows of 128 bytes.
 template <int kSource, bool kLowPart>
 __global__ __launch_bounds__(kThreads) void pack_kernel(Matrices m, MomentumScalars s, double eps) {
-    constexpr int kStride = kTile + 2;
-    __shared__ f16 tile[kTile * kStride];
+    __shared__ f16x4 turned[kLowPart ? 2 : 1][kPack * kPack / 4];
     __shared__ double lds[kThreads / zero::dev::kWave];
     __shared__ double total;
     if (skipped(s.clip)) return;
     const float clip = s.clip != nullptr ? *s.clip : 1.0f;
     uint32_t t;
-    const Desc d = find(m, zero::muon::kByTile, blockIdx.x, &t);
+    const Desc d = find(m, zero::muon::kByPack, blockIdx.x, &t);
+    // The source's rows run along `tall ? N : M`.
+    const bool tall = d.rows > d.cols;
+    const int32_t padded_rows = tall ? d.N : d.M, padded_cols = tall ? d.M : d.N;
+    const uint32_t tiles = padded_cols / kPack;
+    const int32_t r0 = static_cast<int32_t>(t / tiles) * kPack, c0 = static_cast<int32_t>(t % tiles) * kPack;
+    const int down = threadIdx.x / 16, right = threadIdx.x % 16;       // the thread's 4 x 4 values
+    float x[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int32_t r = r0 + down * 4 + k, c = c0 + right * 4;
+        int n = r < d.rows ? d.cols - c : 0;
+        n = n < 0 ? 0 : n > 4 ? 4 : n;
+        input4<kSource, false>(d, static_cast<int64_t>(r) * d.cols + c, n, s, clip, x[k]);
+    }
     double sum = 0.0;
     for (int32_t i = threadIdx.x; i < d.chunks; i += kThreads) sum += m.partials[d.first_partial + i];
     sum = zero::dev::block_sum<kThreads>(sum, lds);
@@ -164,54 +245,40 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(Matrices m, MomentumScal
     }
     if (t == 0 && threadIdx.x == 0) m.kappa[d.id] = kappa;
 
-    // The source's rows run along `tall ? N : M`.
-    const bool tall = d.rows > d.cols;
-    const int32_t padded_rows = tall ? d.N : d.M, padded_cols = tall ? d.M : d.N;
-    const uint32_t tiles = padded_cols / kTile;
-    const int32_t r0 = static_cast<int32_t>(t / tiles) * kTile, c0 = static_cast<int32_t>(t % tiles) * kTile;
+    f16x4 high[4], low[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float y = ldexpf(x[k][j], 13 - e);
+            high[k][j] = static_cast<f16>(y);
+            low[k][j] = static_cast<f16>(y - static_cast<float>(high[k][j]));
+        }
     f16* const along = buffer(m, d, tall ? zero::muon::kT0 : zero::muon::kX);
     f16* const across = buffer(m, d, tall ? zero::muon::kX : zero::muon::kT0);
-    f16* const low = buffer(m, d, zero::muon::kLow);
-    constexpr int kPer = kTile * kTile / kThreads;
-    f16 rest[kLowPart ? kPer : 1];
+    f16* const rest = buffer(m, d, zero::muon::kLow);                  // [N][M], as kT0
+    // Column 4 right + j of the tile, its piece `down` of four rows, at place down ^ right.
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const int at = threadIdx.x + k * kThreads, r = at / kTile, c = at % kTile;
-        float x = 0.0f;
-        if (r0 + r < d.rows && c0 + c < d.cols)
-            x = ldexpf(input<kSource>(d, static_cast<int64_t>(r0 + r) * d.cols + c0 + c, s, clip), 13 - e);
-        const f16 h = static_cast<f16>(x);
-        if constexpr (kLowPart) rest[k] = static_cast<f16>(x - static_cast<float>(h));
-        tile[r * kStride + c] = h;
-        along[static_cast<int64_t>(r0 + r) * padded_cols + c0 + c] = h;
+    for (int j = 0; j < 4; ++j) {
+        turned[0][(right * 4 + j) * 16 + (down ^ right)] = f16x4{high[0][j], high[1][j], high[2][j], high[3][j]};
+        if constexpr (kLowPart)
+            turned[1][(right * 4 + j) * 16 + (down ^ right)] = f16x4{low[0][j], low[1][j], low[2][j], low[3][j]};
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int64_t at = static_cast<int64_t>(r0 + down * 4 + k) * stride(padded_cols) + c0 + right * 4;
+        *reinterpret_cast<f16x4*>(along + at) = high[k];
+        if constexpr (kLowPart)
+            if (tall) *reinterpret_cast<f16x4*>(rest + at) = low[k];
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const int at = threadIdx.x + k * kThreads, c = at / kTile, r = at % kTile;
-        across[static_cast<int64_t>(c0 + c) * padded_rows + r0 + r] = tile[r * kStride + c];
-    }
-    if constexpr (kLowPart) {      // [N][M], as kT0
-        if (tall) {
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                const int at = threadIdx.x + k * kThreads, r = at / kTile, c = at % kTile;
-                low[static_cast<int64_t>(r0 + r) * padded_cols + c0 + c] = rest[k];
-            }
-            return;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int at = threadIdx.x + k * kThreads;
-            tile[at / kTile * kStride + at % kTile] = rest[k];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int at = threadIdx.x + k * kThreads, c = at / kTile, r = at % kTile;
-            low[static_cast<int64_t>(c0 + c) * padded_rows + r0 + r] = tile[r * kStride + c];
-        }
+    for (int k = 0; k < 4; ++k) {
+        const int c = down + k * 16;
+        const int64_t at = static_cast<int64_t>(c0 + c) * stride(padded_rows) + r0 + right * 4;
+        *reinterpret_cast<f16x4*>(across + at) = turned[0][c * 16 + (right ^ (c / 4))];
+        if constexpr (kLowPart)
+            if (!tall) *reinterpret_cast<f16x4*>(rest + at) = turned[1][c * 16 + (right ^ (c / 4))];
     }
 }
 
@@ -222,149 +289,397 @@ struct Update {
     const float* clip;
 };
 
-// An operand's tile rows in LDS: kDepth values, eight 16-byte pieces a row, piece p of row r at place p ^ (r / 2 % 8),
-// so that 16 rows' pieces of one column lie in all banks.
-__device__ __forceinline__ int lds_place(int r, int p) { return r * kDepth + ((p ^ ((r >> 1) & 7)) << 3); }
+// A product's tile and its waves: kRows x kCols waves, each of MI x NI MFMA tiles of 32 x 32.
+template <int T>
+struct Shape;
+template <>
+struct Shape<256> {
+    static constexpr int kRows = 2, kCols = 2, kThreads = 64 * kRows * kCols, kStages = 2;
+};
+template <>
+struct Shape<128> {
+    static constexpr int kRows = 2, kCols = 2, kThreads = 64 * kRows * kCols, kStages = 2;
+};
+template <>
+struct Shape<64> {
+    static constexpr int kRows = 2, kCols = 2, kThreads = 64 * kRows * kCols, kStages = 3;
+};
 
-// One 128 x 128 tile of a product: four waves of 64 x 64, each 2 x 2 MFMA tiles of 32 x 32.
-template <bool kSquareOut, int kEnd>     // kEnd: 0 workspace, 1 orthogonalised matrix, 2 weight update
-__global__ __launch_bounds__(kThreads) void product_kernel(Matrices m, Product p, Update u) {
-    __shared__ f16 lds[2 * kTile * kDepth];
+// K elements of one LDS stage: a row's 128 bytes are one cache line. One stage is multiplied, the others are on their
+// way.
+constexpr int kDepth = 64;
+
+// A stage's rows hold eight 16-byte pieces, piece p of row r at place p ^ (r / 2 % 8): 16 rows' pieces of one column
+// then lie in all banks.
+__device__ __forceinline__ int swizzle(int r, int p) { return p ^ ((r >> 1) & 7); }
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// Waits for the wave's LDS reads and until at most n of its loads are on their way, then for the workgroup.
+template <int n>
+__device__ __forceinline__ void landed_and_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(n) : "memory");
+}
+
+// The four values of one column in each lane of a quad (two in each word), as one row's four columns in each.
+__device__ __forceinline__ f16x4 quad_transpose(f16x4 v) {
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+    u32x2_t w = __builtin_bit_cast(u32x2_t, v);
+    const uint32_t lane = threadIdx.x;
+    // lanes 2k and 2k + 1: (r0 r1 | r2 r3) of two columns -> rows 0 / 1 and 2 / 3 of both
+    const bool odd = lane & 1;
+    // what the neighbour needs of this lane: an even lane's odd rows, an odd lane's even rows
+    const uint32_t give = odd ? __builtin_amdgcn_perm(w.y, w.x, 0x05040100) : __builtin_amdgcn_perm(w.y, w.x, 0x07060302);
+    const uint32_t keep = odd ? __builtin_amdgcn_perm(w.y, w.x, 0x07060302) : __builtin_amdgcn_perm(w.y, w.x, 0x05040100);
+    const uint32_t got = __builtin_amdgcn_mov_dpp(give, 0xB1, 0xF, 0xF, true);       // quad_perm 1 0 3 2
+    // keep: this lane's rows (0, 2) or (1, 3); got: the neighbour's same rows. Columns in order: even lane first.
+    const uint32_t left = odd ? got : keep, right = odd ? keep : got;
+    uint32_t a = __builtin_amdgcn_perm(right, left, 0x05040100);     // row 0 (1), two columns
+    uint32_t b = __builtin_amdgcn_perm(right, left, 0x07060302);     // row 2 (3)
+    // lanes q and q ^ 2: row 0 (1) stays in lanes 0, 1; row 2 (3) goes to lanes 2, 3
+    const bool high = lane & 2;
+    const uint32_t give2 = high ? a : b;
+    const uint32_t got2 = __builtin_amdgcn_mov_dpp(give2, 0x4E, 0xF, 0xF, true);     // quad_perm 2 3 0 1
+    u32x2_t out;
+    out.x = high ? got2 : a;
+    out.y = high ? b : got2;
+    return __builtin_bit_cast(f16x4, out);
+}
+
+// Tile t of a matrix of `rows` x `cols` tiles, in strips of kStrip rows, column by column within a strip: 32 tiles
+// in order share 4 rows' and 8 columns' panels.
+constexpr int32_t kStrip = 4;
+
+__device__ __forceinline__ void rect_tile(uint32_t t, int32_t rows, int32_t cols, int32_t* bi, int32_t* bj) {
+    const uint32_t strip = t / (kStrip * cols), first = strip * kStrip;
+    const uint32_t in = t - strip * (kStrip * cols);
+    const uint32_t h = rows - first < kStrip ? rows - first : kStrip;
+    *bj = static_cast<int32_t>(in / h);
+    *bi = static_cast<int32_t>(first + (in - *bj * h));
+}
+
+// The same of the lower triangle of `rows` x `rows` tiles.
+__device__ __forceinline__ void triangle_tile(uint32_t t, int32_t rows, int32_t* bi, int32_t* bj) {
+    int32_t i = static_cast<int32_t>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
+    while (static_cast<uint32_t>(i) * (i + 1) / 2 > t) --i;
+    while (static_cast<uint32_t>(i + 1) * (i + 2) / 2 <= t) ++i;
+    const int32_t first = i / kStrip * kStrip, h = rows - first < kStrip ? rows - first : kStrip;
+    int32_t in = static_cast<int32_t>(t - static_cast<uint32_t>(first) * (first + 1) / 2);
+    const int32_t whole = h * (first + 1);               // columns up to the diagonal's first
+    if (in < whole) {
+        *bj = in / h;
+        *bi = first + (in - *bj * h);
+        return;
+    }
+    in -= whole;
+    int32_t left = h - 1, c = first + 1;
+    while (in >= left) {
+        in -= left;
+        --left;
+        ++c;
+    }
+    *bj = c;
+    *bi = c + in;
+}
+
+// The tile of a workgroup: the dispatcher deals workgroups round-robin to the 8 XCDs, each with an L2 of its own, so
+// runs of `run` tiles go to one XCD. (The grid is rounded up to whole runs on every XCD.)
+__device__ __forceinline__ uint32_t xcd_tile(uint32_t run) {
+    const uint32_t x = blockIdx.x % 8, s = blockIdx.x / 8;
+    return (s / run * 8 + x) * run + s % run;
+}
+
+// One T x T tile of a product, both operands rows of contiguous K.
+template <int T, bool kSquareOut, int kEnd>     // kEnd: 0 workspace, 1 orthogonalised matrix, 2 weight update
+__device__ __forceinline__ void product(const Matrices& m, const Product& p, const Update& u, uint32_t run) {
+    constexpr int kWaves = Shape<T>::kThreads / 64;
+    constexpr int MI = T / 32 / Shape<T>::kRows, NI = T / 32 / Shape<T>::kCols;
+    constexpr int kOperand = T * kDepth;                 // values of one operand's stage
+    constexpr int kLoads = T / 8 / kWaves;               // of 8 rows each, a wave and operand
+    constexpr int kStages = Shape<T>::kStages;
+    __shared__ __align__(16) f16 lds[kStages * 2 * kOperand];
+    static_assert(kStages * 2 * kOperand >= T * T, "the tile fits where the stages were");
     if (kEnd == 2 && skipped(u.clip)) return;
-    uint32_t t;
-    const Desc d = find(m, kSquareOut ? zero::muon::kByPair : zero::muon::kByTile, blockIdx.x, &t);
+    uint32_t t = xcd_tile(run);
+    constexpr int kGrid = kSquareOut ? zero::muon::kByPair : zero::muon::kByTile;
+    if (t >= m.total[kGrid]) return;
+    const Desc d = find(m, kGrid, t, &t);
     const bool tall = d.rows > d.cols;
     int32_t bi, bj;
-    if constexpr (kSquareOut) {           // tile t of the lower triangle, row by row
-        bi = static_cast<int32_t>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
-        while (static_cast<uint32_t>(bi) * (bi + 1) / 2 > t) --bi;
-        while (static_cast<uint32_t>(bi + 1) * (bi + 2) / 2 <= t) ++bi;
-        bj = static_cast<int32_t>(t - static_cast<uint32_t>(bi) * (bi + 1) / 2);
-    } else {
-        const uint32_t tiles = (tall ? d.M : d.N) / kTile;
-        bi = static_cast<int32_t>(t / tiles);
-        bj = static_cast<int32_t>(t % tiles);
-    }
-    const int32_t K = p.kind == Kind::kGram ? d.N : d.M;
+    if constexpr (kSquareOut)
+        triangle_tile(t, d.M / T, &bi, &bj);
+    else
+        rect_tile(t, (tall ? d.N : d.M) / T, (tall ? d.M : d.N) / T, &bi, &bj);
+    const int32_t K = p.kind == Kind::kGram ? d.N : d.M, ld = stride(K);
     const f16* left = buffer(m, d, p.lhs);
     const f16* right = buffer(m, d, p.rhs);
-    const f16* const low = buffer(m, d, zero::muon::kLow);
     if (!kSquareOut && tall) {            // rows of the output are the source's: X^T on the left
         const f16* const x = left;
         left = right;
         right = x;
     }
+    left += static_cast<int64_t>(bi) * T * ld;
+    right += static_cast<int64_t>(bj) * T * ld;
 
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    const int wr = wave / 2 * 64, wc = wave % 2 * 64;
-    f32x16 acc[2][2] = {};
-    const int passes = p.with_low ? 2 : 1;
-    for (int pass = 0; pass < passes; ++pass) {
-        const f16* a = left;
-        const f16* b = right;
-        if (pass == 1) (tall ? a : b) = low;
-        a += static_cast<int64_t>(bi) * kTile * K;
-        b += static_cast<int64_t>(bj) * kTile * K;
-        for (int32_t k0 = 0; k0 < K; k0 += kDepth) {
-            f16x8 ra[4], rb[4];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int wr = wave / Shape<T>::kCols * (MI * 32), wc = wave % Shape<T>::kCols * (NI * 32);
+
+    // Global to LDS: lane l of a load brings the piece that belongs at place l % 8 of row l / 8.
+    const int32_t steps = K / kDepth, all = p.with_low ? 2 * steps : steps;
+    __amdgpu_buffer_rsrc_t from[2] = {zero::dev::through_rsrc(left), zero::dev::through_rsrc(right)};
+    uint32_t at[kLoads];
+    const int row = lane / 8;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = threadIdx.x + i * kThreads, r = at / 8, c = at % 8;
-                ra[i] = *reinterpret_cast<const f16x8*>(a + static_cast<int64_t>(r) * K + k0 + c * 8);
-                rb[i] = *reinterpret_cast<const f16x8*>(b + static_cast<int64_t>(r) * K + k0 + c * 8);
-            }
-            __syncthreads();
+    for (int i = 0; i < kLoads; ++i) {
+        const int r = (wave * kLoads + i) * 8 + row;
+        at[i] = static_cast<uint32_t>(r) * ld * 2 + swizzle(r, lane % 8) * 16;
+    }
+    // Load q of stage s: the left operand's kLoads, then the right's.
+    auto load = [&](int32_t s, int q) {
+        f16* const to = lds + (s % kStages) * 2 * kOperand;
+        const uint32_t k = static_cast<uint32_t>(s < steps ? s : s - steps) * (kDepth * 2);
+        const int o = q / kLoads, i = q % kLoads;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            from[o], (lds_void*)(to + o * kOperand + (wave * kLoads + i) * 8 * kDepth), 16, at[i], k, 0, 0);
+    };
+    auto load_all = [&](int32_t s) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = threadIdx.x + i * kThreads, r = at / 8, c = at % 8;
-                *reinterpret_cast<f16x8*>(lds + lds_place(r, c)) = ra[i];
-                *reinterpret_cast<f16x8*>(lds + kTile * kDepth + lds_place(r, c)) = rb[i];
-            }
-            __syncthreads();
+        for (int q = 0; q < 2 * kLoads; ++q) load(s, q);
+    };
+    auto use_low = [&] {                                 // the low part of X takes its place
+        const f16* const low = buffer(m, d, zero::muon::kLow) + static_cast<int64_t>(tall ? bi : bj) * T * ld;
+        from[tall ? 0 : 1] = zero::dev::through_rsrc(low);
+    };
+    const int turn = (lane >> 1) & 7;                    // of the lane's rows in a fragment
+    const int a_row = (wr + lane % 32) * kDepth, b_row = kOperand + (wc + lane % 32) * kDepth;
+    f32x16 acc[MI][NI] = {};
+    struct Fragments {
+        f16x8 a[MI], b[NI];
+    };
+    // Read r of the fragments of K elements 16 kk to 16 kk + 15 of stage s.
+    auto read = [&](int32_t s, int kk, int r, Fragments& f) {
+        const f16* const st = lds + (s % kStages) * 2 * kOperand + ((2 * kk + lane / 32) ^ turn) * 8;
+        if (r < MI)
+            f.a[r] = *reinterpret_cast<const f16x8*>(st + a_row + r * 32 * kDepth);
+        else
+            f.b[r - MI] = *reinterpret_cast<const f16x8*>(st + b_row + (r - MI) * 32 * kDepth);
+    };
+    // One phase: MI * NI products of `now`, and between them, in this order, the reads of `next` and loads of stage
+    // `load_stage`: issued in a row they would hold the products up.
+    constexpr int kReads = MI + NI, kProducts = MI * NI;
+    auto phase = [&](const Fragments& now, Fragments& next, int32_t s, int kk, int32_t load_stage, auto first, auto count) {
+        int reads = 0, loads = 0;
 #pragma unroll
-            for (int kk = 0; kk < kDepth / 16; ++kk) {
-                f16x8 fa[2], fb[2];
+        for (int q = 0; q < kProducts; ++q) {
+            acc[q / NI][q % NI] =
+                __builtin_amdgcn_mfma_f32_32x32x16_f16(now.a[q / NI], now.b[q % NI], acc[q / NI][q % NI], 0, 0, 0);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int c = kk * 2 + lane / 32;
-                    fa[i] = *reinterpret_cast<const f16x8*>(lds + lds_place(wr + i * 32 + lane % 32, c));
-                    fb[i] = *reinterpret_cast<const f16x8*>(lds + kTile * kDepth + lds_place(wc + i * 32 + lane % 32, c));
-                }
+            for (; reads * kProducts < (q + 1) * kReads * 2 && reads < kReads; ++reads) read(s, kk, reads, next);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-            }
+            for (; loads * kProducts < (q + 1) * count; ++loads) load(load_stage, first + loads);
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    constexpr std::integral_constant<int, 0> kNone{};
+    constexpr std::integral_constant<int, kLoads> kEarly{};   // loads of the phase after the barrier
+    constexpr std::integral_constant<int, 2 * kLoads - kEarly> kLate{};              // and of the phase after that
+    Fragments f0, f1;
+    // One stage. At its barrier stage s + 1 has landed for every wave, and every wave has read all of stage s, whose place
+    // stage s + kStages takes. With two stages its loads are spread over the last phase and the next stage's first
+    // (early and late of them; what late brings is stage s + 1's).
+    auto stage = [&](int32_t s, auto early, auto late, auto flying) {
+        phase(f0, f1, s, 1, s + 1, kEarly, late);
+        phase(f1, f0, s, 2, 0, kNone, kNone);
+        phase(f0, f1, s, 3, 0, kNone, kNone);
+        landed_and_barrier<flying>();
+        if (p.with_low && s + kStages == steps) use_low();
+        if constexpr (kStages > 2)
+            if (s + kStages < all) load_all(s + kStages);
+        phase(f1, f0, s + 1, 0, s + 2, kNone, early);    // (what it reads after the last stage is not used)
+    };
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) {
+        if (p.with_low && s == steps) use_low();
+        if (s < all) load_all(s);
+    }
+    if (all >= kStages)
+        landed_and_barrier<(kStages - 1) * 2 * kLoads>();
+    else
+        landed_and_barrier<0>();
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read(0, 0, r, f0);
+    if constexpr (kStages == 2) {
+        if (2 < all) {
+            stage(0, kEarly, kNone, kNone);
+            for (int32_t s = 1; s + 2 < all; ++s) stage(s, kEarly, kLate, kNone);
+            stage(all - 2, kNone, kLate, kNone);
+        } else if (1 < all) {
+            stage(0, kNone, kNone, kNone);
+        }
+        stage(all - 1, kNone, kNone, kNone);
+    } else {
+        constexpr std::integral_constant<int, (kStages - 2) * 2 * kLoads> kFlying{};
+        int32_t s = 0;
+        for (; s + kStages <= all; ++s) stage(s, kNone, kNone, kFlying);     // stages s + 2 to s + kStages - 1 may fly
+        for (; s < all; ++s) stage(s, kNone, kNone, kNone);
     }
 
-    // A lane holds one column of each MFMA tile, four consecutive rows at a time.
+    // A lane holds one column of each MFMA tile, four consecutive rows at a time; LDS turns them into whole rows, in
+    // either order of storage, so that memory is read and written 16 bytes a lane and 2 T bytes a row.
     float alpha = p.alpha;
     if (p.kappa_power > 0) {
         const float kappa = m.kappa[d.id];
         alpha = p.kappa_power == 2 ? alpha * (kappa * kappa) : alpha * kappa;
     }
-    const int32_t row0 = bi * kTile + wr + lane / 32 * 4, col0 = bj * kTile + wc + lane % 32;
+    const int down = wr + lane / 32 * 4, over = wc + lane % 32;        // the lane's first row, and its column
+    const int quad = lane % 4;
+    // Where eight bytes lie: four values of row r from column 4 g. Rows that are close lie in other banks.
+    auto place = [&](int r, int g) { return r * T + (((g >> 1) ^ ((2 * r) & (T / 8 - 1))) << 3) + (g & 1) * 4; };
+    constexpr int kPerRow = T / 8, kRowStep = 64 * kWaves / kPerRow;    // 16-byte pieces of a row; rows at a time
+    const int own_row = threadIdx.x / kPerRow, own_piece = threadIdx.x % kPerRow;
+    // The tile in LDS to rows of `ld` values at `to`.
+    auto write_rows = [&](f16* to, int64_t ld) {
+#pragma unroll 8
+        for (int r = own_row; r < T; r += kRowStep)
+            *reinterpret_cast<f16x8*>(to + r * ld + own_piece * 8) =
+                *reinterpret_cast<const f16x8*>(lds + place(r, own_piece * 2));
+    };
+    // Calls f(i, j, q) for the lane's groups of four rows.
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) f(i, j, q);
+    };
+    f16x4 values[MI][NI][4];
+    __syncthreads();
     if constexpr (kSquareOut) {
-        const f16* const add = p.add != zero::muon::kNone ? buffer(m, d, p.add) : nullptr;
         f16* const out = buffer(m, d, p.out);
+        const int64_t ldm = stride(d.M);
+        const int64_t direct = bi * T * ldm + bj * T, mirrored = bj * T * ldm + bi * T;
+        if (p.add != zero::muon::kNone) {                // symmetric: its mirrored tile's rows are this one's columns
+            const f16* const add = buffer(m, d, p.add) + mirrored;
+            constexpr int kAtOnce = T / kRowStep < 8 ? T / kRowStep : 8;
+#pragma unroll 1
+            for (int r0 = own_row; r0 < T; r0 += kAtOnce * kRowStep) {
+                f16x8 x[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+                for (int r = 0; r < kAtOnce; ++r)
+                    x[r] = *reinterpret_cast<const f16x8*>(add + (r0 + r * kRowStep) * ldm + own_piece * 8);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+                for (int r = 0; r < kAtOnce; ++r)
+                    *reinterpret_cast<f16x8*>(lds + place(r0 + r * kRowStep, own_piece * 2)) = x[r];
+            }
+            __syncthreads();
+        }
+        const int diagonal = (bj - bi) * T + over - down;               // row minus `down` of the lane's first column
+        each([&](int i, int j, int q) {
+            f16x4 old = {};
+            if (p.add != zero::muon::kNone)
+                old = *reinterpret_cast<const f16x4*>(lds + place(over + j * 32, (down + i * 32 + q * 8) / 4));
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int32_t r = row0 + i * 32 + q * 8, c = col0 + j * 32;
-                    const int64_t mirrored = static_cast<int64_t>(c) * d.M + r;
-                    f16x4 old = {};
-                    if (add != nullptr) old = *reinterpret_cast<const f16x4*>(add + mirrored);
-                    f16x4 v;
+            for (int k = 0; k < 4; ++k) {
+                float x = alpha * acc[i][j][q * 4 + k] + p.beta * static_cast<float>(old[k]);
+                if (i * 32 + q * 8 + k == diagonal + j * 32) x += p.diag;
+                values[i][j][q][k] = static_cast<f16>(x);
+            }
+        });
+        if (p.add != zero::muon::kNone) __syncthreads();
+        if (bi != bj) {
+            each([&](int i, int j, int q) {
+                *reinterpret_cast<f16x4*>(lds + place(over + j * 32, (down + i * 32 + q * 8) / 4)) = values[i][j][q];
+            });
+            __syncthreads();
+            write_rows(out + mirrored, ldm);
+            __syncthreads();
+        }
+        each([&](int i, int j, int q) {
+            *reinterpret_cast<f16x4*>(lds + place(down + i * 32 + q * 8 + quad, (over + j * 32) / 4)) =
+                quad_transpose(values[i][j][q]);
+        });
+        __syncthreads();
+        write_rows(out + direct, ldm);
+    } else if constexpr (kEnd == 0) {
+        const int64_t down_ld = stride(tall ? d.N : d.M), along_ld = stride(tall ? d.M : d.N);
+        f16* const along = buffer(m, d, tall ? p.out_t : p.out);
+        f16* const across = buffer(m, d, tall ? p.out : p.out_t);
+        each([&](int i, int j, int q) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float x = alpha * acc[i][j][q * 4 + k] + p.beta * static_cast<float>(old[k]);
-                        if (r + k == c) x += p.diag;
-                        v[k] = static_cast<f16>(x);
-                        if (bi != bj) out[static_cast<int64_t>(r + k) * d.M + c] = v[k];
-                    }
-                    *reinterpret_cast<f16x4*>(out + mirrored) = v;
-                }
+            for (int k = 0; k < 4; ++k) values[i][j][q][k] = static_cast<f16>(alpha * acc[i][j][q * 4 + k]);
+            *reinterpret_cast<f16x4*>(lds + place(over + j * 32, (down + i * 32 + q * 8) / 4)) = values[i][j][q];
+        });
+        __syncthreads();
+        write_rows(across + bj * T * down_ld + bi * T, down_ld);
+        __syncthreads();
+        each([&](int i, int j, int q) {
+            *reinterpret_cast<f16x4*>(lds + place(down + i * 32 + q * 8 + quad, (over + j * 32) / 4)) =
+                quad_transpose(values[i][j][q]);
+        });
+        __syncthreads();
+        write_rows(along + bi * T * along_ld + bj * T, along_ld);
     } else {
-        const int32_t out_rows = tall ? d.N : d.M, out_cols = tall ? d.M : d.N;
-        f16* const along = kEnd == 0 ? buffer(m, d, tall ? p.out_t : p.out) : nullptr;
-        f16* const across = kEnd == 0 ? buffer(m, d, tall ? p.out : p.out_t) : nullptr;
+        // The orthogonalised matrix in bf16, as bits.
+        each([&](int i, int j, int q) {
+            typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+            const u32x2_t bits = {zero::dev::pack_bf16(alpha * acc[i][j][q * 4], alpha * acc[i][j][q * 4 + 1]),
+                                  zero::dev::pack_bf16(alpha * acc[i][j][q * 4 + 2], alpha * acc[i][j][q * 4 + 3])};
+            *reinterpret_cast<f16x4*>(lds + place(down + i * 32 + q * 8 + quad, (over + j * 32) / 4)) =
+                quad_transpose(__builtin_bit_cast(f16x4, bits));
+        });
+        __syncthreads();
         const float rate = static_cast<float>(u.lr * d.scale);
+        const int32_t c = bj * T + own_piece * 8;
+        const int n = d.cols - c < 8 ? (d.cols - c < 0 ? 0 : d.cols - c) : 8;
+        // Four rows' loads before the first is used; only the last tiles of a matrix need the guards.
+        constexpr int kAtOnce = T / kRowStep < 4 ? T / kRowStep : 4;
+        static_assert(T / kRowStep % kAtOnce == 0, "whole groups");
+        for (int r0 = 0; r0 < T / kRowStep; r0 += kAtOnce) {
+            float w[kAtOnce][8];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int32_t r = row0 + i * 32 + q * 8, c = col0 + j * 32;
-                    f16x4 v;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float x = alpha * acc[i][j][q * 4 + k];
-                        if constexpr (kEnd == 0) {
-                            v[k] = static_cast<f16>(x);
-                            along[static_cast<int64_t>(r + k) * out_cols + c] = v[k];
-                        } else if (r + k < d.rows && c < d.cols) {
-                            const int64_t at = static_cast<int64_t>(r + k) * d.cols + c;
-                            const uint32_t o = zero::dev::f32_to_bf16(x);
-                            if constexpr (kEnd == 1) {
-                                d.out[at] = static_cast<uint16_t>(o);
-                            } else {
-                                float w = d.master[at] * u.decay;
-                                w = w - rate * zero::dev::bf16_to_f32(o);
-                                d.master[at] = w;
-                                d.out[at] = static_cast<uint16_t>(zero::dev::f32_to_bf16(w));
-                            }
-                        }
-                    }
-                    if constexpr (kEnd == 0)
-                        *reinterpret_cast<f16x4*>(across + static_cast<int64_t>(c) * out_rows + r) = v;
+            for (int r = 0; r < kAtOnce; ++r) {
+                const int32_t row_at = bi * T + own_row + (r0 + r) * kRowStep;
+                const int64_t first = static_cast<int64_t>(row_at) * d.cols + c;
+                const int here = row_at < d.rows ? n : 0;
+                if constexpr (kEnd == 2) {
+                    read4(d.master, first, here < 4 ? here : 4, w[r]);
+                    read4(d.master, first + 4, here < 4 ? 0 : here - 4, w[r] + 4);
                 }
+            }
+#pragma unroll
+            for (int r = 0; r < kAtOnce; ++r) {
+                const int row_in = own_row + (r0 + r) * kRowStep;
+                const int32_t row_at = bi * T + row_in;
+                const int64_t first = static_cast<int64_t>(row_at) * d.cols + c;
+                const int here = row_at < d.rows ? n : 0;
+                typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+                const u16x8 o = __builtin_bit_cast(u16x8, *reinterpret_cast<const f16x8*>(lds + place(row_in, own_piece * 2)));
+                uint16_t bits[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if constexpr (kEnd == 1) {
+                        bits[k] = o[k];
+                    } else {
+                        w[r][k] = w[r][k] * u.decay;
+                        w[r][k] = w[r][k] - rate * zero::dev::bf16_to_f32(o[k]);
+                        bits[k] = static_cast<uint16_t>(zero::dev::f32_to_bf16(w[r][k]));
+                    }
+                }
+                if constexpr (kEnd == 2) {
+                    write4(d.master, first, here < 4 ? here : 4, w[r]);
+                    write4(d.master, first + 4, here < 4 ? 0 : here - 4, w[r] + 4);
+                }
+                write4(d.out, first, here < 4 ? here : 4, bits);
+                write4(d.out, first + 4, here < 4 ? 0 : here - 4, bits + 4);
+            }
+        }
     }
+}
+
+template <int T, bool kSquareOut, int kEnd>
+__global__ __launch_bounds__(Shape<T>::kThreads) void product_kernel(Matrices m, Product p, Update u, uint32_t run) {
+    product<T, kSquareOut, kEnd>(m, p, u, run);
 }
 
 // ------------------------------------------------------------ launches
@@ -380,6 +695,23 @@ struct Call {
     double cost[2];               // of one pair and single steps, and of pairs
 };
 
+template <int T, bool kSquareOut, int kEnd>
+void launch_product(const Matrices& m, const Product& p, const Update& u, hipStream_t stream) {
+    // Whole runs on every XCD; no run longer than an eighth of the tiles, so that a short grid reaches every XCD.
+    const uint32_t total = m.total[kSquareOut ? zero::muon::kByPair : zero::muon::kByTile];
+    const uint32_t run = std::min(32u, (total + 7) / 8);
+    const uint32_t blocks = (total + 8 * run - 1) / (8 * run) * (8 * run);
+    hipLaunchKernelGGL((product_kernel<T, kSquareOut, kEnd>), dim3(blocks),
+                       dim3(Shape<T>::kThreads), 0, stream, m, p, u, run);
+}
+
+template <bool kSquareOut, int kEnd>
+void launch_product(const Matrices& m, const Product& p, const Update& u, hipStream_t stream) {
+    if (m.tile == 64) return launch_product<64, kSquareOut, kEnd>(m, p, u, stream);
+    if (m.tile == 128) return launch_product<128, kSquareOut, kEnd>(m, p, u, stream);
+    launch_product<256, kSquareOut, kEnd>(m, p, u, stream);
+}
+
 template <int kSource, int kEnd>
 zero_status launch_all(const Matrices& m, const Call& c, const std::vector<Product>& program, hipStream_t stream,
                        const char* who) {
@@ -387,17 +719,17 @@ zero_status launch_all(const Matrices& m, const Call& c, const std::vector<Produ
                        c.momentum);
     zero_status st = zero::check_hip(hipGetLastError(), who);
     if (st != ZERO_OK) return st;
-    const dim3 tiles(m.total[zero::muon::kByTile]), pairs(m.total[zero::muon::kByPair]);
-    hipLaunchKernelGGL((pack_kernel<kSource, kSource != 0>), tiles, dim3(kThreads), 0, stream, m, c.momentum, c.eps);
+    hipLaunchKernelGGL((pack_kernel<kSource, kSource != 0>), dim3(m.total[zero::muon::kByPack]), dim3(kThreads), 0,
+                       stream, m, c.momentum, c.eps);
     st = zero::check_hip(hipGetLastError(), who);
     for (const Product& p : program) {
         if (st != ZERO_OK) return st;
         if (p.kind == Kind::kGram || p.kind == Kind::kSquare)
-            hipLaunchKernelGGL((product_kernel<true, 0>), pairs, dim3(kThreads), 0, stream, m, p, c.update);
+            launch_product<true, 0>(m, p, c.update, stream);
         else if (p.kind == Kind::kApply)
-            hipLaunchKernelGGL((product_kernel<false, 0>), tiles, dim3(kThreads), 0, stream, m, p, c.update);
+            launch_product<false, 0>(m, p, c.update, stream);
         else
-            hipLaunchKernelGGL((product_kernel<false, kEnd>), tiles, dim3(kThreads), 0, stream, m, p, c.update);
+            launch_product<false, kEnd>(m, p, c.update, stream);
         st = zero::check_hip(hipGetLastError(), who);
     }
     return st;
@@ -405,8 +737,6 @@ zero_status launch_all(const Matrices& m, const Call& c, const std::vector<Produ
 
 zero_status launch(const Matrices& m, const Call& c, hipStream_t stream, const char* who) {
     std::vector<Product> program;
-    // Pairs where they save a twentieth of the multiplications or more: at equal cost the single steps, whose A comes
-    // from X itself, are more exact (about 1.2e-3 of the result's norm against 1.5e-3 to 1.9e-3).
     const bool pairs = c.cost[1] < 0.95 * c.cost[0];
     try {
         const zero_status st = zero::muon::make_program(c.coefficients, c.n_steps, pairs, c.source != 0, &program, who);
@@ -438,18 +768,21 @@ zero_status check_sides(int64_t rows, int64_t cols, const std::string& what) {
     return ZERO_OK;
 }
 
-constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / kThreads - 1;      // fewer than 2^32 work-items a launch
+constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / 512 - 256;         // fewer than 2^32 work-items a launch
 
 // A stack's sizes: its first matrix's descriptor (sides, chunks), the workgroups and the workspace. ZERO_ERANGE where
 // one launch does not hold it.
 zero_status measure_stack(int64_t count, int64_t rows, int64_t cols, Matrices* m, int64_t* bytes, const char* who) {
     zero_status st = check_sides(rows, cols, who);
     if (st != ZERO_OK) return st;
-    zero::muon::shape(&m->base, rows, cols, kTile);
+    zero::muon::TileChoice choice;
+    choice.add(count, rows, cols);
+    m->tile = choice.best();
+    zero::muon::shape(&m->base, rows, cols, m->tile);
     m->numel = rows * cols;
     m->area = zero::muon::area_bytes(m->base);
-    for (int g = 0; g < 3; ++g) {
-        const int64_t per = zero::muon::grid_count(m->base, g, kTile);
+    for (int g = 0; g < kGrids; ++g) {
+        const int64_t per = zero::muon::grid_count(m->base, g, m->tile);
         if (count > kMaxBlocks / per)
             return zero::fail(ZERO_ERANGE, std::string(who) + ": more workgroups than one launch holds");
         m->per[g] = static_cast<uint32_t>(per);
@@ -501,7 +834,7 @@ zero_status muon_call(double lr, double momentum, int32_t nesterov, double weigh
 
 // A call's cost with one pair and with pairs, summed over its matrices.
 void add_cost(Call* c, const Desc& d) {
-    for (int k = 0; k < 2; ++k) c->cost[k] += zero::muon::program_cost(c->n_steps, k != 0, d.M, d.N);
+    for (int k = 0; k < 2; ++k) c->cost[k] += zero::muon::program_cost(c->n_steps, k != 0, std::min(d.rows, d.cols), std::max(d.rows, d.cols));
 }
 
 }  // namespace
@@ -596,7 +929,7 @@ extern "C" zero_status zero_muon_step(float* master, float* momentum, const uint
 // ------------------------------------------------------------ a list of matrices
 
 struct zero_muon_table {
-    void* mem = nullptr;              // descriptors, then the three grids' indexes
+    void* mem = nullptr;              // descriptors, then the grids' indexes
     int device = -1;
     std::vector<Desc> descs;
     Matrices m{};
@@ -618,14 +951,18 @@ zero_status fill_table(zero_muon_table* tab, const char* who) {
     using zero::fail;
     const std::string w(who);
     if (tab->descs.empty()) return ZERO_OK;              // needs no device
+    zero::muon::TileChoice choice;
+    for (const Desc& d : tab->descs) choice.add(1, d.rows, d.cols);
+    tab->m.tile = choice.best();
+    for (Desc& d : tab->descs) zero::muon::shape(&d, d.rows, d.cols, tab->m.tile);
     std::vector<uint32_t> index;
-    size_t starts[3] = {};
-    for (int g = 0; g < 3; ++g) {
+    size_t starts[kGrids] = {};
+    for (int g = 0; g < kGrids; ++g) {
         starts[g] = index.size();
         int64_t total = 0;
         for (size_t i = 0; i < tab->descs.size(); ++i) {
             Desc& d = tab->descs[i];
-            const int64_t n = zero::muon::grid_count(d, g, kTile);
+            const int64_t n = zero::muon::grid_count(d, g, tab->m.tile);
             if (n > kMaxBlocks - total) return fail(ZERO_ERANGE, w + ": more workgroups than one launch holds");
             d.first[g] = static_cast<int32_t>(total);
             index.insert(index.end(), static_cast<size_t>(n), static_cast<uint32_t>(i));
@@ -653,7 +990,7 @@ zero_status fill_table(zero_muon_table* tab, const char* who) {
     if (st != ZERO_OK) return st;
     char* const at = static_cast<char*>(tab->mem);
     tab->m.table = reinterpret_cast<const Desc*>(at);
-    for (int g = 0; g < 3; ++g) tab->m.index[g] = reinterpret_cast<const uint32_t*>(at + table_bytes) + starts[g];
+    for (int g = 0; g < kGrids; ++g) tab->m.index[g] = reinterpret_cast<const uint32_t*>(at + table_bytes) + starts[g];
     st = zero::check_hip(hipMemcpy(at, tab->descs.data(), table_bytes, hipMemcpyHostToDevice),
                          "zero_muon_table_create: hipMemcpy");
     if (st != ZERO_OK) return st;
@@ -694,7 +1031,8 @@ extern "C" zero_status zero_muon_table_create(float* const* masters, float* cons
             d.out = params_out[i];
             d.scale = scales[i];
             if (!d.src || !d.momentum || !d.master || !d.out) return fail(ZERO_EINVAL, of + " has a NULL array");
-            zero::muon::shape(&d, rows[i], cols[i], kTile);
+            d.rows = static_cast<int32_t>(rows[i]);
+            d.cols = static_cast<int32_t>(cols[i]);
             const size_t n = static_cast<size_t>(rows[i] * cols[i]);
             written.push_back({d.master, 4 * n, "master", i});
             written.push_back({d.momentum, 4 * n, "momentum", i});
@@ -706,7 +1044,7 @@ extern "C" zero_status zero_muon_table_create(float* const* masters, float* cons
         if (!clash.empty()) return fail(ZERO_EINVAL, w + ": " + clash);
         // The longest sums first: the tiles dispatched last are then the shortest.
         std::stable_sort(descs.begin(), descs.end(), [](const Desc& a, const Desc& b) {
-            return int64_t(a.M) + a.N > int64_t(b.M) + b.N;
+            return int64_t(a.rows) + a.cols > int64_t(b.rows) + b.cols;
         });
         tab = new zero_muon_table;
         tab->descs = std::move(descs);

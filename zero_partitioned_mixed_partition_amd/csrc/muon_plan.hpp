@@ -91,14 +91,37 @@ struct alignas(128) Desc {
     int32_t M, N;             // the padded short and long side
     int32_t first_partial;    // its first partial sum
     int32_t chunks;
-    int32_t first[3];         // its first workgroup in the momentum pass, the packing and apply, the square products
+    int32_t first[4];         // its first workgroup of each grid
     int32_t id;
 };
 static_assert(sizeof(Desc) == 128, "one 128-byte descriptor per matrix");
 
-enum Grid : int32_t { kByChunk = 0, kByTile = 1, kByPair = 2 };
+// The grids: by chunk of elements (the momentum pass), by kPack x kPack tile (the packing), by product tile of X (an
+// apply) and by product tile of a square matrix's lower triangle.
+enum Grid : int32_t { kByChunk = 0, kByPack = 1, kByTile = 2, kByPair = 3 };
+constexpr int kGrids = 4;
+constexpr int64_t kPack = 64;
+
+// Values from one row of K to the next: an odd number of 256-byte lines, so that the rows of a tile, which are read at the
+// same K, lie in all memory channels (these change every 256 bytes; a power of two of them puts every row in one).
+constexpr int32_t stride(int32_t k) { return ((k + 127) / 128 | 1) * 128; }
 
 inline int64_t pad(int64_t x, int64_t tile) { return (x + tile - 1) / tile * tile; }
+
+// The tile of a call's products, 64, 128 or 256, by an estimate of five steps' time with each (one workgroup of 256 a
+// compute unit, two of 128, more of 64). Sums over K are measured in stages of 64. Larger tiles read less for each
+// product; smaller ones fill the chip from fewer matrices and pad less.
+class TileChoice {
+public:
+    void add(int64_t count, int64_t rows, int64_t cols);
+    int64_t best() const;
+
+private:
+    struct Total {
+        double square = 0, rect = 0;             // tiles
+        double gram = 0, squares = 0, apply = 0; // tiles times stages
+    } total_[3];
+};
 
 // Fills in M, N, chunk and chunks of a matrix of rows x cols.
 void shape(Desc* d, int64_t rows, int64_t cols, int64_t tile);
