@@ -14,7 +14,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libzero_mi355x.so")
 
 SOURCES = ["status.cpp", "plan.cpp", "pieces.cpp", "schedule.cpp", "offload.cpp", "muon_plan.cpp", "adamw.hip",
-           "adamw8.hip", "muon.hip", "reduce.hip", "gather.hip"]
+           "adamw8.hip", "muon.hip", "muon_short.hip", "reduce.hip", "gather.hip"]
 
 # -ffp-contract=off: the AdamW and reduction arithmetic is specified operation
 # by operation; no multiply-add fusion. Packed fp32 instructions are disabled.

@@ -22,145 +22,17 @@
 #include <type_traits>
 #include <vector>
 
-#include "device_common.hpp"
 #include "internal.hpp"
-#include "muon_plan.hpp"
+#include "muon_device.hpp"
+#include "muon_short.hpp"
 #include "pieces.hpp"
 
 #pragma clang fp contract(off)
 
 namespace {
 
-using zero::muon::Desc;
-using zero::muon::Kind;
-using zero::muon::kGrids;
-using zero::muon::stride;
-using zero::muon::Product;
-
-typedef _Float16 f16;
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-constexpr int kThreads = 256;
-using zero::muon::kPack;
-
-// The matrices of one call: a device table of descriptors, or (table NULL) a stack of equal matrices described by its
-// first.
-struct Matrices {
-    const Desc* table;
-    const uint32_t* index[kGrids];    // per grid, the descriptor of each workgroup
-    Desc base;
-    int64_t src_bytes;            // from one matrix of a stack to the next
-    int64_t numel;
-    int64_t area;
-    int64_t tile;                 // of the products: the sides are padded to it
-    uint32_t per[kGrids];         // workgroups of one matrix of a stack, per grid
-    uint32_t total[kGrids];
-    double* partials;
-    float* kappa;
-    char* ws;
-};
-
-// The matrix of workgroup t of a grid, and the workgroup's number within it.
-__device__ __forceinline__ Desc find(const Matrices& m, int grid, uint32_t t, uint32_t* local) {
-    if (m.table != nullptr) {
-        const Desc d = m.table[m.index[grid][t]];
-        *local = t - static_cast<uint32_t>(d.first[grid]);
-        return d;
-    }
-    const uint32_t i = t / m.per[grid];
-    *local = t - i * m.per[grid];
-    Desc d = m.base;
-    const int64_t at = m.numel * i;
-    d.src = static_cast<const char*>(d.src) + m.src_bytes * i;
-    if (d.momentum != nullptr) d.momentum += at;
-    if (d.master != nullptr) d.master += at;
-    d.out += at;
-    d.ws += m.area * i;
-    d.first_partial = d.chunks * static_cast<int32_t>(i);
-    d.id = static_cast<int32_t>(i);
-    return d;
-}
-
-// What the momentum pass computes per element.
-struct MomentumScalars {
-    float mu;
-    int32_t nesterov;
-    const float* clip;            // NULL: 1
-};
-
-__device__ __forceinline__ bool skipped(const float* clip) { return clip != nullptr && !isfinite(*clip); }
-
-// Four consecutive values; the arrays are aligned to their elements only.
-struct __attribute__((packed, aligned(4))) F32x4 {
-    float v[4];
-};
-struct __attribute__((packed, aligned(2))) U16x4 {
-    uint16_t v[4];
-};
-
-// Reads n <= 4 values at element i as fp32 (the rest 0), four at once where n is 4.
-__device__ __forceinline__ void read4(const float* p, int64_t i, int n, float* out) {
-    if (n == 4) {
-        const F32x4 x = *reinterpret_cast<const F32x4*>(p + i);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) out[k] = x.v[k];
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) out[k] = k < n ? p[i + k] : 0.0f;
-    }
-}
-__device__ __forceinline__ void read4(const uint16_t* p, int64_t i, int n, float* out) {
-    if (n == 4) {
-        const U16x4 x = *reinterpret_cast<const U16x4*>(p + i);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) out[k] = zero::dev::bf16_to_f32(x.v[k]);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) out[k] = k < n ? zero::dev::bf16_to_f32(p[i + k]) : 0.0f;
-    }
-}
-
-// Writes n <= 4 values at element i, four at once where n is 4.
-__device__ __forceinline__ void write4(float* p, int64_t i, int n, const float* v) {
-    if (n == 4) {
-        *reinterpret_cast<F32x4*>(p + i) = F32x4{{v[0], v[1], v[2], v[3]}};
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < n) p[i + k] = v[k];
-    }
-}
-__device__ __forceinline__ void write4(uint16_t* p, int64_t i, int n, const uint16_t* v) {
-    if (n == 4) {
-        *reinterpret_cast<U16x4*>(p + i) = U16x4{{v[0], v[1], v[2], v[3]}};
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < n) p[i + k] = v[k];
-    }
-}
-
-// The matrix to orthogonalise at elements i to i + n - 1. kSource: 0 bf16, 1 fp32, 2 momentum and gradient (kUpdate:
-// the momentum is moved on and written first).
-template <int kSource, bool kUpdate>
-__device__ __forceinline__ void input4(const Desc& d, int64_t i, int n, const MomentumScalars& s, float clip, float* u) {
-    if constexpr (kSource == 0) read4(static_cast<const uint16_t*>(d.src), i, n, u);
-    if constexpr (kSource == 1) read4(static_cast<const float*>(d.src), i, n, u);
-    if constexpr (kSource == 2) {
-        float buf[4], g[4] = {};
-        read4(d.momentum, i, n, buf);
-        if (kUpdate || s.nesterov) read4(static_cast<const uint16_t*>(d.src), i, n, g);
-        if constexpr (kUpdate) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) buf[k] = s.mu * buf[k] + g[k] * clip;
-            write4(d.momentum, i, n, buf);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) u[k] = s.nesterov ? g[k] * clip + s.mu * buf[k] : buf[k];
-    }
-}
+using namespace zero::muon;
+using namespace zero::muon::dev;
 
 // Momentum and squared norm: each workgroup takes one chunk of one matrix.
 template <int kSource>
@@ -250,9 +122,10 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(Matrices m, MomentumScal
     for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float y = ldexpf(x[k][j], 13 - e);
-            high[k][j] = static_cast<f16>(y);
-            low[k][j] = static_cast<f16>(y - static_cast<float>(high[k][j]));
+            f16 h, l;
+            split2(ldexpf(x[k][j], 13 - e), &h, &l);
+            high[k][j] = h;
+            low[k][j] = l;
         }
     f16* const along = buffer(m, d, tall ? zero::muon::kT0 : zero::muon::kX);
     f16* const across = buffer(m, d, tall ? zero::muon::kX : zero::muon::kT0);
@@ -281,13 +154,6 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(Matrices m, MomentumScal
             if (!tall) *reinterpret_cast<f16x4*>(rest + at) = turned[1][c * 16 + (right ^ (c / 4))];
     }
 }
-
-// The weight update of the last product's epilogue.
-struct Update {
-    double lr;
-    float decay;                  // 1 - lr * weight_decay
-    const float* clip;
-};
 
 // A product's tile and its waves: kRows x kCols waves, each of MI x NI MFMA tiles of 32 x 32.
 template <int T>
@@ -319,31 +185,6 @@ typedef __attribute__((address_space(3))) void lds_void;
 template <int n>
 __device__ __forceinline__ void landed_and_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(n) : "memory");
-}
-
-// The four values of one column in each lane of a quad (two in each word), as one row's four columns in each.
-__device__ __forceinline__ f16x4 quad_transpose(f16x4 v) {
-    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-    u32x2_t w = __builtin_bit_cast(u32x2_t, v);
-    const uint32_t lane = threadIdx.x;
-    // lanes 2k and 2k + 1: (r0 r1 | r2 r3) of two columns -> rows 0 / 1 and 2 / 3 of both
-    const bool odd = lane & 1;
-    // what the neighbour needs of this lane: an even lane's odd rows, an odd lane's even rows
-    const uint32_t give = odd ? __builtin_amdgcn_perm(w.y, w.x, 0x05040100) : __builtin_amdgcn_perm(w.y, w.x, 0x07060302);
-    const uint32_t keep = odd ? __builtin_amdgcn_perm(w.y, w.x, 0x07060302) : __builtin_amdgcn_perm(w.y, w.x, 0x05040100);
-    const uint32_t got = __builtin_amdgcn_mov_dpp(give, 0xB1, 0xF, 0xF, true);       // quad_perm 1 0 3 2
-    // keep: this lane's rows (0, 2) or (1, 3); got: the neighbour's same rows. Columns in order: even lane first.
-    const uint32_t left = odd ? got : keep, right = odd ? keep : got;
-    uint32_t a = __builtin_amdgcn_perm(right, left, 0x05040100);     // row 0 (1), two columns
-    uint32_t b = __builtin_amdgcn_perm(right, left, 0x07060302);     // row 2 (3)
-    // lanes q and q ^ 2: row 0 (1) stays in lanes 0, 1; row 2 (3) goes to lanes 2, 3
-    const bool high = lane & 2;
-    const uint32_t give2 = high ? a : b;
-    const uint32_t got2 = __builtin_amdgcn_mov_dpp(give2, 0x4E, 0xF, 0xF, true);     // quad_perm 2 3 0 1
-    u32x2_t out;
-    out.x = high ? got2 : a;
-    out.y = high ? b : got2;
-    return __builtin_bit_cast(f16x4, out);
 }
 
 // Tile t of a matrix of `rows` x `cols` tiles, in strips of kStrip rows, column by column within a strip: 32 tiles
@@ -653,25 +494,10 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
                 const int32_t row_at = bi * T + row_in;
                 const int64_t first = static_cast<int64_t>(row_at) * d.cols + c;
                 const int here = row_at < d.rows ? n : 0;
-                typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-                const u16x8 o = __builtin_bit_cast(u16x8, *reinterpret_cast<const f16x8*>(lds + place(row_in, own_piece * 2)));
+                const f16x8 o = *reinterpret_cast<const f16x8*>(lds + place(row_in, own_piece * 2));
                 uint16_t bits[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if constexpr (kEnd == 1) {
-                        bits[k] = o[k];
-                    } else {
-                        w[r][k] = w[r][k] * u.decay;
-                        w[r][k] = w[r][k] - rate * zero::dev::bf16_to_f32(o[k]);
-                        bits[k] = static_cast<uint16_t>(zero::dev::f32_to_bf16(w[r][k]));
-                    }
-                }
-                if constexpr (kEnd == 2) {
-                    write4(d.master, first, here < 4 ? here : 4, w[r]);
-                    write4(d.master, first + 4, here < 4 ? 0 : here - 4, w[r] + 4);
-                }
-                write4(d.out, first, here < 4 ? here : 4, bits);
-                write4(d.out, first + 4, here < 4 ? 0 : here - 4, bits + 4);
+                __builtin_memcpy(bits, &o, sizeof(bits));
+                finish8<kEnd>(d, u, rate, first, here, bits, w[r]);
             }
         }
     }
@@ -736,7 +562,12 @@ zero_status launch_all(const Matrices& m, const Call& c, const std::vector<Produ
 }
 
 zero_status launch(const Matrices& m, const Call& c, hipStream_t stream, const char* who) {
+    ShortProgram steps;
+    if (m.side != 0 && make_short_program(c.coefficients, c.n_steps, &steps))
+        return launch_short(c.source, m, c.momentum, c.update, steps, c.eps, stream, who);
     std::vector<Product> program;
+    // Pairs where they save a twentieth of the multiplications or more: at equal cost the single steps, whose A comes
+    // from X itself, are more exact (about 1.2e-3 of the result's norm against 1.2e-3 to 1.9e-3).
     const bool pairs = c.cost[1] < 0.95 * c.cost[0];
     try {
         const zero_status st = zero::muon::make_program(c.coefficients, c.n_steps, pairs, c.source != 0, &program, who);
@@ -779,6 +610,8 @@ zero_status measure_stack(int64_t count, int64_t rows, int64_t cols, Matrices* m
     choice.add(count, rows, cols);
     m->tile = choice.best();
     zero::muon::shape(&m->base, rows, cols, m->tile);
+    m->side = short_side(std::min(rows, cols));
+    m->base.parts = m->side != 0 ? short_parts(m->side, std::max(rows, cols), count) : 1;
     m->numel = rows * cols;
     m->area = zero::muon::area_bytes(m->base);
     for (int g = 0; g < kGrids; ++g) {
@@ -788,15 +621,23 @@ zero_status measure_stack(int64_t count, int64_t rows, int64_t cols, Matrices* m
         m->per[g] = static_cast<uint32_t>(per);
         m->total[g] = static_cast<uint32_t>(per * count);
     }
+    m->matrices = static_cast<uint32_t>(count);
     const int64_t head = zero::muon::head_bytes(count * m->base.chunks, count);
     if (count > (INT64_MAX - head) / m->area) return zero::fail(ZERO_ERANGE, std::string(who) + ": workspace overflows");
     *bytes = head + count * m->area;
     m->base.ws = head;
+    if (m->side != 0) {
+        m->base.short_ws = short_head_bytes(m->total[kByPart], count);
+        m->short_area = short_area_bytes(m->side, m->base.parts);
+        *bytes = std::max(*bytes, m->base.short_ws + count * m->short_area);
+    }
     return ZERO_OK;
 }
 
 void place(Matrices* m, void* workspace, int64_t partials) {
     m->ws = static_cast<char*>(workspace);
+    m->part_exponent = static_cast<int32_t*>(workspace);
+    m->short_scale = reinterpret_cast<ShortScale*>(m->ws + short_scales_at(m->total[kByPart]));
     m->partials = static_cast<double*>(workspace);
     m->kappa = reinterpret_cast<float*>(m->partials + partials);
 }
@@ -954,7 +795,14 @@ zero_status fill_table(zero_muon_table* tab, const char* who) {
     zero::muon::TileChoice choice;
     for (const Desc& d : tab->descs) choice.add(1, d.rows, d.cols);
     tab->m.tile = choice.best();
-    for (Desc& d : tab->descs) zero::muon::shape(&d, d.rows, d.cols, tab->m.tile);
+    int64_t most = 0;
+    for (const Desc& d : tab->descs) most = std::max<int64_t>(most, std::min(d.rows, d.cols));
+    tab->m.side = short_side(most);
+    tab->m.matrices = static_cast<uint32_t>(tab->descs.size());
+    for (Desc& d : tab->descs) {
+        zero::muon::shape(&d, d.rows, d.cols, tab->m.tile);
+        d.parts = tab->m.side != 0 ? short_parts(tab->m.side, std::max(d.rows, d.cols), tab->m.matrices) : 1;
+    }
     std::vector<uint32_t> index;
     size_t starts[kGrids] = {};
     for (int g = 0; g < kGrids; ++g) {
@@ -982,6 +830,14 @@ zero_status fill_table(zero_muon_table* tab, const char* who) {
         const int64_t area = zero::muon::area_bytes(d);
         if (area > INT64_MAX - tab->bytes) return fail(ZERO_ERANGE, w + ": workspace overflows");
         tab->bytes += area;
+    }
+    if (tab->m.side != 0) {
+        int64_t bytes = short_head_bytes(tab->m.total[kByPart], tab->m.matrices);
+        for (Desc& d : tab->descs) {
+            d.short_ws = bytes;
+            bytes += short_area_bytes(tab->m.side, d.parts);
+        }
+        tab->bytes = std::max(tab->bytes, bytes);
     }
     zero_status st = zero::check_hip(hipGetDevice(&tab->device), "zero_muon_table_create: hipGetDevice");
     if (st != ZERO_OK) return st;

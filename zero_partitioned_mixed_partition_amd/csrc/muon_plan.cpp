@@ -107,6 +107,54 @@ zero_status make_program(const double* coefficients, int32_t n_steps, bool pairs
     return ZERO_OK;
 }
 
+bool make_short_program(const double* coefficients, int32_t n_steps, ShortProgram* out) {
+    *out = ShortProgram{};
+    out->n_steps = n_steps;
+    double x[kSamples + 1], q[kSamples + 1];         // eigenvalues of A, and of Q
+    double top = 1.0, growth = 1.0;
+    for (int i = 0; i <= kSamples; ++i) x[i] = static_cast<double>(i) / kSamples, q[i] = 1.0;
+    int eA = exponent_for(top), eQ = 0;
+    out->first = std::ldexp(1.0, eA);
+    for (int32_t at = 0; at < n_steps; ++at) {
+        const double a = coefficients[3 * at], b = coefficients[3 * at + 1], c = coefficients[3 * at + 2];
+        double most_c = 0.0, most_t = 0.0, most_a = 0.0, most_q = 0.0;
+        for (int i = 0; i <= kSamples; ++i) {
+            const double p = a + x[i] * (b + x[i] * c);
+            most_c = std::max(most_c, std::fabs(p));
+            most_t = std::max(most_t, std::fabs(x[i] * p));
+            x[i] *= p * p;
+            q[i] *= p;
+            most_a = std::max(most_a, x[i]);
+            most_q = std::max(most_q, std::fabs(q[i]));
+        }
+        // small negative eigenvalues, which roundings make, grow by a^2
+        if (at + 1 < n_steps) growth *= std::max(1.0, std::max(a * a, most_c * most_c));
+        if (!(growth <= 65536.0) || !(most_a <= 1024.0) || !(most_q <= 65536.0)) return false;
+        const double margin = std::pow(1.02, at + 1);
+        const int eC = exponent_for(most_c * margin), eT = exponent_for(most_t * margin),
+                  eN = exponent_for(most_a * margin), eP = at == 0 ? eC : exponent_for(most_q * margin);
+        ShortStep& s = out->step[at];
+        s.a = static_cast<float>(a * pow2(eC));
+        s.b = static_cast<float>(b * pow2(eC - eA));
+        s.c = static_cast<float>(c * pow2(eC - 2 * eA));
+        s.t = pow2(eT - eC - eA);
+        s.next = pow2(eN - eT - eC);
+        s.q = pow2(eP - eC - eQ);
+        eA = eN;
+        eQ = eP;
+    }
+    out->last = pow2(-eQ);
+    return true;
+}
+
+int32_t short_parts(int32_t side, int64_t n, int64_t count) {
+    const int64_t chunks = (n + 63) / 64;
+    const double per = side == 64 ? 2.4 : side == 96 ? 1.6 : 1.2, least = side == 64 ? 16 : side == 96 ? 12 : 8;
+    const int64_t parts = static_cast<int64_t>(std::max(least, per * std::sqrt(static_cast<double>(chunks))));
+    const int64_t room = std::max<int64_t>(1, 2048 / std::max<int64_t>(count, 1));
+    return static_cast<int32_t>(std::min({chunks, parts, room, int64_t(256)}));
+}
+
 namespace {
 
 constexpr int64_t kTiles[3] = {64, 128, 256};
@@ -173,6 +221,7 @@ int64_t grid_count(const Desc& d, int grid, int64_t tile) {
         case kByChunk: return d.chunks;
         case kByPack: return (d.M / kPack) * (d.N / kPack);
         case kByTile: return m * n;
+        case kByPart: return d.parts;
         default: return m * (m + 1) / 2;
     }
 }

@@ -91,15 +91,17 @@ struct alignas(128) Desc {
     int32_t M, N;             // the padded short and long side
     int32_t first_partial;    // its first partial sum
     int32_t chunks;
-    int32_t first[4];         // its first workgroup of each grid
+    int32_t first[5];         // its first workgroup of each grid
     int32_t id;
+    int32_t parts;            // workgroups that share its sums over the long side, where the short side is at most 128
+    int64_t short_ws;         // byte offset of what they use
 };
 static_assert(sizeof(Desc) == 128, "one 128-byte descriptor per matrix");
 
 // The grids: by chunk of elements (the momentum pass), by kPack x kPack tile (the packing), by product tile of X (an
-// apply) and by product tile of a square matrix's lower triangle.
-enum Grid : int32_t { kByChunk = 0, kByPack = 1, kByTile = 2, kByPair = 3 };
-constexpr int kGrids = 4;
+// apply), by product tile of a square matrix's lower triangle, and by part of the long side.
+enum Grid : int32_t { kByChunk = 0, kByPack = 1, kByTile = 2, kByPair = 3, kByPart = 4 };
+constexpr int kGrids = 5;
 constexpr int64_t kPack = 64;
 
 // Values from one row of K to the next: an odd number of 256-byte lines, so that the rows of a tile, which are read at the
@@ -131,6 +133,44 @@ int64_t grid_count(const Desc& d, int grid, int64_t tile);
 
 // Bytes of a matrix's arrays (kLow at the end, where the input is fp32).
 int64_t area_bytes(const Desc& d);
+
+// ------------------------------------------------------------ matrices with a short side of at most 128
+//
+// A = X X^T of such a matrix fits a compute unit's LDS. All steps are then taken on A alone, as one group, in two fp16
+// parts a value (22 bits), and X is read twice: for A, and for the last product with Q = C_n ... C_1.
+
+// 64, 96 or 128 for a short side up to that, else 0.
+inline int32_t short_side(int64_t m) { return m <= 64 ? 64 : m <= 96 ? 96 : m <= 128 ? 128 : 0; }
+
+// One step's factors: C = a + b A + c A^2, then T, the next A and Q from products of what is held.
+struct ShortStep {
+    float a, b, c, t, next, q;
+};
+struct ShortProgram {
+    int32_t n_steps;
+    double first;             // what A is held times
+    float last;               // the result is Q X times this
+    ShortStep step[kMaxSteps];
+};
+
+// Whether the steps can be taken as one group: what rounding A leaves in a direction that the matrix does not have grows
+// with the square of each step's a, and must stay well below 1.
+bool make_short_program(const double* coefficients, int32_t n_steps, ShortProgram* out);
+
+// Parts of a matrix whose longer side is n, one of `count`: as many as make the sums' two halves (a part's run along
+// the long side, and one workgroup's sum over the parts) take equally long, within a chip's worth of workgroups.
+int32_t short_parts(int32_t side, int64_t n, int64_t count);
+
+// Bytes of a matrix's Q and parts (with side 128 two more Qs, which a step reads and writes).
+constexpr int64_t short_area_bytes(int32_t side, int64_t parts) {
+    return 4 * int64_t(side) * side * (parts + (side == 128 ? 3 : 1));
+}
+
+// Bytes at the start of the workspace: the parts' exponents, and an exponent and factor per matrix.
+inline int64_t short_scales_at(int64_t parts) { return (4 * parts + 7) / 8 * 8; }
+inline int64_t short_head_bytes(int64_t parts, int64_t matrices) {
+    return (short_scales_at(parts) + 8 * matrices + 255) / 256 * 256;
+}
 
 // Bytes at the workspace's start: the partial sums and a factor per matrix.
 int64_t head_bytes(int64_t partials, int64_t matrices);
