@@ -119,14 +119,11 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(Matrices m, MomentumScal
 
     f16x4 high[4], low[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 4; ++k) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f16 h, l;
-            split2(ldexpf(x[k][j], 13 - e), &h, &l);
-            high[k][j] = h;
-            low[k][j] = l;
-        }
+        for (int j = 0; j < 4; ++j) x[k][j] = ldexpf(x[k][j], 13 - e);
+        split4(x[k][0], x[k][1], x[k][2], x[k][3], &high[k], &low[k]);
+    }
     f16* const along = buffer(m, d, tall ? zero::muon::kT0 : zero::muon::kX);
     f16* const across = buffer(m, d, tall ? zero::muon::kX : zero::muon::kT0);
     f16* const rest = buffer(m, d, zero::muon::kLow);                  // [N][M], as kT0

@@ -80,14 +80,18 @@ __device__ __forceinline__ Desc find(const Matrices& m, int grid, uint32_t t, ui
     return matrix(m, i);
 }
 
-// x as two fp16 values, hi + lo (22 bits of x). x goes through a register of its own: the compiler may otherwise fold the
-// product that x is into one of the two conversions of hi (the stored one and the subtracted one), which then round
-// apart now and then.
-__device__ __forceinline__ void split2(float x, f16* hi, f16* lo) {
-    asm("" : "+v"(x));
-    const f16 h = static_cast<f16>(x);
-    *hi = h;
-    *lo = static_cast<f16>(x - static_cast<float>(h));
+// Four values as two fp16 parts each, hi + lo (22 bits). They go through registers of their own: the compiler may otherwise
+// fold the product that a value is into one of the two conversions to hi (the stored one and the subtracted one), which
+// then round apart now and then.
+__device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, f16x4* hi, f16x4* lo) {
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    asm("" : "+v"(x0), "+v"(x1), "+v"(x2), "+v"(x3));
+    const f16x2 a = __builtin_convertvector((f32x2{x0, x1}), f16x2), b = __builtin_convertvector((f32x2{x2, x3}), f16x2);
+    const f16x2 c = __builtin_convertvector((f32x2{x0 - static_cast<float>(a.x), x1 - static_cast<float>(a.y)}), f16x2),
+                d = __builtin_convertvector((f32x2{x2 - static_cast<float>(b.x), x3 - static_cast<float>(b.y)}), f16x2);
+    *hi = f16x4{a.x, a.y, b.x, b.y};
+    *lo = f16x4{c.x, c.y, d.x, d.y};
 }
 
 // What the momentum pass computes per element.

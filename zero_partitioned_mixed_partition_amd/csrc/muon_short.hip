@@ -69,14 +69,10 @@ __device__ __forceinline__ void split(const Held<M>& h, bool tall, int shift, in
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             f16x4 hi, lo;
+            float x[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float x = ldexpf(as_held ? h.v[i][k][j] : h.v[i][j][k], shift);
-                f16 h, l;
-                split2(x, &h, &l);
-                hi[j] = h;
-                lo[j] = l;
-            }
+            for (int j = 0; j < 4; ++j) x[j] = ldexpf(as_held ? h.v[i][k][j] : h.v[i][j][k], shift);
+            split4(x[0], x[1], x[2], x[3], &hi, &lo);
             f16* const at = to + ((as_held ? down : right) * 4 + k) * ld + (as_held ? right : down) * 4;
             *reinterpret_cast<f16x4*>(at) = hi;
             if constexpr (kLow) *reinterpret_cast<f16x4*>(at + part) = lo;
@@ -159,29 +155,44 @@ __device__ __forceinline__ void gram(const Matrices& m, const MomentumScalars& s
     }
 }
 
-// All steps of one matrix, on A; a wave for each 32 x 32 block.
+// A wave's 32 x 32 blocks of an M x M matrix: one, or with M = 128, where a wave for each would read LDS too often, two side
+// by side.
+template <int M>
+struct ChainShape {
+    static constexpr int kBlocks = M == 128 ? 2 : 1, kAcross = M / 32 / kBlocks, kWaves = M / 32 * kAcross;
+};
+
+// All steps of one matrix, on A.
 template <int M>
 __device__ __forceinline__ void chain(const Matrices& m, const ShortProgram& program, double eps, const float* clip) {
-    constexpr int B = M / 32, kWaves = B * B, LD = M + 8, kPart = M * LD, kSlot = 2 * kPart;
+    constexpr int NB = ChainShape<M>::kBlocks, kWaves = ChainShape<M>::kWaves, LD = M + 8, kPart = M * LD, kSlot = 2 * kPart;
     constexpr bool kGlobalQ = M == 128;                  // three matrices of two parts do not fit the LDS
     __shared__ __align__(16) f16 lds[(kGlobalQ ? 2 : 3) * kSlot];
     __shared__ double traces[kWaves];
     if (skipped(clip)) return;
     const Desc d = matrix(m, blockIdx.x);
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, bi = wave / B, bj = wave % B;
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int bi = wave / ChainShape<M>::kAcross, bj = wave % ChainShape<M>::kAcross * NB;      // blocks bi, bj + n
+    struct Blocks {
+        f32x16 v[NB];
+    };
     int e = kEmpty;
     for (int p = 0; p < d.parts; ++p) e = max(e, m.part_exponent[d.first[kByPart] + p]);
-    f32x16 a = {};
-    const float* parts = reinterpret_cast<const float*>(m.ws + d.short_ws + short_area_bytes(M, 0)) + (wave * 64 + lane) * 16;
+    Blocks a = {};
+    const float* parts = reinterpret_cast<const float*>(m.ws + d.short_ws + short_area_bytes(M, 0));
+    parts += ((bi * (M / 32) + bj) * 64 + lane) * 16;
 #pragma unroll 4
-    for (int p = 0; p < d.parts; ++p, parts += M * M)
-        a += *reinterpret_cast<const f32x16*>(parts) * ldexpf(1.0f, 2 * (m.part_exponent[d.first[kByPart] + p] - e));
+    for (int p = 0; p < d.parts; ++p, parts += M * M) {
+        const float scale = ldexpf(1.0f, 2 * (m.part_exponent[d.first[kByPart] + p] - e));
+#pragma unroll
+        for (int n = 0; n < NB; ++n) a.v[n] += *reinterpret_cast<const f32x16*>(parts + n * 1024) * scale;
+    }
     double trace = 0.0;
-    if (bi == bj) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-            if (block_row(k) == lane % 32) trace += a[k];
-    }
+            if (bi == bj + n && block_row(k) == lane % 32) trace += a.v[n][k];
     trace = ::zero::dev::wave_sum(trace);
     if (lane == 0) traces[wave] = trace;
     __syncthreads();
@@ -197,75 +208,100 @@ __device__ __forceinline__ void chain(const Matrices& m, const ShortProgram& pro
         factor = __builtin_nan("");
     }
     if (threadIdx.x == 0) m.short_scale[d.id] = ShortScale{trace == 0.0 ? 0 : e, static_cast<float>(factor)};
-    a *= static_cast<float>(factor * factor * program.first);
+    const float unit_a = static_cast<float>(factor * factor * program.first);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) a.v[n] *= unit_a;
 
     f16* const final_q = reinterpret_cast<f16*>(m.ws + d.short_ws);
     // times() takes its right factor's columns, so a matrix is stored by rows as a left factor and by columns as a right
     // one. All are symmetric but for roundings, but with A' = C A C^T and Q' = C Q in this order the roundings of C cancel
-    // (A' stays the A of Q' X); with A C C they grow by a^2 a step (1e-3 of the result against 1e-5).
+    // (A' stays the A of Q' X); with A C C they grow by a^2 a step (1e-3 of the result against 3e-5).
+    // A lane holds a row's values where the factors are swapped in the MFMA, a column's where not: it writes four at once.
     constexpr std::true_type kByRows{};
     constexpr std::false_type kByColumns{};
-    auto put = [&](auto by_rows, f32x16 x, f16* to, int ld, int part) {
+    // The lane's values: with turned those of row (or column) 32 (bj + n) + lane % 32 from place 32 bi on, else the other way.
+    auto put = [&](bool turned, const Blocks& x, f16* to, int ld, int part) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            f16x4 hi, lo;
+        for (int n = 0; n < NB; ++n) {
+            f16* const at = to + ((turned ? bj + n : bi) * 32 + lane % 32) * ld + (turned ? bi : bj + n) * 32 + lane / 32 * 4;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                f16 h, l;
-                split2(x[q * 4 + k], &h, &l);
-                hi[k] = h;
-                lo[k] = l;
+            for (int q = 0; q < 4; ++q) {
+                f16x4 hi, lo;
+                split4(x.v[n][q * 4], x.v[n][q * 4 + 1], x.v[n][q * 4 + 2], x.v[n][q * 4 + 3], &hi, &lo);
+                *reinterpret_cast<f16x4*>(at + q * 8) = hi;
+                *reinterpret_cast<f16x4*>(at + q * 8 + part) = lo;
             }
-            const int r = bi * 32 + q * 8 + lane / 32 * 4, c = bj * 32 + lane % 32;
-            f16* const at = by_rows ? to + (r + lane % 4) * ld + c - lane % 4 : to + c * ld + r;
-            *reinterpret_cast<f16x4*>(at) = by_rows ? quad_transpose(hi) : hi;
-            *reinterpret_cast<f16x4*>(at + part) = by_rows ? quad_transpose(lo) : lo;
         }
     };
-    auto times = [&](const f16* x, const f16* y, int y_ld, int y_part) {
-        f32x16 acc = {};
-        x += (bi * 32 + lane % 32) * LD + lane / 32 * 8;
-        y += (bj * 32 + lane % 32) * y_ld + lane / 32 * 8;
+    // The blocks bi, bj + n (turned: bj + n, bi) of x y, from the rows of x and the columns of y.
+    auto times = [&](auto by_rows, bool turned, const f16* x, const f16* y, int y_ld, int y_part, float scale) {
+        Blocks sum = {};
 #pragma unroll
         for (int kk = 0; kk < M / 16; ++kk) {
-            const f16x8 xh = *reinterpret_cast<const f16x8*>(x + kk * 16), xl = *reinterpret_cast<const f16x8*>(x + kPart + kk * 16);
-            const f16x8 yh = *reinterpret_cast<const f16x8*>(y + kk * 16), yl = *reinterpret_cast<const f16x8*>(y + y_part + kk * 16);
-            acc = mfma(xh, yh, mfma(xl, yh, mfma(xh, yl, acc)));
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const f16* const xr = x + ((turned ? bj + n : bi) * 32 + lane % 32) * LD + lane / 32 * 8 + kk * 16;
+                const f16* const yr = y + ((turned ? bi : bj + n) * 32 + lane % 32) * y_ld + lane / 32 * 8 + kk * 16;
+                const f16x8 xh = *reinterpret_cast<const f16x8*>(xr), xl = *reinterpret_cast<const f16x8*>(xr + kPart);
+                const f16x8 yh = *reinterpret_cast<const f16x8*>(yr), yl = *reinterpret_cast<const f16x8*>(yr + y_part);
+                f32x16& s = sum.v[n];
+                s = by_rows ? mfma(yl, xh, s) : mfma(xh, yl, s);
+                s = by_rows ? mfma(yh, xl, s) : mfma(xl, yh, s);
+                s = by_rows ? mfma(yh, xh, s) : mfma(xh, yh, s);
+            }
         }
-        return acc;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) sum.v[n] *= scale;
+        return sum;
     };
     f16* const slot_a = lds;
     f16* const slot_c = lds + kSlot;
     constexpr int kQLd = kGlobalQ ? M : LD, kQPart = kGlobalQ ? M * M : kPart;
     // Q: in LDS, or the matrix of this step and of the next in turn.
     auto slot_q = [&](int step) { return kGlobalQ ? final_q + (1 + step % 2) * 2 * M * M : lds + 2 * kSlot; };
-    put(kByColumns, a, slot_a, LD, kPart);
+    put(true, a, slot_a, LD, kPart);
     for (int32_t i = 0; i < program.n_steps; ++i) {
         const ShortStep& s = program.step[i];
         const bool last = i + 1 == program.n_steps;
         __syncthreads();
-        f32x16 c = times(slot_a, slot_a, LD, kPart) * s.c;
+        // Turned blocks by rows: A is symmetric, so the lane's values of A, of a column, are those of the row it needs.
+        Blocks c = times(kByRows, true, slot_a, slot_a, LD, kPart, s.c);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            c[k] += s.b * a[k];
-            if (bi == bj && block_row(k) == lane % 32) c[k] += s.a;
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                c.v[n][k] += s.b * a.v[n][k];
+                if (bi == bj + n && block_row(k) == lane % 32) c.v[n][k] += s.a;
+            }
+        put(true, c, slot_c, LD, kPart);
+        if (i == 0 && last) put(true, c, final_q, M, M * M);
+        __syncthreads();
+        Blocks t = {}, q = {};
+        if (last) {
+            if (i > 0) q = times(kByRows, false, slot_c, slot_q(i - 1), kQLd, kQPart, s.q);
+        } else {
+            t = times(kByRows, false, slot_c, slot_a, LD, kPart, s.t);
+            if (i > 0) q = times(kByColumns, false, slot_c, slot_q(i - 1), kQLd, kQPart, s.q);
         }
-        put(kByRows, c, slot_c, LD, kPart);
-        if (i == 0 && last) put(kByRows, c, final_q, M, M * M);
-        if (i == 0 && !last) put(kByColumns, c, slot_q(0), kQLd, kQPart);
         __syncthreads();
-        f32x16 t = {}, q = {};
-        if (i > 0) q = times(slot_c, slot_q(i - 1), kQLd, kQPart) * s.q;
-        if (!last) t = times(slot_c, slot_a, LD, kPart) * s.t;
+        if (last) {
+            if (i > 0) put(false, q, final_q, M, M * M);
+            break;
+        }
+        if (i > 0) put(true, q, slot_q(i), kQLd, kQPart);
+        if (i == 0) {                                    // Q = C, by columns
+            for (int at = threadIdx.x; at < 2 * M * M / 4; at += kWaves * 64) {
+                const int r = at / (M * M / 4), c4 = at / M % (M / 4) * 4, column = at % M;
+                const f16* const from = slot_c + r * kPart + c4 * LD + column;
+                *reinterpret_cast<f16x4*>(slot_q(0) + r * kQPart + column * kQLd + c4) =
+                    f16x4{from[0], from[LD], from[2 * LD], from[3 * LD]};
+            }
+        }
+        put(false, t, slot_a, LD, kPart);
         __syncthreads();
-        if (i > 0 && last) put(kByRows, q, final_q, M, M * M);
-        if (last) break;
-        if (i > 0) put(kByColumns, q, slot_q(i), kQLd, kQPart);
-        put(kByRows, t, slot_a, LD, kPart);
+        a = times(kByColumns, false, slot_a, slot_c, LD, kPart, s.next);
         __syncthreads();
-        a = times(slot_a, slot_c, LD, kPart) * s.next;
-        __syncthreads();
-        put(kByColumns, a, slot_a, LD, kPart);
+        put(true, a, slot_a, LD, kPart);
     }
 }
 
@@ -358,7 +394,7 @@ __global__ __launch_bounds__(kThreads) void short_gram_kernel(Matrices m, Moment
 }
 
 template <int M>
-__global__ __launch_bounds__(M / 32 * (M / 32) * 64) void short_chain_kernel(Matrices m, ShortProgram program, double eps,
+__global__ __launch_bounds__(64 * ChainShape<M>::kWaves) void short_chain_kernel(Matrices m, ShortProgram program, double eps,
                                                                             const float* clip) {
     chain<M>(m, program, eps, clip);
 }
@@ -375,7 +411,7 @@ zero_status launch(const Matrices& m, const MomentumScalars& s, const Update& u,
     hipLaunchKernelGGL((short_gram_kernel<M, kSource>), parts, dim3(kThreads), 0, stream, m, s);
     zero_status st = zero::check_hip(hipGetLastError(), who);
     if (st != ZERO_OK) return st;
-    hipLaunchKernelGGL((short_chain_kernel<M>), dim3(m.matrices), dim3(M / 32 * (M / 32) * 64), 0, stream, m, program, eps, s.clip);
+    hipLaunchKernelGGL((short_chain_kernel<M>), dim3(m.matrices), dim3(64 * ChainShape<M>::kWaves), 0, stream, m, program, eps, s.clip);
     st = zero::check_hip(hipGetLastError(), who);
     if (st != ZERO_OK) return st;
     hipLaunchKernelGGL((short_apply_kernel<M, kSource, kSource == 2 ? 2 : 1>), parts, dim3(kThreads), 0, stream, m, s, u,
