@@ -24,7 +24,7 @@ parameter all-gather.
 from __future__ import annotations
 
 from dataclasses import dataclass
-from typing import List, Optional, Sequence, Tuple
+from typing import Dict, List, Optional, Sequence, Tuple
 
 import torch
 
@@ -42,6 +42,21 @@ class Hyper:
     def as_kwargs(self) -> dict:
         return dict(lr=self.lr, beta1=self.beta1, beta2=self.beta2, eps=self.eps,
                     weight_decay=self.weight_decay)
+
+
+@dataclass
+class MuonHyper:
+    """Muon's settings (zero_muon_step); the rate of a matrix is lr times muon_scale of its sides."""
+    lr: float = 1e-3
+    momentum: float = 0.95
+    nesterov: bool = True
+    weight_decay: float = 0.01
+    eps: float = 1e-7
+    coefficients: Sequence[Tuple[float, float, float]] = zb.MUON_COEFFICIENTS
+
+    def as_kwargs(self) -> dict:
+        return dict(lr=self.lr, momentum=self.momentum, nesterov=self.nesterov, weight_decay=self.weight_decay,
+                    eps=self.eps, coefficients=self.coefficients)
 
 
 class RankStep:
@@ -86,6 +101,14 @@ class RankStep:
                  byte per 128 elements (zero_shard_adamw8_step; 10 bytes a
                  parameter with the gradient instead of 16). Every form of the step but
                  offload; load_moments() and moments() convert from and to fp32.
+    muon         a MuonHyper, with per_param: the tensors of muon_shapes (their index
+                 in the plan's list -> (rows, cols)) are weight matrices that Muon
+                 updates, all others AdamW. An update needs its whole matrix, so
+                 a matrix must lie in one rank's shard (ValueError where this rank
+                 holds a part of one): where tensors are dealt to ranks whole, a
+                 rank's plan is that of its own tensors with n_ranks=1. A matrix's
+                 momentum is its exp_avg_tensors entry, its exp_avg_sq_tensors
+                 entry is empty. fp32 state only.
     seed         with state_bits=8, the run's seed of the stochastic rounding (the
                  same on every rank: each rank draws the words of its own place in
                  the flat buffer).
@@ -103,7 +126,8 @@ class RankStep:
                  device: torch.device, gather: bool = True, offload: bool = False,
                  offload_chunk: int = 1 << 21, host_threads: int = 0, fuse: bool = True,
                  per_param: bool = False, device_step: bool = False, state_bits: int = 32,
-                 seed: int = 0):
+                 seed: int = 0, muon: Optional[MuonHyper] = None,
+                 muon_shapes: Optional[Dict[int, Tuple[int, int]]] = None):
         if per_param and offload:
             raise ValueError("per-parameter state and ZeRO-Offload are separate layouts")
         if device_step and offload:
@@ -112,6 +136,12 @@ class RankStep:
             raise ValueError("state_bits is 8 or 32")
         if state_bits == 8 and offload:
             raise ValueError("ZeRO-Offload's host update takes fp32 moments")
+        if muon is None and muon_shapes:
+            raise ValueError("muon_shapes without Muon's settings")
+        if muon is not None and not per_param:
+            raise ValueError("Muon updates whole matrices: per-parameter state only")
+        if muon is not None and state_bits != 32:
+            raise ValueError("Muon's momentum is fp32: state_bits is 32 with it")
         self.state_bits, self.seed = state_bits, seed
         self.plan, self.rank, self.hyper, self.max_norm = plan, rank, hyper, max_norm
         self.device = device
@@ -122,6 +152,8 @@ class RankStep:
         # moved STAGGER bytes past the previous end (the value measured best
         # on MI355X; see STAGGER).
         self.segments = plan.segments(rank) if per_param else []
+        self.muon = muon
+        self.muon_segments = _whole_matrices(plan, self.segments, muon_shapes or {})
         moment = torch.float32 if state_bits == 32 else torch.uint8
         self.exp_avg_scale = self.exp_avg_sq_scale = None
         if per_param:
@@ -131,7 +163,8 @@ class RankStep:
             lens = [ln for (_, _, _, ln) in self.segments]
             self.master_tensors = [torch.zeros(n, dtype=torch.float32, device=device) for n in lens]
             self.exp_avg_tensors = [torch.zeros(n, dtype=moment, device=device) for n in lens]
-            self.exp_avg_sq_tensors = [torch.zeros(n, dtype=moment, device=device) for n in lens]
+            self.exp_avg_sq_tensors = [torch.zeros(0 if i in self.muon_segments else n, dtype=moment, device=device)
+                                       for i, n in enumerate(lens)]
             if state_bits == 8:
                 self.exp_avg_scale_tensors = [torch.zeros(zb.state8_blocks(n), dtype=torch.uint8, device=device)
                                               for n in lens]
@@ -232,6 +265,9 @@ class RankStep:
         lowers self.t.)"""
         self.t += 1
         clip = self.scale if self.max_norm > 0 else None
+        if self.muon_segments:                           # independent of AdamW's part, and before its step is counted
+            self._prepared("muon", stream, lambda st: self._muon_table().prepare_step(
+                clip_scale=clip, stream=st, **self.muon.as_kwargs()))()
         if self.state_bits == 8:
             self._adamw8(clip, stream)
             return
@@ -355,9 +391,19 @@ class RankStep:
         """The per-parameter state's device table (the gradient and the parameter
         shard cut at the segments)."""
         own = self.param_shards[self.rank]
-        sl = [slice(soff, soff + ln) for (_, _, soff, ln) in self.segments]
-        return zb.MultiTensorTable(self.master_tensors, self.exp_avg_tensors, self.exp_avg_sq_tensors,
+        at = [i for i in range(len(self.segments)) if i not in self.muon_segments]
+        sl = [slice(self.segments[i][2], self.segments[i][2] + self.segments[i][3]) for i in at]
+        return zb.MultiTensorTable(*[[x[i] for i in at] for x in (self.master_tensors, self.exp_avg_tensors,
+                                                                  self.exp_avg_sq_tensors)],
                                    [self.grad[x] for x in sl], [own[x] for x in sl])
+
+    def _muon_table(self) -> zb.MuonTable:
+        """The weight matrices' device table (the gradient and the parameter shard cut at the segments)."""
+        own = self.param_shards[self.rank]
+        at = list(self.muon_segments)
+        sl = [slice(self.segments[i][2], self.segments[i][2] + self.segments[i][3]) for i in at]
+        return zb.MuonTable([self.master_tensors[i] for i in at], [self.exp_avg_tensors[i] for i in at],
+                            [self.grad[x] for x in sl], [own[x] for x in sl], [self.muon_segments[i] for i in at])
 
     def steps_applied(self) -> int:
         """Updates applied: the device count with device_step (a synchronous read),
@@ -464,6 +510,23 @@ def staggered_replicas(n_replicas: int, numel: int, device) -> List[torch.Tensor
     (the reduce reads the replica streams in lockstep)."""
     views, _ = _staggered_arena([(numel, torch.int16)] * n_replicas, device)
     return views      # each view keeps the shared allocation alive
+
+
+def _whole_matrices(plan: zb.Plan, segments, shapes: Dict[int, Tuple[int, int]]) -> Dict[int, Tuple[int, int]]:
+    """The rank's segments that are matrices for Muon: segment index -> (rows, cols)."""
+    for t, (rows, cols) in shapes.items():
+        if not 0 <= t < plan.num_tensors:
+            raise ValueError(f"muon_shapes names tensor {t}; the plan has {plan.num_tensors}")
+        if rows < 0 or cols < 0 or rows * cols != plan.tensor_numel(t):
+            raise ValueError(f"tensor {t} of {plan.tensor_numel(t)} elements is no {rows} x {cols} matrix")
+    out = {}
+    for i, (t, _, _, length) in enumerate(segments):
+        if t in shapes:
+            if length != plan.tensor_numel(t):
+                raise ValueError(f"the rank holds {length} elements of tensor {t}'s {plan.tensor_numel(t)}: Muon needs "
+                                 "the whole matrix on one rank")
+            out[i] = (int(shapes[t][0]), int(shapes[t][1]))
+    return out
 
 
 def plan_numels(plan: zb.Plan) -> List[int]:
