@@ -152,21 +152,8 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(Matrices m, MomentumScal
     }
 }
 
-// A product's tile and its waves: kRows x kCols waves, each of MI x NI MFMA tiles of 32 x 32.
-template <int T>
-struct Shape;
-template <>
-struct Shape<256> {
-    static constexpr int kRows = 2, kCols = 2, kThreads = 64 * kRows * kCols, kStages = 2;
-};
-template <>
-struct Shape<128> {
-    static constexpr int kRows = 2, kCols = 2, kThreads = 64 * kRows * kCols, kStages = 2;
-};
-template <>
-struct Shape<64> {
-    static constexpr int kRows = 2, kCols = 2, kThreads = 64 * kRows * kCols, kStages = 3;
-};
+// A product's tile: kRows x kCols waves, each of MI x NI MFMA tiles of 32 x 32.
+constexpr int kRows = 2, kCols = 2, kWaves = kRows * kCols;
 
 // K elements of one LDS stage: a row's 128 bytes are one cache line. One stage is multiplied, the others are on their
 // way.
@@ -228,13 +215,11 @@ __device__ __forceinline__ uint32_t xcd_tile(uint32_t run) {
 }
 
 // One T x T tile of a product, both operands rows of contiguous K.
-template <int T, bool kSquareOut, int kEnd>     // kEnd: 0 workspace, 1 orthogonalised matrix, 2 weight update
+template <int T, int kStages, bool kSquareOut, int kEnd>     // kEnd: 0 workspace, 1 orthogonalised matrix, 2 weight update
 __device__ __forceinline__ void product(const Matrices& m, const Product& p, const Update& u, uint32_t run) {
-    constexpr int kWaves = Shape<T>::kThreads / 64;
-    constexpr int MI = T / 32 / Shape<T>::kRows, NI = T / 32 / Shape<T>::kCols;
+    constexpr int MI = T / 32 / kRows, NI = T / 32 / kCols;
     constexpr int kOperand = T * kDepth;                 // values of one operand's stage
     constexpr int kLoads = T / 8 / kWaves;               // of 8 rows each, a wave and operand
-    constexpr int kStages = Shape<T>::kStages;
     __shared__ __align__(16) f16 lds[kStages * 2 * kOperand];
     static_assert(kStages * 2 * kOperand >= T * T, "the tile fits where the stages were");
     if (kEnd == 2 && skipped(u.clip)) return;
@@ -260,7 +245,7 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
     right += static_cast<int64_t>(bj) * T * ld;
 
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int wr = wave / Shape<T>::kCols * (MI * 32), wc = wave % Shape<T>::kCols * (NI * 32);
+    const int wr = wave / kCols * (MI * 32), wc = wave % kCols * (NI * 32);
 
     // Global to LDS: lane l of a load brings the piece that belongs at place l % 8 of row l / 8.
     const int32_t steps = K / kDepth, all = p.with_low ? 2 * steps : steps;
@@ -302,15 +287,17 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
         else
             f.b[r - MI] = *reinterpret_cast<const f16x8*>(st + b_row + (r - MI) * 32 * kDepth);
     };
+    constexpr int kReads = MI + NI, kProducts = MI * NI;
+    auto multiply = [&](const Fragments& f, int q) {
+        acc[q / NI][q % NI] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.a[q / NI], f.b[q % NI], acc[q / NI][q % NI], 0, 0, 0);
+    };
     // One phase: MI * NI products of `now`, and between them, in this order, the reads of `next` and loads of stage
     // `load_stage`: issued in a row they would hold the products up.
-    constexpr int kReads = MI + NI, kProducts = MI * NI;
     auto phase = [&](const Fragments& now, Fragments& next, int32_t s, int kk, int32_t load_stage, auto first, auto count) {
         int reads = 0, loads = 0;
 #pragma unroll
         for (int q = 0; q < kProducts; ++q) {
-            acc[q / NI][q % NI] =
-                __builtin_amdgcn_mfma_f32_32x32x16_f16(now.a[q / NI], now.b[q % NI], acc[q / NI][q % NI], 0, 0, 0);
+            multiply(now, q);
 #pragma unroll
             for (; reads * kProducts < (q + 1) * kReads * 2 && reads < kReads; ++reads) read(s, kk, reads, next);
 #pragma unroll
@@ -319,47 +306,80 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
         }
     };
     constexpr std::integral_constant<int, 0> kNone{};
-    constexpr std::integral_constant<int, kLoads> kEarly{};   // loads of the phase after the barrier
-    constexpr std::integral_constant<int, 2 * kLoads - kEarly> kLate{};              // and of the phase after that
-    Fragments f0, f1;
-    // One stage. At its barrier stage s + 1 has landed for every wave, and every wave has read all of stage s, whose place
-    // stage s + kStages takes. With two stages its loads are spread over the last phase and the next stage's first
-    // (early and late of them; what late brings is stage s + 1's).
-    auto stage = [&](int32_t s, auto early, auto late, auto flying) {
-        phase(f0, f1, s, 1, s + 1, kEarly, late);
-        phase(f1, f0, s, 2, 0, kNone, kNone);
-        phase(f0, f1, s, 3, 0, kNone, kNone);
-        landed_and_barrier<flying>();
-        if (p.with_low && s + kStages == steps) use_low();
-        if constexpr (kStages > 2)
-            if (s + kStages < all) load_all(s + kStages);
-        phase(f1, f0, s + 1, 0, s + 2, kNone, early);    // (what it reads after the last stage is not used)
-    };
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) {
-        if (p.with_low && s == steps) use_low();
-        if (s < all) load_all(s);
-    }
-    if (all >= kStages)
-        landed_and_barrier<(kStages - 1) * 2 * kLoads>();
-    else
-        landed_and_barrier<0>();
-#pragma unroll
-    for (int r = 0; r < kReads; ++r) read(0, 0, r, f0);
     if constexpr (kStages == 2) {
+        // One stage. At its barrier stage s + 1 has landed for every wave, and every wave has read all of stage s, whose
+        // place stage s + 2 takes: its loads are spread over the last phase and the next stage's first (early and late of
+        // them; what late brings is stage s + 1's).
+        constexpr std::integral_constant<int, kLoads> kEarly{}, kLate{};
+        Fragments f0, f1;
+        auto stage = [&](int32_t s, auto early, auto late) {
+            phase(f0, f1, s, 1, s + 1, kEarly, late);
+            phase(f1, f0, s, 2, 0, kNone, kNone);
+            phase(f0, f1, s, 3, 0, kNone, kNone);
+            landed_and_barrier<0>();
+            if (p.with_low && s + 2 == steps) use_low();
+            phase(f1, f0, s + 1, 0, s + 2, kNone, early);    // (what it reads after the last stage is not used)
+        };
+        load_all(0);
+        if (p.with_low && steps == 1) use_low();
+        if (1 < all) load_all(1);
+        if (1 < all)
+            landed_and_barrier<2 * kLoads>();
+        else
+            landed_and_barrier<0>();
+#pragma unroll
+        for (int r = 0; r < kReads; ++r) read(0, 0, r, f0);
         if (2 < all) {
-            stage(0, kEarly, kNone, kNone);
-            for (int32_t s = 1; s + 2 < all; ++s) stage(s, kEarly, kLate, kNone);
-            stage(all - 2, kNone, kLate, kNone);
+            stage(0, kEarly, kNone);
+            for (int32_t s = 1; s + 2 < all; ++s) stage(s, kEarly, kLate);
+            stage(all - 2, kNone, kLate);
         } else if (1 < all) {
-            stage(0, kNone, kNone, kNone);
+            stage(0, kNone, kNone);
         }
-        stage(all - 1, kNone, kNone, kNone);
+        stage(all - 1, kNone, kNone);
     } else {
+        // With few products between two reads their latency would show at each phase: all fragments of stage s + 1 are read
+        // while stage s multiplies. At a stage's barrier stage s + 1 has landed for every wave, and every wave has
+        // read all of stage s, whose place stage s + kStages takes.
         constexpr std::integral_constant<int, (kStages - 2) * 2 * kLoads> kFlying{};
+        constexpr int kPhases = kDepth / 16;
+        Fragments f0[kPhases], f1[kPhases];
+        auto stage = [&](int32_t s, const Fragments* now, Fragments* next) {
+            if (s + kStages <= all)
+                landed_and_barrier<kFlying>();           // stages s + 2 to s + kStages - 1 may fly
+            else
+                landed_and_barrier<0>();
+            if (p.with_low && s + kStages == steps) use_low();
+            if (s + kStages < all) load_all(s + kStages);
+            int reads = 0;
+#pragma unroll
+            for (int at = 0; at < kPhases * kProducts; ++at) {
+                multiply(now[at / kProducts], at % kProducts);
+#pragma unroll
+                for (; reads * kProducts < (at + 1) * kReads * 2 && reads < kPhases * kReads; ++reads)
+                    read(s + 1, reads / kReads, reads % kReads, next[reads / kReads]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) {
+            if (p.with_low && s == steps) use_low();
+            if (s < all) load_all(s);
+        }
+        if (all >= kStages)
+            landed_and_barrier<(kStages - 1) * 2 * kLoads>();
+        else
+            landed_and_barrier<0>();
+#pragma unroll
+        for (int kk = 0; kk < kPhases; ++kk)
+#pragma unroll
+            for (int r = 0; r < kReads; ++r) read(0, kk, r, f0[kk]);
         int32_t s = 0;
-        for (; s + kStages <= all; ++s) stage(s, kNone, kNone, kFlying);     // stages s + 2 to s + kStages - 1 may fly
-        for (; s < all; ++s) stage(s, kNone, kNone, kNone);
+        for (; s + 1 < all; s += 2) {
+            stage(s, f0, f1);
+            stage(s + 1, f1, f0);
+        }
+        if (s < all) stage(s, f0, f1);                   // (what the last one reads is not used)
     }
 
     // A lane holds one column of each MFMA tile, four consecutive rows at a time; LDS turns them into whole rows, in
@@ -500,9 +520,9 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
     }
 }
 
-template <int T, bool kSquareOut, int kEnd>
-__global__ __launch_bounds__(Shape<T>::kThreads) void product_kernel(Matrices m, Product p, Update u, uint32_t run) {
-    product<T, kSquareOut, kEnd>(m, p, u, run);
+template <int T, int kStages, bool kSquareOut, int kEnd>
+__global__ __launch_bounds__(64 * kWaves) void product_kernel(Matrices m, Product p, Update u, uint32_t run) {
+    product<T, kStages, kSquareOut, kEnd>(m, p, u, run);
 }
 
 // ------------------------------------------------------------ launches
@@ -518,21 +538,27 @@ struct Call {
     double cost[2];               // of one pair and single steps, and of pairs
 };
 
-template <int T, bool kSquareOut, int kEnd>
+template <int T, int kStages, bool kSquareOut, int kEnd>
 void launch_product(const Matrices& m, const Product& p, const Update& u, hipStream_t stream) {
     // Whole runs on every XCD; no run longer than an eighth of the tiles, so that a short grid reaches every XCD.
     const uint32_t total = m.total[kSquareOut ? zero::muon::kByPair : zero::muon::kByTile];
     const uint32_t run = std::min(32u, (total + 7) / 8);
     const uint32_t blocks = (total + 8 * run - 1) / (8 * run) * (8 * run);
-    hipLaunchKernelGGL((product_kernel<T, kSquareOut, kEnd>), dim3(blocks),
-                       dim3(Shape<T>::kThreads), 0, stream, m, p, u, run);
+    hipLaunchKernelGGL((product_kernel<T, kStages, kSquareOut, kEnd>), dim3(blocks),
+                       dim3(64 * kWaves), 0, stream, m, p, u, run);
 }
 
 template <bool kSquareOut, int kEnd>
 void launch_product(const Matrices& m, const Product& p, const Update& u, hipStream_t stream) {
-    if (m.tile == 64) return launch_product<64, kSquareOut, kEnd>(m, p, u, stream);
-    if (m.tile == 128) return launch_product<128, kSquareOut, kEnd>(m, p, u, stream);
-    launch_product<256, kSquareOut, kEnd>(m, p, u, stream);
+    if (m.tile == 64) {
+        // More stages on their way where they cost no third workgroup on a compute unit. (Kernel times of five steps:
+        // 487 x 1000 takes 143 us with four stages and 152 with three, six matrices of a 124 M GPT 447 and 414.)
+        const uint32_t total = m.total[kSquareOut ? zero::muon::kByPair : zero::muon::kByTile];
+        if (total <= 2 * zero::muon::kUnits) return launch_product<64, 4, kSquareOut, kEnd>(m, p, u, stream);
+        return launch_product<64, 3, kSquareOut, kEnd>(m, p, u, stream);
+    }
+    if (m.tile == 128) return launch_product<128, 2, kSquareOut, kEnd>(m, p, u, stream);
+    launch_product<256, 2, kSquareOut, kEnd>(m, p, u, stream);
 }
 
 template <int kSource, int kEnd>

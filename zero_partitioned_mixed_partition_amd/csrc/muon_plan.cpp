@@ -50,7 +50,9 @@ zero_status make_program(const double* coefficients, int32_t n_steps, bool pairs
     double top = 1.0;        // bound of the eigenvalues of A, X X^T of a matrix of norm 1
     int32_t from = kT0, to = kT1;
     for (int32_t at = 0; at < n_steps;) {
-        const bool pair = at + 1 < n_steps && (pairs || at == 0), first = at == 0;
+        const bool first = at == 0;
+        // (in the pair's A' roundings grow by the square of its first step's a)
+        const bool pair = at + 1 < n_steps && (pairs || first) && std::fabs(coefficients[3 * at]) <= 4.0;
         const double a = coefficients[3 * at], b = coefficients[3 * at + 1], c = coefficients[3 * at + 2];
         auto poly = [&](double x) { return a + x * (b + x * c); };
         auto product = [&](Kind kind, int32_t lhs, int32_t rhs, int32_t o, double alpha) {

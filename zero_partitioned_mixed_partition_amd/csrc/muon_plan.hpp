@@ -104,6 +104,8 @@ enum Grid : int32_t { kByChunk = 0, kByPack = 1, kByTile = 2, kByPair = 3, kByPa
 constexpr int kGrids = 5;
 constexpr int64_t kPack = 64;
 
+constexpr uint32_t kUnits = 256;                 // compute units of the chip
+
 // Values from one row of K to the next: an odd number of 256-byte lines, so that the rows of a tile, which are read at the
 // same K, lie in all memory channels (these change every 256 bytes; a power of two of them puts every row in one).
 constexpr int32_t stride(int32_t k) { return ((k + 127) / 128 | 1) * 128; }
