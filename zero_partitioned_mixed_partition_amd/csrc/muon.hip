@@ -228,11 +228,15 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
     if (t >= m.total[kGrid]) return;
     const Desc d = find(m, kGrid, t, &t);
     const bool tall = d.rows > d.cols;
+    const int32_t height = !kSquareOut && tall ? d.N : d.M, width = kSquareOut || tall ? d.M : d.N;
     int32_t bi, bj;
     if constexpr (kSquareOut)
-        triangle_tile(t, d.M / T, &bi, &bj);
+        triangle_tile(t, (height + T - 1) / T, &bi, &bj);
     else
-        rect_tile(t, (tall ? d.N : d.M) / T, (tall ? d.M : d.N) / T, &bi, &bj);
+        rect_tile(t, (height + T - 1) / T, (width + T - 1) / T, &bi, &bj);
+    // The last tiles end with the matrix; the rows and columns that they share with the tiles before are those tiles'.
+    const int32_t r0 = min(bi * T, height - T), c0 = min(bj * T, width - T);
+    const int32_t skip_rows = bi * T - r0, skip_cols = bj * T - c0;
     const int32_t K = p.kind == Kind::kGram ? d.N : d.M, ld = stride(K);
     const f16* left = buffer(m, d, p.lhs);
     const f16* right = buffer(m, d, p.rhs);
@@ -241,8 +245,8 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
         left = right;
         right = x;
     }
-    left += static_cast<int64_t>(bi) * T * ld;
-    right += static_cast<int64_t>(bj) * T * ld;
+    left += static_cast<int64_t>(r0) * ld;
+    right += static_cast<int64_t>(c0) * ld;
 
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int wr = wave / kCols * (MI * 32), wc = wave % kCols * (NI * 32);
@@ -270,7 +274,7 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
         for (int q = 0; q < 2 * kLoads; ++q) load(s, q);
     };
     auto use_low = [&] {                                 // the low part of X takes its place
-        const f16* const low = buffer(m, d, zero::muon::kLow) + static_cast<int64_t>(tall ? bi : bj) * T * ld;
+        const f16* const low = buffer(m, d, zero::muon::kLow) + static_cast<int64_t>(tall ? r0 : c0) * ld;
         from[tall ? 0 : 1] = zero::dev::through_rsrc(low);
     };
     const int turn = (lane >> 1) & 7;                    // of the lane's rows in a fragment
@@ -392,15 +396,29 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
     const int down = wr + lane / 32 * 4, over = wc + lane % 32;        // the lane's first row, and its column
     const int quad = lane % 4;
     // Where eight bytes lie: four values of row r from column 4 g. Rows that are close lie in other banks.
-    auto place = [&](int r, int g) { return r * T + (((g >> 1) ^ ((2 * r) & (T / 8 - 1))) << 3) + (g & 1) * 4; };
-    constexpr int kPerRow = T / 8, kRowStep = 64 * kWaves / kPerRow;    // 16-byte pieces of a row; rows at a time
-    const int own_row = threadIdx.x / kPerRow, own_piece = threadIdx.x % kPerRow;
-    // The tile in LDS to rows of `ld` values at `to`.
-    auto write_rows = [&](f16* to, int64_t ld) {
-#pragma unroll 8
-        for (int r = own_row; r < T; r += kRowStep)
-            *reinterpret_cast<f16x8*>(to + r * ld + own_piece * 8) =
-                *reinterpret_cast<const f16x8*>(lds + place(r, own_piece * 2));
+    auto place = [&](int r, int g) {
+        const int turned = T % 128 == 0 || T == 64 ? (2 * r) & (T / 8 - 1) : (r >> 1) & 7;
+        return r * T + (((g >> 1) ^ turned) << 3) + (g & 1) * 4;
+    };
+    // A thread's 16-byte pieces: kGroup threads, a power of two, hold pieces next to each other of one row.
+    constexpr int kPerRow = T / 8, kGroup = kPerRow & -kPerRow, kAcross = kPerRow / kGroup;
+    constexpr int kRowStep = 64 * kWaves / kGroup, kOwn = T / kRowStep * kAcross;
+    auto row_of = [&](int k) { return static_cast<int>(threadIdx.x) / kGroup + k / kAcross * kRowStep; };
+    auto piece_of = [&](int k) { return static_cast<int>(threadIdx.x) % kGroup + k % kAcross * kGroup; };
+    // The tile in LDS to rows of `ld` values at `to`, but for what another tile writes.
+    auto write_rows = [&](f16* to, int64_t ld, int32_t first_row, int32_t first_col) {
+        constexpr int kAtOnce = kOwn < 8 ? kOwn : kOwn % 8 == 0 ? 8 : 6;
+        static_assert(kOwn % kAtOnce == 0, "whole groups");
+#pragma unroll 1
+        for (int k0 = 0; k0 < kOwn; k0 += kAtOnce) {
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int r = row_of(k0 + k), piece = piece_of(k0 + k);
+                if (r >= first_row && piece * 8 >= first_col)
+                    *reinterpret_cast<f16x8*>(to + r * ld + piece * 8) =
+                        *reinterpret_cast<const f16x8*>(lds + place(r, piece * 2));
+            }
+        }
     };
     // Calls f(i, j, q) for the lane's groups of four rows.
     auto each = [&](auto f) {
@@ -416,23 +434,23 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
     if constexpr (kSquareOut) {
         f16* const out = buffer(m, d, p.out);
         const int64_t ldm = stride(d.M);
-        const int64_t direct = bi * T * ldm + bj * T, mirrored = bj * T * ldm + bi * T;
+        const int64_t direct = r0 * ldm + c0, mirrored = c0 * ldm + r0;
         if (p.add != zero::muon::kNone) {                // symmetric: its mirrored tile's rows are this one's columns
             const f16* const add = buffer(m, d, p.add) + mirrored;
-            constexpr int kAtOnce = T / kRowStep < 8 ? T / kRowStep : 8;
+            constexpr int kAtOnce = kOwn < 8 ? kOwn : kOwn % 8 == 0 ? 8 : 6;
 #pragma unroll 1
-            for (int r0 = own_row; r0 < T; r0 += kAtOnce * kRowStep) {
+            for (int k0 = 0; k0 < kOwn; k0 += kAtOnce) {
                 f16x8 x[kAtOnce];
 #pragma unroll
-                for (int r = 0; r < kAtOnce; ++r)
-                    x[r] = *reinterpret_cast<const f16x8*>(add + (r0 + r * kRowStep) * ldm + own_piece * 8);
+                for (int k = 0; k < kAtOnce; ++k)
+                    x[k] = *reinterpret_cast<const f16x8*>(add + row_of(k0 + k) * ldm + piece_of(k0 + k) * 8);
 #pragma unroll
-                for (int r = 0; r < kAtOnce; ++r)
-                    *reinterpret_cast<f16x8*>(lds + place(r0 + r * kRowStep, own_piece * 2)) = x[r];
+                for (int k = 0; k < kAtOnce; ++k)
+                    *reinterpret_cast<f16x8*>(lds + place(row_of(k0 + k), piece_of(k0 + k) * 2)) = x[k];
             }
             __syncthreads();
         }
-        const int diagonal = (bj - bi) * T + over - down;               // row minus `down` of the lane's first column
+        const int diagonal = c0 - r0 + over - down;               // row minus `down` of the lane's first column
         each([&](int i, int j, int q) {
             f16x4 old = {};
             if (p.add != zero::muon::kNone)
@@ -450,7 +468,7 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
                 *reinterpret_cast<f16x4*>(lds + place(over + j * 32, (down + i * 32 + q * 8) / 4)) = values[i][j][q];
             });
             __syncthreads();
-            write_rows(out + mirrored, ldm);
+            write_rows(out + mirrored, ldm, skip_cols, skip_rows);
             __syncthreads();
         }
         each([&](int i, int j, int q) {
@@ -458,7 +476,7 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
                 quad_transpose(values[i][j][q]);
         });
         __syncthreads();
-        write_rows(out + direct, ldm);
+        write_rows(out + direct, ldm, skip_rows, skip_cols);
     } else if constexpr (kEnd == 0) {
         const int64_t down_ld = stride(tall ? d.N : d.M), along_ld = stride(tall ? d.M : d.N);
         f16* const along = buffer(m, d, tall ? p.out_t : p.out);
@@ -469,14 +487,14 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
             *reinterpret_cast<f16x4*>(lds + place(over + j * 32, (down + i * 32 + q * 8) / 4)) = values[i][j][q];
         });
         __syncthreads();
-        write_rows(across + bj * T * down_ld + bi * T, down_ld);
+        write_rows(across + c0 * down_ld + r0, down_ld, skip_cols, skip_rows);
         __syncthreads();
         each([&](int i, int j, int q) {
             *reinterpret_cast<f16x4*>(lds + place(down + i * 32 + q * 8 + quad, (over + j * 32) / 4)) =
                 quad_transpose(values[i][j][q]);
         });
         __syncthreads();
-        write_rows(along + bi * T * along_ld + bj * T, along_ld);
+        write_rows(along + r0 * along_ld + c0, along_ld, skip_rows, skip_cols);
     } else {
         // The orthogonalised matrix in bf16, as bits.
         each([&](int i, int j, int q) {
@@ -488,33 +506,32 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
         });
         __syncthreads();
         const float rate = static_cast<float>(u.lr * d.scale);
-        const int32_t c = bj * T + own_piece * 8;
-        const int n = d.cols - c < 8 ? (d.cols - c < 0 ? 0 : d.cols - c) : 8;
-        // Four rows' loads before the first is used; only the last tiles of a matrix need the guards.
-        constexpr int kAtOnce = T / kRowStep < 4 ? T / kRowStep : 4;
-        static_assert(T / kRowStep % kAtOnce == 0, "whole groups");
-        for (int r0 = 0; r0 < T / kRowStep; r0 += kAtOnce) {
+        // Four pieces' loads before the first is used; only the last tiles of a matrix need the guards.
+        constexpr int kAtOnce = kOwn < 4 ? kOwn : kOwn % 4 == 0 ? 4 : 3;
+        static_assert(kOwn % kAtOnce == 0, "whole groups");
+#pragma unroll 1
+        for (int k0 = 0; k0 < kOwn; k0 += kAtOnce) {
             float w[kAtOnce][8];
+            int64_t first[kAtOnce];
+            int here[kAtOnce];
 #pragma unroll
-            for (int r = 0; r < kAtOnce; ++r) {
-                const int32_t row_at = bi * T + own_row + (r0 + r) * kRowStep;
-                const int64_t first = static_cast<int64_t>(row_at) * d.cols + c;
-                const int here = row_at < d.rows ? n : 0;
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int r = row_of(k0 + k), piece = piece_of(k0 + k);
+                const int32_t c = c0 + piece * 8;
+                first[k] = static_cast<int64_t>(r0 + r) * d.cols + c;
+                const bool own = r >= skip_rows && piece * 8 >= skip_cols && r0 + r < d.rows && c < d.cols;
+                here[k] = !own ? 0 : d.cols - c < 8 ? d.cols - c : 8;
                 if constexpr (kEnd == 2) {
-                    read4(d.master, first, here < 4 ? here : 4, w[r]);
-                    read4(d.master, first + 4, here < 4 ? 0 : here - 4, w[r] + 4);
+                    read4(d.master, first[k], here[k] < 4 ? here[k] : 4, w[k]);
+                    read4(d.master, first[k] + 4, here[k] < 4 ? 0 : here[k] - 4, w[k] + 4);
                 }
             }
 #pragma unroll
-            for (int r = 0; r < kAtOnce; ++r) {
-                const int row_in = own_row + (r0 + r) * kRowStep;
-                const int32_t row_at = bi * T + row_in;
-                const int64_t first = static_cast<int64_t>(row_at) * d.cols + c;
-                const int here = row_at < d.rows ? n : 0;
-                const f16x8 o = *reinterpret_cast<const f16x8*>(lds + place(row_in, own_piece * 2));
+            for (int k = 0; k < kAtOnce; ++k) {
+                const f16x8 o = *reinterpret_cast<const f16x8*>(lds + place(row_of(k0 + k), piece_of(k0 + k) * 2));
                 uint16_t bits[8];
                 __builtin_memcpy(bits, &o, sizeof(bits));
-                finish8<kEnd>(d, u, rate, first, here, bits, w[r]);
+                finish8<kEnd>(d, u, rate, first[k], here[k], bits, w[k]);
             }
         }
     }
@@ -550,14 +567,17 @@ void launch_product(const Matrices& m, const Product& p, const Update& u, hipStr
 
 template <bool kSquareOut, int kEnd>
 void launch_product(const Matrices& m, const Product& p, const Update& u, hipStream_t stream) {
-    if (m.tile == 64) {
+    const int64_t tile = kSquareOut ? m.square_tile : m.rect_tile;
+    if (tile == 64) {
         // More stages on their way where they cost no third workgroup on a compute unit. (Kernel times of five steps:
         // 487 x 1000 takes 143 us with four stages and 152 with three, six matrices of a 124 M GPT 447 and 414.)
         const uint32_t total = m.total[kSquareOut ? zero::muon::kByPair : zero::muon::kByTile];
         if (total <= 2 * zero::muon::kUnits) return launch_product<64, 4, kSquareOut, kEnd>(m, p, u, stream);
         return launch_product<64, 3, kSquareOut, kEnd>(m, p, u, stream);
     }
-    if (m.tile == 128) return launch_product<128, 2, kSquareOut, kEnd>(m, p, u, stream);
+    if (tile == 128) return launch_product<128, 2, kSquareOut, kEnd>(m, p, u, stream);
+    if constexpr (kSquareOut)
+        if (tile == 192) return launch_product<192, 2, kSquareOut, kEnd>(m, p, u, stream);
     launch_product<256, 2, kSquareOut, kEnd>(m, p, u, stream);
 }
 
@@ -631,14 +651,14 @@ zero_status measure_stack(int64_t count, int64_t rows, int64_t cols, Matrices* m
     if (st != ZERO_OK) return st;
     zero::muon::TileChoice choice;
     choice.add(count, rows, cols);
-    m->tile = choice.best();
-    zero::muon::shape(&m->base, rows, cols, m->tile);
+    choice.best(&m->square_tile, &m->rect_tile);
+    zero::muon::shape(&m->base, rows, cols, std::max(m->square_tile, m->rect_tile));
     m->side = short_side(std::min(rows, cols));
     m->base.parts = m->side != 0 ? short_parts(m->side, std::max(rows, cols), count) : 1;
     m->numel = rows * cols;
     m->area = zero::muon::area_bytes(m->base);
     for (int g = 0; g < kGrids; ++g) {
-        const int64_t per = zero::muon::grid_count(m->base, g, m->tile);
+        const int64_t per = zero::muon::grid_count(m->base, g, m->square_tile, m->rect_tile);
         if (count > kMaxBlocks / per)
             return zero::fail(ZERO_ERANGE, std::string(who) + ": more workgroups than one launch holds");
         m->per[g] = static_cast<uint32_t>(per);
@@ -817,13 +837,13 @@ zero_status fill_table(zero_muon_table* tab, const char* who) {
     if (tab->descs.empty()) return ZERO_OK;              // needs no device
     zero::muon::TileChoice choice;
     for (const Desc& d : tab->descs) choice.add(1, d.rows, d.cols);
-    tab->m.tile = choice.best();
+    choice.best(&tab->m.square_tile, &tab->m.rect_tile);
     int64_t most = 0;
     for (const Desc& d : tab->descs) most = std::max<int64_t>(most, std::min(d.rows, d.cols));
     tab->m.side = short_side(most);
     tab->m.matrices = static_cast<uint32_t>(tab->descs.size());
     for (Desc& d : tab->descs) {
-        zero::muon::shape(&d, d.rows, d.cols, tab->m.tile);
+        zero::muon::shape(&d, d.rows, d.cols, std::max(tab->m.square_tile, tab->m.rect_tile));
         d.parts = tab->m.side != 0 ? short_parts(tab->m.side, std::max(d.rows, d.cols), tab->m.matrices) : 1;
     }
     std::vector<uint32_t> index;
@@ -833,7 +853,7 @@ zero_status fill_table(zero_muon_table* tab, const char* who) {
         int64_t total = 0;
         for (size_t i = 0; i < tab->descs.size(); ++i) {
             Desc& d = tab->descs[i];
-            const int64_t n = zero::muon::grid_count(d, g, tab->m.tile);
+            const int64_t n = zero::muon::grid_count(d, g, tab->m.square_tile, tab->m.rect_tile);
             if (n > kMaxBlocks - total) return fail(ZERO_ERANGE, w + ": more workgroups than one launch holds");
             d.first[g] = static_cast<int32_t>(total);
             index.insert(index.end(), static_cast<size_t>(n), static_cast<uint32_t>(i));

@@ -32,7 +32,7 @@ struct Matrices {
     int64_t src_bytes;            // from one matrix of a stack to the next
     int64_t numel;
     int64_t area;
-    int64_t tile;                 // of the products: the sides are padded to it
+    int64_t square_tile, rect_tile;    // of the products of square matrices, and of those with X's shape
     uint32_t per[kGrids];         // workgroups of one matrix of a stack, per grid
     uint32_t total[kGrids];
     double* partials;

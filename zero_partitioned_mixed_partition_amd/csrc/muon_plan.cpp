@@ -159,72 +159,83 @@ int32_t short_parts(int32_t side, int64_t n, int64_t count) {
 
 namespace {
 
-constexpr int64_t kTiles[3] = {64, 128, 256};
+constexpr int64_t kTiles[kTileSizes] = {64, 128, 192, 256};
 
 // Microseconds on MI355X of one product: a launch with its descriptors and first loads, each tile's epilogue, and a
-// stage of a tile alone on its compute unit or as a share of a full one. Fitted to 12 matrices of a 1.3 B GPT and 6 of
-// GPT-2 small with each tile: within 15% of their launches.
+// stage of a tile alone on its compute unit or as a share of a full one. Fitted to 12 matrices of a 1.3 B GPT, 6 of
+// GPT-2 small, 14,336 x 4096 and 8192 x 8192 with each tile: within 15% of their launches.
 struct TileCost {
     double launch, tile, alone, share;
 };
-constexpr TileCost kCosts[3] = {{5.0, 0.6, 0.33, 0.27}, {6.0, 2.0, 0.58, 0.64}, {3.0, 10.0, 1.65, 1.65}};
+constexpr TileCost kCosts[kTileSizes] = {
+    {5.0, 0.6, 0.33, 0.27}, {6.0, 2.0, 0.58, 0.64}, {3.0, 6.0, 1.08, 1.08}, {3.0, 10.0, 1.33, 1.62}};
 
 double product_time(const TileCost& c, double tiles, double stages) {
     if (tiles == 0.0) return 0.0;
-    const double load = std::ceil(tiles / 256.0);        // tiles of one compute unit
-    return c.launch + c.tile * load + stages / tiles * std::max(c.alone, c.share * load);
+    const double load = std::ceil(tiles / kUnits);       // tiles of one compute unit
+    return c.launch + c.tile * load + stages / tiles * (load > 1.0 ? std::max(c.alone, c.share * load) : c.alone);
 }
+
+int64_t padded(int64_t side, int64_t tile) { return std::max(pad(side, 64), tile); }
 
 }  // namespace
 
 void TileChoice::add(int64_t count, int64_t rows, int64_t cols) {
-    for (int k = 0; k < 3; ++k) {
-        const int64_t t = kTiles[k];
-        const double m = static_cast<double>(pad(std::min(rows, cols), t)) / t,
-                     n = static_cast<double>(pad(std::max(rows, cols), t)) / t, c = static_cast<double>(count);
-        const double stages = static_cast<double>(t) / 64.0, square = c * m * (m + 1) / 2, rect = c * m * n;
-        total_[k].square += square;
-        total_[k].rect += rect;
-        total_[k].gram += square * n * stages;
-        total_[k].squares += square * m * stages;
-        total_[k].apply += rect * m * stages;
+    const int64_t least = std::min(rows, cols), most = std::max(rows, cols);
+    for (int k = 0; k < kTileSizes; ++k) {
+        for (int j = 0; j < kTileSizes; ++j) {
+            const int64_t ts = kTiles[k], tr = kTiles[j], M = padded(least, std::max(ts, tr)),
+                          N = padded(most, std::max(ts, tr)), across = (M + ts - 1) / ts;
+            const double c = static_cast<double>(count), square = c * (across * (across + 1) / 2),
+                         rect = c * ((M + tr - 1) / tr) * ((N + tr - 1) / tr);
+            Total& x = total_[k][j];
+            x.square += square;
+            x.rect += rect;
+            x.gram += square * (N / 64);
+            x.squares += square * (M / 64);
+            x.apply += rect * (M / 64);
+        }
     }
 }
 
-int64_t TileChoice::best() const {
-    int at = 0;
+void TileChoice::best(int64_t* square, int64_t* rect) const {
     double least = 0.0;
-    for (int k = 0; k < 3; ++k) {
-        const Total& x = total_[k];
-        // as five steps in pairs: 3 products X X^T, 11 of square matrices, 3 applies and the first one's low part
-        const double time = 3 * product_time(kCosts[k], x.square, x.gram) + 11 * product_time(kCosts[k], x.square, x.squares) +
-                            4 * product_time(kCosts[k], x.rect, x.apply);
-        if (k == 0 || time < least) {
-            at = k;
-            least = time;
+    *square = *rect = 0;
+    for (int k = 0; k < kTileSizes; ++k) {
+        for (int j = 0; j < kTileSizes; ++j) {
+            if (kTiles[j] == 192) continue;
+            const Total& x = total_[k][j];
+            // as five steps in pairs: 3 products X X^T, 11 of square matrices, 3 applies and the first one's low part
+            const double time = 3 * product_time(kCosts[k], x.square, x.gram) +
+                                11 * product_time(kCosts[k], x.square, x.squares) +
+                                4 * product_time(kCosts[j], x.rect, x.apply);
+            if (*square == 0 || time < least) {
+                *square = kTiles[k];
+                *rect = kTiles[j];
+                least = time;
+            }
         }
     }
-    return kTiles[at];
 }
 
 void shape(Desc* d, int64_t rows, int64_t cols, int64_t tile) {
     const int64_t numel = rows * cols;
     d->rows = static_cast<int32_t>(rows);
     d->cols = static_cast<int32_t>(cols);
-    d->M = static_cast<int32_t>(pad(std::min(rows, cols), tile));
-    d->N = static_cast<int32_t>(pad(std::max(rows, cols), tile));
+    d->M = static_cast<int32_t>(padded(std::min(rows, cols), tile));
+    d->N = static_cast<int32_t>(padded(std::max(rows, cols), tile));
     d->chunk = std::max(kChunk, pad((numel + kMaxChunks - 1) / kMaxChunks, kChunk));
     d->chunks = static_cast<int32_t>((numel + d->chunk - 1) / d->chunk);
 }
 
-int64_t grid_count(const Desc& d, int grid, int64_t tile) {
-    const int64_t m = d.M / tile, n = d.N / tile;
+int64_t grid_count(const Desc& d, int grid, int64_t square_tile, int64_t rect_tile) {
+    const int64_t across = (d.M + square_tile - 1) / square_tile;
     switch (grid) {
         case kByChunk: return d.chunks;
         case kByPack: return (d.M / kPack) * (d.N / kPack);
-        case kByTile: return m * n;
+        case kByTile: return ((d.M + rect_tile - 1) / rect_tile) * ((d.N + rect_tile - 1) / rect_tile);
         case kByPart: return d.parts;
-        default: return m * (m + 1) / 2;
+        default: return across * (across + 1) / 2;
     }
 }
 

@@ -24,7 +24,8 @@
 namespace zero {
 namespace muon {
 
-// A matrix's arrays in the workspace, all fp16, both sides padded to whole tiles with zeros (M >= m, N >= n).
+// A matrix's arrays in the workspace, all fp16, both sides padded with zeros to multiples of 64 that hold a tile (M >= m,
+// N >= n).
 enum Buffer : int32_t {
     kX = 0,      // [M][N]: X
     kT0 = 1,     // [N][M]: X transposed, and
@@ -112,26 +113,29 @@ constexpr int32_t stride(int32_t k) { return ((k + 127) / 128 | 1) * 128; }
 
 inline int64_t pad(int64_t x, int64_t tile) { return (x + tile - 1) / tile * tile; }
 
-// The tile of a call's products, 64, 128 or 256, by an estimate of five steps' time with each (one workgroup of 256 a
-// compute unit, two of 128, more of 64). Sums over K are measured in stages of 64. Larger tiles read less for each
-// product; smaller ones fill the chip from fewer matrices and pad less.
+// The tiles of a call's products by an estimate of five steps' time with each pair: 64, 128, 192 or 256 for those of
+// square matrices, 64, 128 or 256 for those with X's shape. Sums over K are measured in stages of 64. Larger tiles read
+// less for each product; smaller ones fill the chip from fewer matrices and pad less. 192 is for the last round of
+// workgroups, which with 256 can leave half of the chip idle: X X^T of a side of 4096 has 136 tiles of 256 (98 us at K
+// 4096) and 253 of 192 (79 us); where both fill whole rounds 256 is up to a fifth faster.
+constexpr int kTileSizes = 4;
 class TileChoice {
 public:
     void add(int64_t count, int64_t rows, int64_t cols);
-    int64_t best() const;
+    void best(int64_t* square, int64_t* rect) const;
 
 private:
     struct Total {
         double square = 0, rect = 0;             // tiles
         double gram = 0, squares = 0, apply = 0; // tiles times stages
-    } total_[3];
+    } total_[kTileSizes][kTileSizes];
 };
 
-// Fills in M, N, chunk and chunks of a matrix of rows x cols.
+// Fills in M, N, chunk and chunks of a matrix of rows x cols, whose sides are padded to `tile` at least.
 void shape(Desc* d, int64_t rows, int64_t cols, int64_t tile);
 
 // Workgroups of a matrix in each grid.
-int64_t grid_count(const Desc& d, int grid, int64_t tile);
+int64_t grid_count(const Desc& d, int grid, int64_t square_tile, int64_t rect_tile);
 
 // Bytes of a matrix's arrays (kLow at the end, where the input is fp32).
 int64_t area_bytes(const Desc& d);
