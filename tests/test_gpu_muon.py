@@ -85,6 +85,36 @@ def test_large(zm, count, rows, cols):
     check(got, [oracle.muon.orthogonalize(m) for m in x], (rows, cols))
 
 
+def on_gpu_in_64_bits(x, steps=STEPS, eps=1e-7):
+    """The oracle's formula in float64 on the GPU, for sides whose products take a CPU too long."""
+    if x.shape[0] > x.shape[1]:
+        return on_gpu_in_64_bits(x.T.contiguous(), steps, eps).T
+    x = x.double()
+    x = x / (x.norm() + eps)
+    for a, b, c in steps:
+        gram = x @ x.T.contiguous()
+        x = a * x + (b * gram + c * (gram @ gram)) @ x
+    return x
+
+
+@pytest.mark.parametrize("count,rows,cols", [(1, 2853, 3010), (1, 3010, 2853), (1, 4417, 4600), (9, 1030, 1100), (1, 2200, 2201), (3, 400, 5000)])
+def test_tiles_that_end_inside_the_one_before(zm, count, rows, cols):
+    """Sides that are no multiple of the tiles that such sizes take: each value is written once, by one workgroup."""
+    note(f"{count} x {rows} x {cols}")
+    x = to_dev_f32(matrices(7, count, rows, cols, strong=3).reshape(-1))
+    out = [torch.full((x.numel() + 64,), 0x55, dtype=torch.int16, device=dev()) for _ in range(2)]
+    for o in out:
+        zm.zero_orthogonalize(x, o[:x.numel()], rows, cols)
+    assert torch.equal(out[0], out[1]) and (out[0][x.numel():] == 0x55).all()
+    got = out[0][:x.numel()].view(torch.bfloat16).view(count, rows, cols).double()
+    for i in range(count):
+        want = on_gpu_in_64_bits(x.view(count, rows, cols)[i])
+        off = (got[i] - want).abs()
+        rms = want.norm() / want.numel() ** 0.5
+        assert (off <= 2.0 ** -8 * want.abs() + 8 * 4e-3 * rms).all(), i
+        assert off.norm() <= FROBENIUS * want.norm(), (i, float(off.norm() / want.norm()))
+
+
 @pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 9])
 @pytest.mark.parametrize("shape", [(1, 96, 96), (2, 48, 400), (1, 400, 48)])
 def test_step_counts(zm, shape, steps):
@@ -205,6 +235,14 @@ def test_step_is_momentum_orthogonalize_and_update(zm, count, rows, cols, hyper)
     d = on_device(s)
     zm.zero_muon_step(*d, rows, cols, **dict(HYPER, **hyper))
     same(d, composed(zm, s, rows, cols, hyper), (rows, cols, hyper))
+
+
+@pytest.mark.parametrize("count,rows,cols", [(1, 2853, 3010), (1, 4600, 4417), (9, 1030, 1100)])
+def test_a_step_with_large_tiles_updates_each_weight_once(zm, count, rows, cols):
+    s = state(6, count * rows * cols)
+    d = on_device(s)
+    zm.zero_muon_step(*d, rows, cols, **HYPER)
+    same(d, composed(zm, s, rows, cols, {}), (count, rows, cols))
 
 
 def test_step_against_the_oracle(zm):
