@@ -152,8 +152,11 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(Matrices m, MomentumScal
     }
 }
 
-// A product's tile: kRows x kCols waves, each of MI x NI MFMA tiles of 32 x 32.
+// A product's tile: kRows x kCols waves, each of MI x NI MFMA tiles of kSide x kSide, kInner deep. (A chip full of MFMAs is
+// limited by its power: from registers alone 16 x 16 x 32 sustains 1905 TFLOP/s and 32 x 32 x 16, which reads its
+// accumulators twice as often, 1640.)
 constexpr int kRows = 2, kCols = 2, kWaves = kRows * kCols;
+constexpr int kSide = 16, kInner = 32;
 
 // K elements of one LDS stage: a row's 128 bytes are one cache line. One stage is multiplied, the others are on their
 // way.
@@ -217,7 +220,7 @@ __device__ __forceinline__ uint32_t xcd_tile(uint32_t run) {
 // One T x T tile of a product, both operands rows of contiguous K.
 template <int T, int kStages, bool kSquareOut, int kEnd>     // kEnd: 0 workspace, 1 orthogonalised matrix, 2 weight update
 __device__ __forceinline__ void product(const Matrices& m, const Product& p, const Update& u, uint32_t run) {
-    constexpr int MI = T / 32 / kRows, NI = T / 32 / kCols;
+    constexpr int MI = T / kSide / kRows, NI = T / kSide / kCols;
     constexpr int kOperand = T * kDepth;                 // values of one operand's stage
     constexpr int kLoads = T / 8 / kWaves;               // of 8 rows each, a wave and operand
     __shared__ __align__(16) f16 lds[kStages * 2 * kOperand];
@@ -249,7 +252,7 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
     right += static_cast<int64_t>(c0) * ld;
 
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int wr = wave / kCols * (MI * 32), wc = wave % kCols * (NI * 32);
+    const int wr = wave / kCols * (MI * kSide), wc = wave % kCols * (NI * kSide);
 
     // Global to LDS: lane l of a load brings the piece that belongs at place l % 8 of row l / 8.
     const int32_t steps = K / kDepth, all = p.with_low ? 2 * steps : steps;
@@ -277,52 +280,65 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
         const f16* const low = buffer(m, d, zero::muon::kLow) + static_cast<int64_t>(tall ? r0 : c0) * ld;
         from[tall ? 0 : 1] = zero::dev::through_rsrc(low);
     };
-    const int turn = (lane >> 1) & 7;                    // of the lane's rows in a fragment
-    const int a_row = (wr + lane % 32) * kDepth, b_row = kOperand + (wc + lane % 32) * kDepth;
-    f32x16 acc[MI][NI] = {};
+    const int turn = (lane % kSide) >> 1;                // of the lane's rows in a fragment
+    const int a_row = (wr + lane % kSide) * kDepth, b_row = kOperand + (wc + lane % kSide) * kDepth;
+    f32x4 acc[MI][NI] = {};
+    auto keep_sums = [&] {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) asm volatile("" : "+a"(acc[i][j]));
+    };
     struct Fragments {
         f16x8 a[MI], b[NI];
     };
-    // Read r of the fragments of K elements 16 kk to 16 kk + 15 of stage s.
+    // Read r of the fragments of K elements 32 kk to 32 kk + 31 of stage s.
     auto read = [&](int32_t s, int kk, int r, Fragments& f) {
-        const f16* const st = lds + (s % kStages) * 2 * kOperand + ((2 * kk + lane / 32) ^ turn) * 8;
+        const f16* const st = lds + (s % kStages) * 2 * kOperand + ((4 * kk + lane / kSide) ^ turn) * 8;
         if (r < MI)
-            f.a[r] = *reinterpret_cast<const f16x8*>(st + a_row + r * 32 * kDepth);
+            f.a[r] = *reinterpret_cast<const f16x8*>(st + a_row + r * kSide * kDepth);
         else
-            f.b[r - MI] = *reinterpret_cast<const f16x8*>(st + b_row + (r - MI) * 32 * kDepth);
+            f.b[r - MI] = *reinterpret_cast<const f16x8*>(st + b_row + (r - MI) * kSide * kDepth);
     };
     constexpr int kReads = MI + NI, kProducts = MI * NI;
+    // In assembly, so that the sum stays where it is: the compiler may give the result of this shape other registers, and
+    // with 256 of them moves them all in every stage. (It also knows of no wait before the sums are read: see below.)
     auto multiply = [&](const Fragments& f, int q) {
-        acc[q / NI][q % NI] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.a[q / NI], f.b[q % NI], acc[q / NI][q % NI], 0, 0, 0);
+        asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc[q / NI][q % NI]) : "v"(f.a[q / NI]), "v"(f.b[q % NI]));
     };
-    // One phase: MI * NI products of `now`, and between them, in this order, the reads of `next` and loads of stage
-    // `load_stage`: issued in a row they would hold the products up.
-    auto phase = [&](const Fragments& now, Fragments& next, int32_t s, int kk, int32_t load_stage, auto first, auto count) {
-        int reads = 0, loads = 0;
-#pragma unroll
-        for (int q = 0; q < kProducts; ++q) {
-            multiply(now, q);
-#pragma unroll
-            for (; reads * kProducts < (q + 1) * kReads * 2 && reads < kReads; ++reads) read(s, kk, reads, next);
-#pragma unroll
-            for (; loads * kProducts < (q + 1) * count; ++loads) load(load_stage, first + loads);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    };
-    constexpr std::integral_constant<int, 0> kNone{};
+    keep_sums();                                         // set to 0, and two cycles before the first product
+    asm volatile("s_nop 3" ::: "memory");
     if constexpr (kStages == 2) {
-        // One stage. At its barrier stage s + 1 has landed for every wave, and every wave has read all of stage s, whose
-        // place stage s + 2 takes: its loads are spread over the last phase and the next stage's first (early and late of
-        // them; what late brings is stage s + 1's).
-        constexpr std::integral_constant<int, kLoads> kEarly{}, kLate{};
+        // A stage is two phases of MI * NI products, and between these are issued, in this order, the reads of the next
+        // phase's fragments and the loads of stage s + 2: in a row they would hold the products up. At the barrier all
+        // waves have read stage s, whose place stage s + 2 takes, and stage s + 1 has landed for every wave; its loads had
+        // the other quarter of a stage to. (8192 x 8192, 128 stages: the loads spread over half a stage 1 % slower, over
+        // a quarter 7 %; four stages of half the depth, with twice the barriers, 6 %.)
         Fragments f0, f1;
-        auto stage = [&](int32_t s, auto early, auto late) {
-            phase(f0, f1, s, 1, s + 1, kEarly, late);
-            phase(f1, f0, s, 2, 0, kNone, kNone);
-            phase(f0, f1, s, 3, 0, kNone, kNone);
-            landed_and_barrier<0>();
-            if (p.with_low && s + 2 == steps) use_low();
-            phase(f1, f0, s + 1, 0, s + 2, kNone, early);    // (what it reads after the last stage is not used)
+        static_assert(kDepth == 2 * kInner, "two phases");
+        constexpr int kFree = kProducts * 3 / 4, kSpread = 2 * kProducts - kFree;
+        auto stage = [&](int32_t s, auto load_next) {
+            constexpr int kCount = load_next ? 2 * kLoads : 0;
+            int loads = 0;
+            auto phase = [&](const Fragments& now, Fragments& next, int32_t from_stage, int kk, int first) {
+                int reads = 0;
+#pragma unroll
+                for (int q = 0; q < kProducts; ++q) {
+                    const int at = first + q - kFree;    // products since the barrier
+                    if (at == 0) {
+                        landed_and_barrier<0>();
+                        if (p.with_low && s + 2 == steps) use_low();
+                    }
+                    multiply(now, q);
+#pragma unroll
+                    for (; reads * kProducts < (q + 1) * kReads * 2 && reads < kReads; ++reads) read(from_stage, kk, reads, next);
+#pragma unroll
+                    for (; loads * kSpread < (at + 1) * kCount; ++loads) load(s + 2, loads);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            };
+            phase(f0, f1, s, 1, 0);
+            phase(f1, f0, s + 1, 0, kProducts);          // (what it reads after the last stage is not used)
         };
         load_all(0);
         if (p.with_low && steps == 1) use_low();
@@ -333,20 +349,15 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
             landed_and_barrier<0>();
 #pragma unroll
         for (int r = 0; r < kReads; ++r) read(0, 0, r, f0);
-        if (2 < all) {
-            stage(0, kEarly, kNone);
-            for (int32_t s = 1; s + 2 < all; ++s) stage(s, kEarly, kLate);
-            stage(all - 2, kNone, kLate);
-        } else if (1 < all) {
-            stage(0, kNone, kNone);
-        }
-        stage(all - 1, kNone, kNone);
+        int32_t s = 0;
+        for (; s + 2 < all; ++s) stage(s, std::true_type{});
+        for (; s < all; ++s) stage(s, std::false_type{});
     } else {
         // With few products between two reads their latency would show at each phase: all fragments of stage s + 1 are read
         // while stage s multiplies. At a stage's barrier stage s + 1 has landed for every wave, and every wave has
         // read all of stage s, whose place stage s + kStages takes.
         constexpr std::integral_constant<int, (kStages - 2) * 2 * kLoads> kFlying{};
-        constexpr int kPhases = kDepth / 16;
+        constexpr int kPhases = kDepth / kInner;
         Fragments f0[kPhases], f1[kPhases];
         auto stage = [&](int32_t s, const Fragments* now, Fragments* next) {
             if (s + kStages <= all)
@@ -386,6 +397,10 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
         if (s < all) stage(s, f0, f1);                   // (what the last one reads is not used)
     }
 
+    // The last products take 8 passes of 4 cycles; nothing reads a sum before they are through.
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    keep_sums();
+
     // A lane holds one column of each MFMA tile, four consecutive rows at a time; LDS turns them into whole rows, in
     // either order of storage, so that memory is read and written 16 bytes a lane and 2 T bytes a row.
     float alpha = p.alpha;
@@ -393,7 +408,7 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
         const float kappa = m.kappa[d.id];
         alpha = p.kappa_power == 2 ? alpha * (kappa * kappa) : alpha * kappa;
     }
-    const int down = wr + lane / 32 * 4, over = wc + lane % 32;        // the lane's first row, and its column
+    const int down = wr + lane / kSide * 4, over = wc + lane % kSide;  // the lane's first row, and its column
     const int quad = lane % 4;
     // Where eight bytes lie: four values of row r from column 4 g. Rows that are close lie in other banks.
     auto place = [&](int r, int g) {
@@ -420,16 +435,14 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
             }
         }
     };
-    // Calls f(i, j, q) for the lane's groups of four rows.
+    // Calls f(i, j) for the lane's groups of four rows.
     auto each = [&](auto f) {
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < NI; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) f(i, j, q);
+            for (int j = 0; j < NI; ++j) f(i, j);
     };
-    f16x4 values[MI][NI][4];
+    f16x4 values[MI][NI];
     __syncthreads();
     if constexpr (kSquareOut) {
         f16* const out = buffer(m, d, p.out);
@@ -451,29 +464,29 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
             __syncthreads();
         }
         const int diagonal = c0 - r0 + over - down;               // row minus `down` of the lane's first column
-        each([&](int i, int j, int q) {
+        each([&](int i, int j) {
             f16x4 old = {};
             if (p.add != zero::muon::kNone)
-                old = *reinterpret_cast<const f16x4*>(lds + place(over + j * 32, (down + i * 32 + q * 8) / 4));
+                old = *reinterpret_cast<const f16x4*>(lds + place(over + j * kSide, (down + i * kSide) / 4));
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                float x = alpha * acc[i][j][q * 4 + k] + p.beta * static_cast<float>(old[k]);
-                if (i * 32 + q * 8 + k == diagonal + j * 32) x += p.diag;
-                values[i][j][q][k] = static_cast<f16>(x);
+                float x = alpha * acc[i][j][k] + p.beta * static_cast<float>(old[k]);
+                if (i * kSide + k == diagonal + j * kSide) x += p.diag;
+                values[i][j][k] = static_cast<f16>(x);
             }
         });
         if (p.add != zero::muon::kNone) __syncthreads();
         if (bi != bj) {
-            each([&](int i, int j, int q) {
-                *reinterpret_cast<f16x4*>(lds + place(over + j * 32, (down + i * 32 + q * 8) / 4)) = values[i][j][q];
+            each([&](int i, int j) {
+                *reinterpret_cast<f16x4*>(lds + place(over + j * kSide, (down + i * kSide) / 4)) = values[i][j];
             });
             __syncthreads();
             write_rows(out + mirrored, ldm, skip_cols, skip_rows);
             __syncthreads();
         }
-        each([&](int i, int j, int q) {
-            *reinterpret_cast<f16x4*>(lds + place(down + i * 32 + q * 8 + quad, (over + j * 32) / 4)) =
-                quad_transpose(values[i][j][q]);
+        each([&](int i, int j) {
+            *reinterpret_cast<f16x4*>(lds + place(down + i * kSide + quad, (over + j * kSide) / 4)) =
+                quad_transpose(values[i][j]);
         });
         __syncthreads();
         write_rows(out + direct, ldm, skip_rows, skip_cols);
@@ -481,27 +494,27 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
         const int64_t down_ld = stride(tall ? d.N : d.M), along_ld = stride(tall ? d.M : d.N);
         f16* const along = buffer(m, d, tall ? p.out_t : p.out);
         f16* const across = buffer(m, d, tall ? p.out : p.out_t);
-        each([&](int i, int j, int q) {
+        each([&](int i, int j) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) values[i][j][q][k] = static_cast<f16>(alpha * acc[i][j][q * 4 + k]);
-            *reinterpret_cast<f16x4*>(lds + place(over + j * 32, (down + i * 32 + q * 8) / 4)) = values[i][j][q];
+            for (int k = 0; k < 4; ++k) values[i][j][k] = static_cast<f16>(alpha * acc[i][j][k]);
+            *reinterpret_cast<f16x4*>(lds + place(over + j * kSide, (down + i * kSide) / 4)) = values[i][j];
         });
         __syncthreads();
         write_rows(across + c0 * down_ld + r0, down_ld, skip_cols, skip_rows);
         __syncthreads();
-        each([&](int i, int j, int q) {
-            *reinterpret_cast<f16x4*>(lds + place(down + i * 32 + q * 8 + quad, (over + j * 32) / 4)) =
-                quad_transpose(values[i][j][q]);
+        each([&](int i, int j) {
+            *reinterpret_cast<f16x4*>(lds + place(down + i * kSide + quad, (over + j * kSide) / 4)) =
+                quad_transpose(values[i][j]);
         });
         __syncthreads();
         write_rows(along + r0 * along_ld + c0, along_ld, skip_rows, skip_cols);
     } else {
         // The orthogonalised matrix in bf16, as bits.
-        each([&](int i, int j, int q) {
+        each([&](int i, int j) {
             typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-            const u32x2_t bits = {zero::dev::pack_bf16(alpha * acc[i][j][q * 4], alpha * acc[i][j][q * 4 + 1]),
-                                  zero::dev::pack_bf16(alpha * acc[i][j][q * 4 + 2], alpha * acc[i][j][q * 4 + 3])};
-            *reinterpret_cast<f16x4*>(lds + place(down + i * 32 + q * 8 + quad, (over + j * 32) / 4)) =
+            const u32x2_t bits = {zero::dev::pack_bf16(alpha * acc[i][j][0], alpha * acc[i][j][1]),
+                                  zero::dev::pack_bf16(alpha * acc[i][j][2], alpha * acc[i][j][3])};
+            *reinterpret_cast<f16x4*>(lds + place(down + i * kSide + quad, (over + j * kSide) / 4)) =
                 quad_transpose(__builtin_bit_cast(f16x4, bits));
         });
         __syncthreads();

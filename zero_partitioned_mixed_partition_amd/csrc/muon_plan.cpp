@@ -168,7 +168,7 @@ struct TileCost {
     double launch, tile, alone, share;
 };
 constexpr TileCost kCosts[kTileSizes] = {
-    {5.0, 0.6, 0.33, 0.27}, {6.0, 2.0, 0.58, 0.64}, {3.0, 6.0, 1.08, 1.08}, {3.0, 10.0, 1.33, 1.62}};
+    {5.0, 0.6, 0.30, 0.23}, {6.0, 2.0, 0.62, 0.52}, {3.0, 6.0, 0.96, 1.02}, {3.0, 9.0, 1.18, 1.45}};
 
 double product_time(const TileCost& c, double tiles, double stages) {
     if (tiles == 0.0) return 0.0;

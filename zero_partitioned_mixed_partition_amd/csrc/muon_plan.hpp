@@ -116,8 +116,8 @@ inline int64_t pad(int64_t x, int64_t tile) { return (x + tile - 1) / tile * til
 // The tiles of a call's products by an estimate of five steps' time with each pair: 64, 128, 192 or 256 for those of
 // square matrices, 64, 128 or 256 for those with X's shape. Sums over K are measured in stages of 64. Larger tiles read
 // less for each product; smaller ones fill the chip from fewer matrices and pad less. 192 is for the last round of
-// workgroups, which with 256 can leave half of the chip idle: X X^T of a side of 4096 has 136 tiles of 256 (98 us at K
-// 4096) and 253 of 192 (79 us); where both fill whole rounds 256 is up to a fifth faster.
+// workgroups, which with 256 can leave half of the chip idle: X X^T of a side of 4096 has 136 tiles of 256 (87 us at K
+// 4096) and 253 of 192 (70 us); where both fill whole rounds 256 is up to a sixth faster.
 constexpr int kTileSizes = 4;
 class TileChoice {
 public:
