@@ -660,18 +660,23 @@ zero_status zero_state8_dequantize(const uint8_t* codes, const uint8_t* scales, 
  * or NaN gives NaN throughout, and no other matrix of the call is touched by it.
  * Precision: products of fp16 values (scaled by powers of two) summed in fp32,
  * the first X of fp32 inputs held in two fp16 parts where it is multiplied; about
- * 2e-3 of the result's Frobenius norm off the exact steps, as much as rounding
- * it to bf16. Singular values below about 1e-5 of the norm, and directions
+ * 1.5e-3 of the result's Frobenius norm off the exact steps, less than rounding
+ * it to bf16 (1.7e-3). Where no matrix of a call has a short side above 128 and
+ * the coefficients are like these all values are held in two fp16 parts, and it
+ * is about 3e-5. Singular values below
+ * about 1e-5 of the norm, and directions
  * that G does not have, come out as noise of up to 0.02; elements below 3e-10
- * (a norm far below eps) as zeros or noise of that size. Deterministic: no atomics.
+ * (a norm far below eps) as zeros or noise of that size. Two steps are taken as
+ * one on the smaller side where that saves work and the first's |a| is at most 4.
+ * Deterministic: no atomics.
  *
  * coefficients host [3 * n_steps] doubles, (a, b, c) of each step.
  * n_steps      1..32.
  * eps          >= 0.
  * workspace    device, 256-byte aligned, zero_muon_workspace_bytes(count, rows,
  *              cols) bytes or more (0 where the arguments are refused or there is nothing to do):
- *              8 bytes an element and 6 per element of the smaller side's
- *              square, both padded to whole tiles. It needs no initialisation, its
+ *              about 8 bytes an element and 6 per element of the smaller side's
+ *              square, both sides padded (to 64 or more). It needs no initialisation, its
  *              contents on return are unspecified, and calls that may run at the
  *              same time need separate ones.
  * Sides: the shorter up to 65,536, the longer up to 2^22.

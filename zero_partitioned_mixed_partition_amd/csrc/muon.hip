@@ -9,7 +9,7 @@
 //
 // One call is: the momentum pass (momentum written, |u|^2 as fixed-order
 // partial sums), the packing (u scaled by a power of two into fp16, in both
-// orders of storage and padded to whole tiles, so that every product reads
+// orders of storage and padded with zeros, so that every product reads
 // rows of contiguous K and needs no bounds checks), then the products, each one
 // launch over the tiles of every matrix of the call; the last one's epilogue is
 // the weight update.
@@ -34,7 +34,8 @@ namespace {
 using namespace zero::muon;
 using namespace zero::muon::dev;
 
-// Momentum and squared norm: each workgroup takes one chunk of one matrix.
+// Momentum and squared norm: each workgroup takes one chunk of one matrix. Bound by HBM: 10 bytes an element read and
+// written at 5.3 TB/s (two 8192 x 8192: 254 us; a copy of 1 GB runs at 5.1).
 template <int kSource>
 __global__ __launch_bounds__(kThreads) void momentum_kernel(Matrices m, MomentumScalars s) {
     __shared__ double lds[kThreads / zero::dev::kWave];
@@ -77,7 +78,8 @@ __device__ __forceinline__ f16* buffer(const Matrices& m, const Desc& d, int32_t
 
 // Packs a 64 x 64 tile of the padded matrix: u * 2^(13 - e), where |u| lies in [2^e, 2^(e + 1)), as fp16 in both
 // orders, and with kLowPart what the rounding left. X is 2^-14 kappa times what is held. A thread holds 4 x 4 values;
-// the other order goes through LDS, so that both are written in rows of 128 bytes.
+// the other order goes through LDS, so that both are written in rows of 128 bytes. Bound by HBM: 12 bytes an element (u
+// formed again from 6, three fp16 arrays written) at 4.9 TB/s (two 8192 x 8192: 324 us).
 template <int kSource, bool kLowPart>
 __global__ __launch_bounds__(kThreads) void pack_kernel(Matrices m, MomentumScalars s, double eps) {
     __shared__ f16x4 turned[kLowPart ? 2 : 1][kPack * kPack / 4];
@@ -218,6 +220,14 @@ __device__ __forceinline__ uint32_t xcd_tile(uint32_t run) {
 }
 
 // One T x T tile of a product, both operands rows of contiguous K.
+//
+// With 256 the MFMAs bound it and the chip's power their clock: two applies of 8192 x 8192 x 8192 take 1.60 ms, 1375
+// TFLOP/s (the library's product of that size 1395), the MFMAs busy 71 % of the time at 1.84 GHz (2048 of a stage's 2,800
+// cycles; its loads, 64 KB into one compute unit's LDS, need 1024). Symmetric products run at the same
+// rate, but their 1056 tiles take five rounds of 256 workgroups where 4.1 hold them (0.92-1.0 ms). Where the tiles are
+// few (487 x 1000: 36 of 64 x 64, 7.2 us a product) it is latency: 1.4 us of launch, 1 to the first load, 2.4 for eight
+// stages, 1.8 for the way out through LDS. One workgroup's rows of K come straight from memory to LDS
+// (16 bytes a lane), so that no register holds what is on its way.
 template <int T, int kStages, bool kSquareOut, int kEnd>     // kEnd: 0 workspace, 1 orthogonalised matrix, 2 weight update
 __device__ __forceinline__ void product(const Matrices& m, const Product& p, const Update& u, uint32_t run) {
     constexpr int MI = T / kSide / kRows, NI = T / kSide / kCols;
