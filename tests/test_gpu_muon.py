@@ -97,9 +97,11 @@ def on_gpu_in_64_bits(x, steps=STEPS, eps=1e-7):
     return x
 
 
-@pytest.mark.parametrize("count,rows,cols", [(1, 2853, 3010), (1, 3010, 2853), (1, 4417, 4600), (9, 1030, 1100), (1, 2200, 2201), (3, 400, 5000)])
+@pytest.mark.parametrize("count,rows,cols", [(1, 2853, 3010), (1, 3010, 2853), (1, 4417, 4600), (9, 1030, 1100), (1, 2200, 2201), (3, 400, 5000),
+                                             (1, 5950, 6001), (4, 2900, 2853)])
 def test_tiles_that_end_inside_the_one_before(zm, count, rows, cols):
-    """Sides that are no multiple of the tiles that such sizes take: each value is written once, by one workgroup."""
+    """Sides that are no multiple of the tiles that such sizes take (the last two: tiles of which the last few are cut into
+    quarters): each value is written once, by one workgroup."""
     note(f"{count} x {rows} x {cols}")
     x = to_dev_f32(matrices(7, count, rows, cols, strong=3).reshape(-1))
     out = [torch.full((x.numel() + 64,), 0x55, dtype=torch.int16, device=dev()) for _ in range(2)]
@@ -237,7 +239,7 @@ def test_step_is_momentum_orthogonalize_and_update(zm, count, rows, cols, hyper)
     same(d, composed(zm, s, rows, cols, hyper), (rows, cols, hyper))
 
 
-@pytest.mark.parametrize("count,rows,cols", [(1, 2853, 3010), (1, 4600, 4417), (9, 1030, 1100)])
+@pytest.mark.parametrize("count,rows,cols", [(1, 2853, 3010), (1, 4600, 4417), (9, 1030, 1100), (4, 2853, 2900)])
 def test_a_step_with_large_tiles_updates_each_weight_once(zm, count, rows, cols):
     s = state(6, count * rows * cols)
     d = on_device(s)

@@ -219,37 +219,33 @@ __device__ __forceinline__ uint32_t xcd_tile(uint32_t run) {
     return (s / run * 8 + x) * run + s % run;
 }
 
+// Where a tile lies: its first row and column, how many of them another tile writes, and whether it is also written
+// mirrored.
+struct Place {
+    int32_t r0, c0, skip_rows, skip_cols;
+    bool mirror;
+};
+
+// Whether a product's last tiles can be cut into quarters.
+template <int T, bool kSquareOut>
+constexpr bool has_quarters = T == 256 && kSquareOut;
+
 // One T x T tile of a product, both operands rows of contiguous K.
 //
 // With 256 the MFMAs bound it and the chip's power their clock: two applies of 8192 x 8192 x 8192 take 1.60 ms, 1375
 // TFLOP/s (the library's product of that size 1395), the MFMAs busy 71 % of the time at 1.84 GHz (2048 of a stage's 2,800
-// cycles; its loads, 64 KB into one compute unit's LDS, need 1024). Symmetric products run at the same
-// rate, but their 1056 tiles take five rounds of 256 workgroups where 4.1 hold them (0.92-1.0 ms). Where the tiles are
-// few (487 x 1000: 36 of 64 x 64, 7.2 us a product) it is latency: 1.4 us of launch, 1 to the first load, 2.4 for eight
-// stages, 1.8 for the way out through LDS. One workgroup's rows of K come straight from memory to LDS
-// (16 bytes a lane), so that no register holds what is on its way.
+// cycles; its loads, 64 KB into one compute unit's LDS, need 1024). Symmetric products run at the same rate, half of
+// each computed. Where the tiles are few (487 x 1000: 36 of 64 x 64, 7.2 us a product) it is latency: 1.4 us of launch,
+// 1 to the first load, 2.4 for eight stages, 1.8 for the way out through LDS. Rows of K come straight from memory to
+// LDS (16 bytes a lane), so that no register holds what is on its way.
 template <int T, int kStages, bool kSquareOut, int kEnd>     // kEnd: 0 workspace, 1 orthogonalised matrix, 2 weight update
-__device__ __forceinline__ void product(const Matrices& m, const Product& p, const Update& u, uint32_t run) {
+__device__ __forceinline__ void tile(const Matrices& m, const Product& p, const Update& u, const Desc& d, const Place& at_place,
+                                     f16* lds) {
     constexpr int MI = T / kSide / kRows, NI = T / kSide / kCols;
     constexpr int kOperand = T * kDepth;                 // values of one operand's stage
     constexpr int kLoads = T / 8 / kWaves;               // of 8 rows each, a wave and operand
-    __shared__ __align__(16) f16 lds[kStages * 2 * kOperand];
-    static_assert(kStages * 2 * kOperand >= T * T, "the tile fits where the stages were");
-    if (kEnd == 2 && skipped(u.clip)) return;
-    uint32_t t = xcd_tile(run);
-    constexpr int kGrid = kSquareOut ? zero::muon::kByPair : zero::muon::kByTile;
-    if (t >= m.total[kGrid]) return;
-    const Desc d = find(m, kGrid, t, &t);
+    const int32_t r0 = at_place.r0, c0 = at_place.c0, skip_rows = at_place.skip_rows, skip_cols = at_place.skip_cols;
     const bool tall = d.rows > d.cols;
-    const int32_t height = !kSquareOut && tall ? d.N : d.M, width = kSquareOut || tall ? d.M : d.N;
-    int32_t bi, bj;
-    if constexpr (kSquareOut)
-        triangle_tile(t, (height + T - 1) / T, &bi, &bj);
-    else
-        rect_tile(t, (height + T - 1) / T, (width + T - 1) / T, &bi, &bj);
-    // The last tiles end with the matrix; the rows and columns that they share with the tiles before are those tiles'.
-    const int32_t r0 = min(bi * T, height - T), c0 = min(bj * T, width - T);
-    const int32_t skip_rows = bi * T - r0, skip_cols = bj * T - c0;
     const int32_t K = p.kind == Kind::kGram ? d.N : d.M, ld = stride(K);
     const f16* left = buffer(m, d, p.lhs);
     const f16* right = buffer(m, d, p.rhs);
@@ -486,7 +482,7 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
             }
         });
         if (p.add != zero::muon::kNone) __syncthreads();
-        if (bi != bj) {
+        if (at_place.mirror) {
             each([&](int i, int j) {
                 *reinterpret_cast<f16x4*>(lds + place(over + j * kSide, (down + i * kSide) / 4)) = values[i][j];
             });
@@ -560,9 +556,59 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
     }
 }
 
+// The tile of a workgroup. Tiles from `whole` on, the few that a last round of 256 x 256 would be for, are cut into
+// quarters, each a workgroup's (a side of 8192 has 528 tiles, of which 512 fill two rounds: 570 to 510 us at K 8192).
 template <int T, int kStages, bool kSquareOut, int kEnd>
-__global__ __launch_bounds__(64 * kWaves) void product_kernel(Matrices m, Product p, Update u, uint32_t run) {
-    product<T, kStages, kSquareOut, kEnd>(m, p, u, run);
+__device__ __forceinline__ void product(const Matrices& m, const Product& p, const Update& u, uint32_t run, uint32_t whole) {
+    constexpr int kValues = kStages * 2 * T * kDepth;    // values of all stages
+    __shared__ __align__(16) f16 lds[kValues];
+    static_assert(kValues >= T * T, "the tile fits where the stages were");
+    if (kEnd == 2 && skipped(u.clip)) return;
+    uint32_t t = xcd_tile(run), quarter = 0;
+    const bool cut = has_quarters<T, kSquareOut> && t >= whole;
+    if (cut) {
+        quarter = (t - whole) % 4;
+        t = whole + (t - whole) / 4;
+    }
+    constexpr int kGrid = kSquareOut ? zero::muon::kByPair : zero::muon::kByTile;
+    if (t >= m.total[kGrid]) return;
+    const Desc d = find(m, kGrid, t, &t);
+    const bool tall = d.rows > d.cols;
+    const int32_t height = !kSquareOut && tall ? d.N : d.M, width = kSquareOut || tall ? d.M : d.N;
+    int32_t bi, bj;
+    if constexpr (kSquareOut)
+        triangle_tile(t, (height + T - 1) / T, &bi, &bj);
+    else
+        rect_tile(t, (height + T - 1) / T, (width + T - 1) / T, &bi, &bj);
+    // The last tiles end with the matrix; the rows and columns that they share with the tiles before are those tiles'.
+    Place at;
+    at.r0 = min(bi * T, height - T);
+    at.c0 = min(bj * T, width - T);
+    at.skip_rows = bi * T - at.r0;
+    at.skip_cols = bj * T - at.c0;
+    at.mirror = bi != bj;
+    if constexpr (has_quarters<T, kSquareOut>) {
+        if (cut) {
+            constexpr int kHalf = T / 2;
+            const int32_t down = quarter / 2 * kHalf, right = quarter % 2 * kHalf;
+            if (bi == bj && down < right) return;        // the one below the diagonal is mirrored there
+            if (at.skip_rows >= down + kHalf || at.skip_cols >= right + kHalf) return;
+            at.r0 += down;
+            at.c0 += right;
+            at.skip_rows = max(at.skip_rows - down, 0);
+            at.skip_cols = max(at.skip_cols - right, 0);
+            at.mirror = at.mirror || down != right;
+            return tile<kHalf, kStages, kSquareOut, kEnd>(m, p, u, d, at, lds);
+        }
+    }
+    tile<T, kStages, kSquareOut, kEnd>(m, p, u, d, at, lds);
+}
+
+template <int T, int kStages, bool kSquareOut, int kEnd>
+__global__ __launch_bounds__(64 * kWaves) void product_kernel(Matrices m, Product p, Update u, uint32_t run, uint32_t whole) {
+#ifdef __HIP_DEVICE_COMPILE__                            // the host has no such instructions
+    product<T, kStages, kSquareOut, kEnd>(m, p, u, run, whole);
+#endif
 }
 
 // ------------------------------------------------------------ launches
@@ -581,11 +627,13 @@ struct Call {
 template <int T, int kStages, bool kSquareOut, int kEnd>
 void launch_product(const Matrices& m, const Product& p, const Update& u, hipStream_t stream) {
     // Whole runs on every XCD; no run longer than an eighth of the tiles, so that a short grid reaches every XCD.
-    const uint32_t total = m.total[kSquareOut ? zero::muon::kByPair : zero::muon::kByTile];
+    const uint32_t tiles = m.total[kSquareOut ? zero::muon::kByPair : zero::muon::kByTile];
+    const uint32_t whole = has_quarters<T, kSquareOut> ? zero::muon::whole_tiles(tiles) : tiles;
+    const uint32_t total = whole + 4 * (tiles - whole);
     const uint32_t run = std::min(32u, (total + 7) / 8);
     const uint32_t blocks = (total + 8 * run - 1) / (8 * run) * (8 * run);
     hipLaunchKernelGGL((product_kernel<T, kStages, kSquareOut, kEnd>), dim3(blocks),
-                       dim3(64 * kWaves), 0, stream, m, p, u, run);
+                       dim3(64 * kWaves), 0, stream, m, p, u, run, whole);
 }
 
 template <bool kSquareOut, int kEnd>

@@ -176,6 +176,18 @@ double product_time(const TileCost& c, double tiles, double stages) {
     return c.launch + c.tile * load + stages / tiles * (load > 1.0 ? std::max(c.alone, c.share * load) : c.alone);
 }
 
+// Of a square product's tiles kTiles[k].
+double square_time(int k, double tiles, double stages) {
+    if (kTiles[k] == 256 && tiles < 1e9) {
+        const double whole = whole_tiles(static_cast<uint32_t>(tiles));
+        if (whole < tiles) {
+            const double each = stages / tiles;          // a quarter of a tile is one of 128, alone on its unit
+            return product_time(kCosts[k], whole, each * whole) + kCosts[1].tile + each * kCosts[1].alone;
+        }
+    }
+    return product_time(kCosts[k], tiles, stages);
+}
+
 int64_t padded(int64_t side, int64_t tile) { return std::max(pad(side, 64), tile); }
 
 }  // namespace
@@ -206,8 +218,7 @@ void TileChoice::best(int64_t* square, int64_t* rect) const {
             if (kTiles[j] == 192) continue;
             const Total& x = total_[k][j];
             // as five steps in pairs: 3 products X X^T, 11 of square matrices, 3 applies and the first one's low part
-            const double time = 3 * product_time(kCosts[k], x.square, x.gram) +
-                                11 * product_time(kCosts[k], x.square, x.squares) +
+            const double time = 3 * square_time(k, x.square, x.gram) + 11 * square_time(k, x.square, x.squares) +
                                 4 * product_time(kCosts[j], x.rect, x.apply);
             if (*square == 0 || time < least) {
                 *square = kTiles[k];

@@ -131,6 +131,13 @@ private:
     } total_[kTileSizes][kTileSizes];
 };
 
+// Of `tiles` 256-tiles of square products those that are computed whole: all but a last round that fills at most a
+// quarter of the chip, whose quarters then do.
+constexpr uint32_t whole_tiles(uint32_t tiles) {
+    const uint32_t last = tiles % kUnits;
+    return tiles > kUnits && last <= kUnits / 4 ? tiles - last : tiles;
+}
+
 // Fills in M, N, chunk and chunks of a matrix of rows x cols, whose sides are padded to `tile` at least.
 void shape(Desc* d, int64_t rows, int64_t cols, int64_t tile);
 
