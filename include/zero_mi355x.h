@@ -659,9 +659,10 @@ zero_status zero_state8_dequantize(const uint8_t* codes, const uint8_t* scales, 
  * 1.2. A zero matrix gives zeros (with eps = 0 too); one that holds an infinity
  * or NaN gives NaN throughout, and no other matrix of the call is touched by it.
  * Precision: products of fp16 values (scaled by powers of two) summed in fp32,
- * the first X of fp32 inputs held in two fp16 parts where it is multiplied; about
- * 1.5e-3 of the result's Frobenius norm off the exact steps, less than rounding
- * it to bf16 (1.7e-3). Where no matrix of a call has a short side above 128 and
+ * with what rounding the first X of fp32 inputs left carried past the first of
+ * them; about 1.5e-3 of the result's Frobenius norm off the exact steps, less than
+ * rounding it to bf16 (1.7e-3), and up to 8e-3 where nearly all of the norm lies in
+ * one direction or half of the singular values lie far below the rest. Where no matrix of a call has a short side above 128 and
  * the coefficients are like these all values are held in two fp16 parts, and it
  * is about 3e-5. Singular values below
  * about 1e-5 of the norm, and directions

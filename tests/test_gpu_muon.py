@@ -124,6 +124,15 @@ def test_step_counts(zm, shape, steps):
     check(got, [oracle.muon.orthogonalize(m, STEPS[:1] * steps) for m in x], (shape, steps))
 
 
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 7])
+@pytest.mark.parametrize("shape", [(1, 150, 260), (1, 260, 150), (2, 200, 200)])
+def test_step_counts_of_the_tiled_form(zm, shape, steps, bf16):
+    """Sides past 128; with one step or two the first apply, which adds what rounding X left, is the last product."""
+    got, x = run(zm, matrices(steps, *shape), bf16, coefficients=STEPS[:1] * steps)
+    check(got, [oracle.muon.orthogonalize(m, STEPS[:1] * steps) for m in x], (shape, steps))
+
+
 def test_other_coefficients(zm):
     """Steps of their own each, growing and shrinking, and one that is the identity."""
     steps = ((2.0, -1.5, 0.5), (1.5, -0.5, 0.0), (1.0, 0.0, 0.0), (1.875, -1.25, 0.375), (0.25, 0.0, 0.0))

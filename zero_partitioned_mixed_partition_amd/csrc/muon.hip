@@ -69,10 +69,10 @@ __device__ __forceinline__ f16* buffer(const Matrices& m, const Desc& d, int32_t
         case zero::muon::kX: return at;
         case zero::muon::kT0: return at + x;
         case zero::muon::kT1: return at + x + xt;
-        case zero::muon::kLow: return at + x + 2 * xt;
-        case zero::muon::kS0: return at + x + 3 * xt;
-        case zero::muon::kS1: return at + x + 3 * xt + mm;
-        default: return at + x + 3 * xt + 2 * mm;
+        case zero::muon::kS0: return at + x + 2 * xt;
+        case zero::muon::kS1: return at + x + 2 * xt + mm;
+        case zero::muon::kS2: return at + x + 2 * xt + 2 * mm;
+        default: return at + x + 2 * xt + 3 * mm;        // kLow
     }
 }
 
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(Matrices m, MomentumScal
     }
     f16* const along = buffer(m, d, tall ? zero::muon::kT0 : zero::muon::kX);
     f16* const across = buffer(m, d, tall ? zero::muon::kX : zero::muon::kT0);
-    f16* const rest = buffer(m, d, zero::muon::kLow);                  // [N][M], as kT0
+    f16* const rest = buffer(m, d, zero::muon::kLow);                  // as `across`
     // Column 4 right + j of the tile, its piece `down` of four rows, at place down ^ right.
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -140,8 +140,6 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(Matrices m, MomentumScal
     for (int k = 0; k < 4; ++k) {
         const int64_t at = static_cast<int64_t>(r0 + down * 4 + k) * stride(padded_cols) + c0 + right * 4;
         *reinterpret_cast<f16x4*>(along + at) = high[k];
-        if constexpr (kLowPart)
-            if (tall) *reinterpret_cast<f16x4*>(rest + at) = low[k];
     }
     __syncthreads();
 #pragma unroll
@@ -150,7 +148,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(Matrices m, MomentumScal
         const int64_t at = static_cast<int64_t>(c0 + c) * stride(padded_rows) + r0 + right * 4;
         *reinterpret_cast<f16x4*>(across + at) = turned[0][c * 16 + (right ^ (c / 4))];
         if constexpr (kLowPart)
-            if (!tall) *reinterpret_cast<f16x4*>(rest + at) = turned[1][c * 16 + (right ^ (c / 4))];
+            *reinterpret_cast<f16x4*>(rest + at) = turned[1][c * 16 + (right ^ (c / 4))];
     }
 }
 
@@ -246,6 +244,7 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
     constexpr int kLoads = T / 8 / kWaves;               // of 8 rows each, a wave and operand
     const int32_t r0 = at_place.r0, c0 = at_place.c0, skip_rows = at_place.skip_rows, skip_cols = at_place.skip_cols;
     const bool tall = d.rows > d.cols;
+    const int32_t height = tall ? d.N : d.M;             // of an apply's output
     const int32_t K = p.kind == Kind::kGram ? d.N : d.M, ld = stride(K);
     const f16* left = buffer(m, d, p.lhs);
     const f16* right = buffer(m, d, p.rhs);
@@ -261,7 +260,7 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
     const int wr = wave / kCols * (MI * kSide), wc = wave % kCols * (NI * kSide);
 
     // Global to LDS: lane l of a load brings the piece that belongs at place l % 8 of row l / 8.
-    const int32_t steps = K / kDepth, all = p.with_low ? 2 * steps : steps;
+    const int32_t all = K / kDepth;
     __amdgpu_buffer_rsrc_t from[2] = {zero::dev::through_rsrc(left), zero::dev::through_rsrc(right)};
     uint32_t at[kLoads];
     const int row = lane / 8;
@@ -273,7 +272,7 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
     // Load q of stage s: the left operand's kLoads, then the right's.
     auto load = [&](int32_t s, int q) {
         f16* const to = lds + (s % kStages) * 2 * kOperand;
-        const uint32_t k = static_cast<uint32_t>(s < steps ? s : s - steps) * (kDepth * 2);
+        const uint32_t k = static_cast<uint32_t>(s) * (kDepth * 2);
         const int o = q / kLoads, i = q % kLoads;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             from[o], (lds_void*)(to + o * kOperand + (wave * kLoads + i) * 8 * kDepth), 16, at[i], k, 0, 0);
@@ -281,10 +280,6 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
     auto load_all = [&](int32_t s) {
 #pragma unroll
         for (int q = 0; q < 2 * kLoads; ++q) load(s, q);
-    };
-    auto use_low = [&] {                                 // the low part of X takes its place
-        const f16* const low = buffer(m, d, zero::muon::kLow) + static_cast<int64_t>(tall ? r0 : c0) * ld;
-        from[tall ? 0 : 1] = zero::dev::through_rsrc(low);
     };
     const int turn = (lane % kSide) >> 1;                // of the lane's rows in a fragment
     const int a_row = (wr + lane % kSide) * kDepth, b_row = kOperand + (wc + lane % kSide) * kDepth;
@@ -331,10 +326,7 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
 #pragma unroll
                 for (int q = 0; q < kProducts; ++q) {
                     const int at = first + q - kFree;    // products since the barrier
-                    if (at == 0) {
-                        landed_and_barrier<0>();
-                        if (p.with_low && s + 2 == steps) use_low();
-                    }
+                    if (at == 0) landed_and_barrier<0>();
                     multiply(now, q);
 #pragma unroll
                     for (; reads * kProducts < (q + 1) * kReads * 2 && reads < kReads; ++reads) read(from_stage, kk, reads, next);
@@ -347,7 +339,6 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
             phase(f1, f0, s + 1, 0, kProducts);          // (what it reads after the last stage is not used)
         };
         load_all(0);
-        if (p.with_low && steps == 1) use_low();
         if (1 < all) load_all(1);
         if (1 < all)
             landed_and_barrier<2 * kLoads>();
@@ -370,7 +361,6 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
                 landed_and_barrier<kFlying>();           // stages s + 2 to s + kStages - 1 may fly
             else
                 landed_and_barrier<0>();
-            if (p.with_low && s + kStages == steps) use_low();
             if (s + kStages < all) load_all(s + kStages);
             int reads = 0;
 #pragma unroll
@@ -383,10 +373,8 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
             }
         };
 #pragma unroll
-        for (int s = 0; s < kStages; ++s) {
-            if (p.with_low && s == steps) use_low();
+        for (int s = 0; s < kStages; ++s)
             if (s < all) load_all(s);
-        }
         if (all >= kStages)
             landed_and_barrier<(kStages - 1) * 2 * kLoads>();
         else
@@ -409,10 +397,11 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
 
     // A lane holds one column of each MFMA tile, four consecutive rows at a time; LDS turns them into whole rows, in
     // either order of storage, so that memory is read and written 16 bytes a lane and 2 T bytes a row.
-    float alpha = p.alpha;
+    float alpha = p.alpha, low = p.low;
     if (p.kappa_power > 0) {
         const float kappa = m.kappa[d.id];
         alpha = p.kappa_power == 2 ? alpha * (kappa * kappa) : alpha * kappa;
+        low *= kappa;
     }
     const int down = wr + lane / kSide * 4, over = wc + lane % kSide;  // the lane's first row, and its column
     const int quad = lane % 4;
@@ -441,6 +430,20 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
             }
         }
     };
+    // And `from` there.
+    auto read_rows = [&](const f16* from, int64_t ld) {
+        constexpr int kAtOnce = kOwn < 8 ? kOwn : kOwn % 8 == 0 ? 8 : 6;
+#pragma unroll 1
+        for (int k0 = 0; k0 < kOwn; k0 += kAtOnce) {
+            f16x8 x[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                x[k] = *reinterpret_cast<const f16x8*>(from + row_of(k0 + k) * ld + piece_of(k0 + k) * 8);
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                *reinterpret_cast<f16x8*>(lds + place(row_of(k0 + k), piece_of(k0 + k) * 2)) = x[k];
+        }
+    };
     // Calls f(i, j) for the lane's groups of four rows.
     auto each = [&](auto f) {
 #pragma unroll
@@ -450,23 +453,26 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
     };
     f16x4 values[MI][NI];
     __syncthreads();
+    // The first apply's low part of X, times Q's value at the eigenvalue 0.
+    if constexpr (!kSquareOut)
+        if (low != 0.0f) {
+            const int64_t low_ld = stride(height);
+            read_rows(buffer(m, d, zero::muon::kLow) + c0 * low_ld + r0, low_ld);
+            __syncthreads();
+            each([&](int i, int j) {
+                const f16x4 x = *reinterpret_cast<const f16x4*>(lds + place(over + j * kSide, (down + i * kSide) / 4));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[i][j][k] = alpha * acc[i][j][k] + low * static_cast<float>(x[k]);
+            });
+            alpha = 1.0f;
+            __syncthreads();
+        }
     if constexpr (kSquareOut) {
         f16* const out = buffer(m, d, p.out);
         const int64_t ldm = stride(d.M);
         const int64_t direct = r0 * ldm + c0, mirrored = c0 * ldm + r0;
         if (p.add != zero::muon::kNone) {                // symmetric: its mirrored tile's rows are this one's columns
-            const f16* const add = buffer(m, d, p.add) + mirrored;
-            constexpr int kAtOnce = kOwn < 8 ? kOwn : kOwn % 8 == 0 ? 8 : 6;
-#pragma unroll 1
-            for (int k0 = 0; k0 < kOwn; k0 += kAtOnce) {
-                f16x8 x[kAtOnce];
-#pragma unroll
-                for (int k = 0; k < kAtOnce; ++k)
-                    x[k] = *reinterpret_cast<const f16x8*>(add + row_of(k0 + k) * ldm + piece_of(k0 + k) * 8);
-#pragma unroll
-                for (int k = 0; k < kAtOnce; ++k)
-                    *reinterpret_cast<f16x8*>(lds + place(row_of(k0 + k), piece_of(k0 + k) * 2)) = x[k];
-            }
+            read_rows(buffer(m, d, p.add) + mirrored, ldm);
             __syncthreads();
         }
         const int diagonal = c0 - r0 + over - down;               // row minus `down` of the lane's first column

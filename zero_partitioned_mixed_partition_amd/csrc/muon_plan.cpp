@@ -100,7 +100,10 @@ zero_status make_program(const double* coefficients, int32_t n_steps, bool pairs
         Product* p = product(last ? Kind::kFinal : Kind::kApply, q, from, last ? kNone : kX,
                              pow2((last ? 0 : eN) - eQ - eX));
         p->out_t = last ? kNone : to;
-        p->with_low = first && low;
+        // Q times what rounding the first X left: in directions that X hardly has Q is its value at 0, a or a a', and only
+        // there is the rounding magnified (simulated on twelve spectra: as exact as the product, to two digits).
+        if (first && low)
+            p->low = static_cast<float>(pow2((last ? 0 : eN) - eX) * a * (pair ? coefficients[3 * at - 3] : 1.0));
         p->kappa_power = first ? 1 : 0;
         std::swap(from, to);
         eX = eN;
@@ -217,9 +220,9 @@ void TileChoice::best(int64_t* square, int64_t* rect) const {
         for (int j = 0; j < kTileSizes; ++j) {
             if (kTiles[j] == 192) continue;
             const Total& x = total_[k][j];
-            // as five steps in pairs: 3 products X X^T, 11 of square matrices, 3 applies and the first one's low part
+            // as five steps in pairs: 3 products X X^T, 11 of square matrices, 3 applies
             const double time = 3 * square_time(k, x.square, x.gram) + 11 * square_time(k, x.square, x.squares) +
-                                4 * product_time(kCosts[j], x.rect, x.apply);
+                                3 * product_time(kCosts[j], x.rect, x.apply);
             if (*square == 0 || time < least) {
                 *square = kTiles[k];
                 *rect = kTiles[j];
@@ -252,7 +255,7 @@ int64_t grid_count(const Desc& d, int grid, int64_t square_tile, int64_t rect_ti
 
 int64_t area_bytes(const Desc& d) {
     const int64_t m = d.M, n = d.N, ldm = stride(d.M), ldn = stride(d.N);
-    return pad(2 * (m * ldn + 3 * n * ldm + 3 * m * ldm), 256);
+    return pad(2 * (m * ldn + 2 * n * ldm + 3 * m * ldm + std::max(m * ldn, n * ldm)), 256);
 }
 
 int64_t head_bytes(int64_t partials, int64_t matrices) { return pad(8 * partials + 4 * matrices, 256); }

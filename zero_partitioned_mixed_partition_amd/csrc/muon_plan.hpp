@@ -33,7 +33,7 @@ enum Buffer : int32_t {
     kS0 = 3,     // [M][M]: three square ones for A, C and their products
     kS1 = 4,
     kS2 = 5,
-    kLow = 6,    // [N][M]: what rounding the transposed first X to fp16 left (fp32 inputs)
+    kLow = 6,    // what rounding the first X to fp16 left (fp32 inputs), the source transposed
     kNone = 7,
 };
 
@@ -51,9 +51,9 @@ enum class Kind : int32_t {
 struct Product {
     Kind kind;
     int32_t lhs, rhs, add, out, out_t;
-    int32_t with_low;        // the rhs is kT0 + kLow
     int32_t kappa_power;
     float alpha, beta, diag;
+    float low;               // not 0: low * kappa * kLow is added
 };
 
 // The most steps one call takes.
