@@ -668,8 +668,9 @@ zero_status zero_state8_dequantize(const uint8_t* codes, const uint8_t* scales, 
  * about 1e-5 of the norm, and directions
  * that G does not have, come out as noise of up to 0.02; elements below 3e-10
  * (a norm far below eps) as zeros or noise of that size. Two steps are taken as
- * one on the smaller side where that saves work and the first's |a| is at most 4.
- * Deterministic: no atomics.
+ * one on the smaller side where that saves time and the first's |a| is at most 4;
+ * this and the products' tiles follow the sizes and number of a call's matrices.
+ * The same call gives the same bits: no atomics.
  *
  * coefficients host [3 * n_steps] doubles, (a, b, c) of each step.
  * n_steps      1..32.
@@ -729,8 +730,8 @@ zero_status zero_muon_step(float* master, float* momentum, const uint16_t* grad,
 
 /* zero_muon_step over a list of matrices of any shapes, described once in
  * device memory (as zero_mt_table_*): every product is one launch over all of
- * them. The results are zero_muon_step's on each matrix, up to the choice of how the
- * steps are grouped (below its stated precision), which follows the whole list.
+ * them. The results are zero_muon_step's on each matrix, up to the choice of tiles and
+ * of how the steps are grouped (below its stated precision), which follows the whole list.
  * Create: host arrays of n_matrices pointers, sides and scales; a matrix without
  * elements is left out. hipMalloc and a synchronous hipMemcpy on the current
  * device, once (128 bytes a matrix and 4 per workgroup). The table keeps the pointers,

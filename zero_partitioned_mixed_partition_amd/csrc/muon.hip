@@ -627,7 +627,7 @@ struct Call {
     int source;                   // 0 bf16, 1 fp32, 2 momentum and gradient
     MomentumScalars momentum;
     Update update;
-    double cost[2];               // of one pair and single steps, and of pairs
+    zero::muon::Times times;
 };
 
 template <int T, int kStages, bool kSquareOut, int kEnd>
@@ -686,9 +686,11 @@ zero_status launch(const Matrices& m, const Call& c, hipStream_t stream, const c
     if (m.side != 0 && make_short_program(c.coefficients, c.n_steps, &steps))
         return launch_short(c.source, m, c.momentum, c.update, steps, c.eps, stream, who);
     std::vector<Product> program;
-    // Pairs where they save a twentieth of the multiplications or more: at equal cost the single steps, whose A comes
-    // from X itself, are more exact (about 1.2e-3 of the result's norm against 1.2e-3 to 1.9e-3).
-    const bool pairs = c.cost[1] < 0.95 * c.cost[0];
+    // Pairs where they save a fiftieth of the time or more (six GPT-2 small matrices: 350 us against 364; 487 x 1000: 135
+    // against 129): at equal time the single steps, whose A comes from X itself, are more exact (about 1.2e-3 of the
+    // result's norm against 1.2e-3 to 1.9e-3).
+    const bool pairs = zero::muon::program_time(c.times, c.n_steps, true) <
+                       0.98 * zero::muon::program_time(c.times, c.n_steps, false);
     try {
         const zero_status st = zero::muon::make_program(c.coefficients, c.n_steps, pairs, c.source != 0, &program, who);
         if (st != ZERO_OK) return st;
@@ -721,14 +723,15 @@ zero_status check_sides(int64_t rows, int64_t cols, const std::string& what) {
 
 constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / 512 - 256;         // fewer than 2^32 work-items a launch
 
-// A stack's sizes: its first matrix's descriptor (sides, chunks), the workgroups and the workspace. ZERO_ERANGE where
-// one launch does not hold it.
-zero_status measure_stack(int64_t count, int64_t rows, int64_t cols, Matrices* m, int64_t* bytes, const char* who) {
+// A stack's sizes: its first matrix's descriptor (sides, chunks), the workgroups, the products' times and the workspace.
+// ZERO_ERANGE where one launch does not hold it.
+zero_status measure_stack(int64_t count, int64_t rows, int64_t cols, Matrices* m, zero::muon::Times* times, int64_t* bytes,
+                          const char* who) {
     zero_status st = check_sides(rows, cols, who);
     if (st != ZERO_OK) return st;
     zero::muon::TileChoice choice;
     choice.add(count, rows, cols);
-    choice.best(&m->square_tile, &m->rect_tile);
+    choice.best(&m->square_tile, &m->rect_tile, times);
     zero::muon::shape(&m->base, rows, cols, std::max(m->square_tile, m->rect_tile));
     m->side = short_side(std::min(rows, cols));
     m->base.parts = m->side != 0 ? short_parts(m->side, std::max(rows, cols), count) : 1;
@@ -793,19 +796,15 @@ zero_status muon_call(double lr, double momentum, int32_t nesterov, double weigh
     return ZERO_OK;
 }
 
-// A call's cost with one pair and with pairs, summed over its matrices.
-void add_cost(Call* c, const Desc& d) {
-    for (int k = 0; k < 2; ++k) c->cost[k] += zero::muon::program_cost(c->n_steps, k != 0, std::min(d.rows, d.cols), std::max(d.rows, d.cols));
-}
-
 }  // namespace
 
 extern "C" size_t zero_muon_workspace_bytes(int64_t count, int64_t rows, int64_t cols) {
     Matrices m{};
     int64_t bytes = 0;
     bool empty = false;
+    zero::muon::Times times;
     if (check_counts(count, rows, cols, &empty, "zero_muon_workspace_bytes") != ZERO_OK || empty) return 0;
-    if (measure_stack(count, rows, cols, &m, &bytes, "zero_muon_workspace_bytes") != ZERO_OK) return 0;
+    if (measure_stack(count, rows, cols, &m, &times, &bytes, "zero_muon_workspace_bytes") != ZERO_OK) return 0;
     return static_cast<size_t>(bytes);
 }
 
@@ -824,8 +823,9 @@ extern "C" zero_status zero_orthogonalize(const void* x, int32_t x_type, uint16_
     if (st != ZERO_OK || empty) return st;
     if (!x || !out) return fail(ZERO_EINVAL, "zero_orthogonalize: NULL array");
     Matrices m{};
+    Call c{};
     int64_t need = 0;
-    st = measure_stack(count, rows, cols, &m, &need, who);
+    st = measure_stack(count, rows, cols, &m, &c.times, &need, who);
     if (st == ZERO_OK) st = check_workspace(workspace, workspace_bytes, need, who);
     if (st != ZERO_OK) return st;
     const size_t n = static_cast<size_t>(count * m.numel), size = x_type == ZERO_MATRIX_F32 ? 4 : 2;
@@ -837,12 +837,10 @@ extern "C" zero_status zero_orthogonalize(const void* x, int32_t x_type, uint16_
     m.base.out = out;
     m.src_bytes = m.numel * static_cast<int64_t>(size);
     place(&m, workspace, count * m.base.chunks);
-    Call c{};
     c.coefficients = coefficients;
     c.n_steps = n_steps;
     c.eps = eps;
     c.source = x_type == ZERO_MATRIX_F32 ? 1 : 0;
-    add_cost(&c, m.base);
     return launch(m, c, stream, who);
 }
 
@@ -865,7 +863,7 @@ extern "C" zero_status zero_muon_step(float* master, float* momentum, const uint
     if (!master || !momentum || !grad || !param_out) return fail(ZERO_EINVAL, "zero_muon_step: NULL array");
     Matrices m{};
     int64_t need = 0;
-    st = measure_stack(count, rows, cols, &m, &need, who);
+    st = measure_stack(count, rows, cols, &m, &c.times, &need, who);
     if (st == ZERO_OK) st = check_workspace(workspace, workspace_bytes, need, who);
     if (st != ZERO_OK) return st;
     const size_t n = static_cast<size_t>(count * m.numel);
@@ -883,7 +881,6 @@ extern "C" zero_status zero_muon_step(float* master, float* momentum, const uint
     m.base.scale = scale;
     m.src_bytes = 2 * m.numel;
     place(&m, workspace, count * m.base.chunks);
-    add_cost(&c, m.base);
     return launch(m, c, stream, who);
 }
 
@@ -896,6 +893,7 @@ struct zero_muon_table {
     Matrices m{};
     int64_t partials = 0;
     int64_t bytes = 0;                // of the workspace
+    zero::muon::Times times{};
 };
 
 extern "C" void zero_muon_table_free(zero_muon_table* table) {
@@ -914,7 +912,7 @@ zero_status fill_table(zero_muon_table* tab, const char* who) {
     if (tab->descs.empty()) return ZERO_OK;              // needs no device
     zero::muon::TileChoice choice;
     for (const Desc& d : tab->descs) choice.add(1, d.rows, d.cols);
-    choice.best(&tab->m.square_tile, &tab->m.rect_tile);
+    choice.best(&tab->m.square_tile, &tab->m.rect_tile, &tab->times);
     int64_t most = 0;
     for (const Desc& d : tab->descs) most = std::max<int64_t>(most, std::min(d.rows, d.cols));
     tab->m.side = short_side(most);
@@ -1071,8 +1069,8 @@ extern "C" zero_status zero_muon_table_step(const zero_muon_table* table, double
             {d.src, 2 * n, "grad"}, {d.momentum, 4 * n, "momentum"}, {d.master, 4 * n, "master"}, {d.out, 2 * n, "param_out"}};
         const std::string clash = zero::first_overlap(&ws, 1, others, 4);
         if (!clash.empty()) return fail(ZERO_EINVAL, std::string(who) + ": " + clash);
-        add_cost(&c, d);
     }
+    c.times = table->times;
     Matrices m = table->m;
     place(&m, workspace, table->partials);
     return launch(m, c, stream, who);

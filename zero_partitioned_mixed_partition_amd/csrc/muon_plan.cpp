@@ -38,9 +38,9 @@ zero_status check_coefficients(const double* coefficients, int32_t n_steps, cons
     return ZERO_OK;
 }
 
-double program_cost(int32_t n_steps, bool pairs, double m, double n) {
+double program_time(const Times& t, int32_t n_steps, bool pairs) {
     const int32_t two = n_steps < 2 ? 0 : pairs ? n_steps / 2 : 1, one = n_steps - 2 * two;
-    return m * m * (two * (3 * n + 5 * m) + one * (3 * n + m));
+    return two * (t.gram + 5 * t.square + t.apply) + one * (t.gram + t.square + t.apply);
 }
 
 zero_status make_program(const double* coefficients, int32_t n_steps, bool pairs, bool low, std::vector<Product>* out,
@@ -213,19 +213,20 @@ void TileChoice::add(int64_t count, int64_t rows, int64_t cols) {
     }
 }
 
-void TileChoice::best(int64_t* square, int64_t* rect) const {
+void TileChoice::best(int64_t* square, int64_t* rect, Times* times) const {
     double least = 0.0;
     *square = *rect = 0;
     for (int k = 0; k < kTileSizes; ++k) {
         for (int j = 0; j < kTileSizes; ++j) {
             if (kTiles[j] == 192) continue;
             const Total& x = total_[k][j];
-            // as five steps in pairs: 3 products X X^T, 11 of square matrices, 3 applies
-            const double time = 3 * square_time(k, x.square, x.gram) + 11 * square_time(k, x.square, x.squares) +
-                                3 * product_time(kCosts[j], x.rect, x.apply);
+            const Times t{square_time(k, x.square, x.gram), square_time(k, x.square, x.squares),
+                          product_time(kCosts[j], x.rect, x.apply)};
+            const double time = program_time(t, 5, true);
             if (*square == 0 || time < least) {
                 *square = kTiles[k];
                 *rect = kTiles[j];
+                *times = t;
                 least = time;
             }
         }

@@ -67,8 +67,13 @@ zero_status make_program(const double* coefficients, int32_t n_steps, bool pairs
 // ZERO_EINVAL for NULL or non-finite coefficients, or n_steps outside [1, kMaxSteps].
 zero_status check_coefficients(const double* coefficients, int32_t n_steps, const char* who);
 
-// Multiplications of one matrix's program, in units of the padded sides' products, for choosing between the two.
-double program_cost(int32_t n_steps, bool pairs, double m, double n);
+// Estimated microseconds of a call's products of each kind: X X^T, other square ones, applies.
+struct Times {
+    double gram, square, apply;
+};
+
+// And of its program, for choosing between the two.
+double program_time(const Times& t, int32_t n_steps, bool pairs);
 
 // ------------------------------------------------------------ sizes
 
@@ -122,7 +127,7 @@ constexpr int kTileSizes = 4;
 class TileChoice {
 public:
     void add(int64_t count, int64_t rows, int64_t cols);
-    void best(int64_t* square, int64_t* rect) const;
+    void best(int64_t* square, int64_t* rect, Times* times) const;
 
 private:
     struct Total {
