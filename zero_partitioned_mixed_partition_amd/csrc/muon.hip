@@ -303,7 +303,8 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
     };
     constexpr int kReads = MI + NI, kProducts = MI * NI;
     // In assembly, so that the sum stays where it is: the compiler may give the result of this shape other registers, and
-    // with 256 of them moves them all in every stage. (It also knows of no wait before the sums are read: see below.)
+    // with 256 of them moves them all in every stage. (A product that adds to
+    // the one before needs no wait; one before the sums are read is the compiler's no longer: see below.)
     auto multiply = [&](const Fragments& f, int q) {
         asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc[q / NI][q % NI]) : "v"(f.a[q / NI]), "v"(f.b[q % NI]));
     };
@@ -391,7 +392,7 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
         if (s < all) stage(s, f0, f1);                   // (what the last one reads is not used)
     }
 
-    // The last products take 8 passes of 4 cycles; nothing reads a sum before they are through.
+    // A sum may be read eight wait states after its last product (the compiler's own distance); these are 32.
     asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
     keep_sums();
 
