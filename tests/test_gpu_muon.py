@@ -124,6 +124,32 @@ def test_step_counts(zm, shape, steps):
     check(got, [oracle.muon.orthogonalize(m, STEPS[:1] * steps) for m in x], (shape, steps))
 
 
+@pytest.mark.parametrize("rows,cols", [(33000, 70000), (70000, 33001)])
+def test_past_2_to_the_31_elements(zm, rows, cols):
+    """One value a row of the shorter side, each in a column of its own: they are the singular values, and the result is
+    each one's polynomial in its place and zeros elsewhere."""
+    note(f"{rows} x {cols}")
+    m = min(rows, cols)
+    gen = torch.Generator(device=dev()).manual_seed(1)
+    values = (torch.rand(m, device=dev(), generator=gen) + 0.5).bfloat16()
+    short = torch.arange(m, device=dev())
+    at = short * cols + 2 * short + 1 if rows < cols else (2 * short + 1) * cols + short
+    x = torch.zeros(rows * cols, dtype=torch.bfloat16, device=dev())
+    x[at] = values
+    out = torch.empty_like(x)
+    zm.zero_orthogonalize(x, out, rows, cols)
+    del x
+    v = values.double()
+    v = v / (v.norm() + 1e-7)
+    for a, b, c in STEPS:
+        v = a * v + b * v ** 3 + c * v ** 5
+    got = out[at].double()
+    # of a row's products all but one are of zeros: each step rounds X, A, C and what they make, as in the bound above
+    assert ((got - v).abs() <= 2.0 ** -8 * v.abs() + 8 * 2.0 ** -11 * v.abs()).all(), float(((got - v) / v).abs().max())
+    out[at] = 0
+    assert not out.view(torch.int16).bitwise_and_(0x7fff).any()
+
+
 @pytest.mark.parametrize("bf16", [True, False])
 @pytest.mark.parametrize("steps", [1, 2, 3, 4, 7])
 @pytest.mark.parametrize("shape", [(1, 150, 260), (1, 260, 150), (2, 200, 200)])
