@@ -671,6 +671,12 @@ zero_status zero_state8_dequantize(const uint8_t* codes, const uint8_t* scales, 
  * one on the smaller side where that saves time and the first's |a| is at most 4;
  * this and the products' tiles follow the sizes and number of a call's matrices.
  * The same call gives the same bits: no atomics.
+ * Steps that contract to the very end of the interval that the one before leaves
+ * and grow steeply past it (the published Polar Express coefficients, undivided)
+ * would let fp16's roundings carry a singular value past that end. Where values are
+ * held in one fp16 part, such a set is taken with (a, b, c) / (s, s^3, s^5) in all
+ * steps but the last, s = 1 + 3 / 2048; divided by 1.003 or more those coefficients
+ * are taken as they are.
  *
  * coefficients host [3 * n_steps] doubles, (a, b, c) of each step.
  * n_steps      1..32.
@@ -688,8 +694,8 @@ zero_status zero_state8_dequantize(const uint8_t* codes, const uint8_t* scales, 
  * out          device [count * rows * cols] bf16, rounded to nearest even once.
  *              Must not overlap x or the workspace.
  * Errors: ZERO_EINVAL (an unknown x_type, a negative count or side, bad steps
- * or eps, coefficients that let singular values grow past 2^20; with something
- * to do, null pointers, a workspace not 256-byte aligned, overlapping arrays,
+ * or eps, coefficients that let singular values, with what roundings add to
+ * them, grow past 2^20; with something to do, null pointers, a workspace not 256-byte aligned, overlapping arrays,
  * named in zero_last_error()); ZERO_ERANGE (a side past its limit, or more
  * workgroups than one launch holds); ZERO_ENOSPACE; ZERO_ENOMEM; ZERO_EHIP.
  *

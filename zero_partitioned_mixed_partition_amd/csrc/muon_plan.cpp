@@ -18,13 +18,43 @@ float pow2(int e) { return static_cast<float>(std::ldexp(1.0, e)); }
 
 constexpr int kSamples = 2048;
 
-// The largest |f(x)| over [0, top], by samples, with a margin for what lies between them.
+// The largest |f(x)| over [0, top], by samples.
 template <typename F>
 double largest(double top, F f) {
     double most = 0.0;
     for (int i = 0; i <= kSamples; ++i) most = std::max(most, std::fabs(f(top * i / kSamples)));
-    return most * 1.02;
+    return most;
 }
+
+// For an exponent: a margin for what lies between the samples.
+int exponent_for_largest(double most) { return exponent_for(1.02 * most); }
+
+// The largest eigenvalue that a step leaves of those in [0, top].
+double step_top(const double* step, double top) {
+    return largest(top, [&](double x) {
+        const double p = step[0] + x * (step[1] + x * step[2]);
+        return x * p * p;
+    });
+}
+
+// How far the roundings of a step can carry an eigenvalue of X X^T past the end of its interval, relative to it. An fp16
+// value is off by at most 2^-11 of itself, and X counts twice, A once, C twice; in two fp16 parts 2^-22 of it.
+constexpr double kSlack = 5.0 / (1 << 11), kShortSlack = 5.0 / (1 << 22);
+
+// Whether every interval that the steps leave stays within a quarter of itself where roundings make each longer.
+bool steady(const double* coefficients, int32_t n_steps, double slack) {
+    double exact = 1.0, longer = 1.0;
+    for (int32_t i = 0; i < n_steps; ++i) {
+        exact = step_top(coefficients + 3 * i, exact);
+        longer = step_top(coefficients + 3 * i, longer * (1.0 + slack));
+        if (!(longer <= 1.25 * exact)) return false;
+    }
+    return true;
+}
+
+// Steps that contract to the very end of an interval and grow steeply past it (the published Polar Express coefficients
+// end so) are taken of X / kSafety, all but the last: past the end then lies 2.9e-3 of the eigenvalue, more than kSlack.
+constexpr double kSafety = 1.0 + 3.0 / (1 << 11);
 
 }  // namespace
 
@@ -46,14 +76,25 @@ double program_time(const Times& t, int32_t n_steps, bool pairs) {
 zero_status make_program(const double* coefficients, int32_t n_steps, bool pairs, bool low, std::vector<Product>* out,
                          const char* who) {
     out->clear();
+    double taken[3 * kMaxSteps];
+    std::copy(coefficients, coefficients + 3 * n_steps, taken);
+    if (!steady(coefficients, n_steps, kSlack)) {
+        for (int32_t i = 0; i + 1 < n_steps; ++i) {
+            const double s2 = kSafety * kSafety;
+            taken[3 * i] /= kSafety;
+            taken[3 * i + 1] /= kSafety * s2;
+            taken[3 * i + 2] /= kSafety * s2 * s2;
+        }
+        if (!steady(taken, n_steps, kSlack)) std::copy(coefficients, coefficients + 3 * n_steps, taken);
+    }
     int eX = 14;             // the first X: kappa * 2^-14 times what is held
-    double top = 1.0;        // bound of the eigenvalues of A, X X^T of a matrix of norm 1
+    double top = 1.0 + kSlack;       // bound of the eigenvalues of A, X X^T of a matrix of norm 1, with what roundings add
     int32_t from = kT0, to = kT1;
     for (int32_t at = 0; at < n_steps;) {
         const bool first = at == 0;
+        const double a = taken[3 * at], b = taken[3 * at + 1], c = taken[3 * at + 2];
         // (in the pair's A' roundings grow by the square of its first step's a)
-        const bool pair = at + 1 < n_steps && (pairs || first) && std::fabs(coefficients[3 * at]) <= 4.0;
-        const double a = coefficients[3 * at], b = coefficients[3 * at + 1], c = coefficients[3 * at + 2];
+        const bool pair = at + 1 < n_steps && (pairs || first) && std::fabs(a) <= 4.0;
         auto poly = [&](double x) { return a + x * (b + x * c); };
         auto product = [&](Kind kind, int32_t lhs, int32_t rhs, int32_t o, double alpha) {
             Product p{};
@@ -69,75 +110,82 @@ zero_status make_program(const double* coefficients, int32_t n_steps, bool pairs
             p->beta = static_cast<float>(b0 * pow2(eC - eA));
             p->diag = static_cast<float>(a0 * pow2(eC));
         };
-        const int eA = exponent_for(top), eC = exponent_for(largest(top, poly));
+        const int eA = exponent_for_largest(top), eC = exponent_for_largest(largest(top, poly));
         product(Kind::kGram, kX, kX, kS0, pow2(eA - 2 * eX))->kappa_power = first ? 2 : 0;
         polynomial(a, b, c, kS0, kS1, eA, eC);
         int32_t q = kS1;
         int eQ = eC;
-        double next = largest(top, [&](double x) { return x * poly(x) * poly(x); });
+        double next = step_top(taken + 3 * at, top);
         if (pair) {
-            const double a1 = coefficients[3 * at + 3], b1 = coefficients[3 * at + 4], c1 = coefficients[3 * at + 5];
+            const double a1 = taken[3 * at + 3], b1 = taken[3 * at + 4], c1 = taken[3 * at + 5];
+            const double between = next * (1.0 + kSlack);
             auto poly1 = [&](double x) { return a1 + x * (b1 + x * c1); };
             auto after = [&](double x) { return x * poly(x) * poly(x); };       // the eigenvalue after the first step
-            const int eT = exponent_for(largest(top, [&](double x) { return x * poly(x); }));
-            const int eA1 = exponent_for(next), eC1 = exponent_for(largest(next, poly1));
-            eQ = exponent_for(largest(top, [&](double x) { return poly(x) * poly1(after(x)); }));
+            const int eT = exponent_for_largest(largest(top, [&](double x) { return x * poly(x); }));
+            const int eA1 = exponent_for_largest(between), eC1 = exponent_for_largest(largest(between, poly1));
+            eQ = exponent_for_largest(largest(top, [&](double x) { return poly(x) * poly1(after(x)); }));
             product(Kind::kSquare, kS1, kS0, kS2, pow2(eT - eC - eA));
             product(Kind::kSquare, kS2, kS1, kS0, pow2(eA1 - eT - eC));
             polynomial(a1, b1, c1, kS0, kS2, eA1, eC1);
             product(Kind::kSquare, kS2, kS1, kS0, pow2(eQ - eC1 - eC));
             q = kS0;
-            next = largest(top, [&](double x) {
-                const double y = after(x), p1 = poly1(y);
-                return y * p1 * p1;
-            });
+            next = step_top(taken + 3 * at + 3, between);
         }
         if (!(next <= std::ldexp(1.0, 40)))
-            return fail(ZERO_EINVAL, std::string(who) + ": these coefficients let singular values grow past 2^20");
+            return fail(ZERO_EINVAL, std::string(who) + ": these coefficients let singular values, with what roundings add "
+                                                        "to them, grow past 2^20");
         at += pair ? 2 : 1;
         const bool last = at == n_steps;
-        const int eN = exponent_for(std::sqrt(next));
+        const int eN = exponent_for_largest(std::sqrt(next));
         Product* p = product(last ? Kind::kFinal : Kind::kApply, q, from, last ? kNone : kX,
                              pow2((last ? 0 : eN) - eQ - eX));
         p->out_t = last ? kNone : to;
         // Q times what rounding the first X left: in directions that X hardly has Q is its value at 0, a or a a', and only
         // there is the rounding magnified (simulated on twelve spectra: as exact as the product, to two digits).
         if (first && low)
-            p->low = static_cast<float>(pow2((last ? 0 : eN) - eX) * a * (pair ? coefficients[3 * at - 3] : 1.0));
+            p->low = static_cast<float>(pow2((last ? 0 : eN) - eX) * a * (pair ? taken[3 * at - 3] : 1.0));
         p->kappa_power = first ? 1 : 0;
         std::swap(from, to);
         eX = eN;
-        top = next;
+        top = next * (1.0 + kSlack);
     }
     return ZERO_OK;
 }
 
 bool make_short_program(const double* coefficients, int32_t n_steps, ShortProgram* out) {
     *out = ShortProgram{};
+    if (!steady(coefficients, n_steps, kShortSlack)) return false;
     out->n_steps = n_steps;
-    double x[kSamples + 1], q[kSamples + 1];         // eigenvalues of A, and of Q
-    double top = 1.0, growth = 1.0;
-    for (int i = 0; i <= kSamples; ++i) x[i] = static_cast<double>(i) / kSamples, q[i] = 1.0;
-    int eA = exponent_for(top), eQ = 0;
+    // Eigenvalues of A and of Q, carried through the steps: evenly spaced ones, and as many from 1e-12 up at equal ratios,
+    // which cover every interval that small ones grow into.
+    constexpr int kCarried = 2 * kSamples + 2;
+    double x[kCarried], q[kCarried];
+    for (int i = 0; i <= kSamples; ++i) {
+        x[2 * i] = static_cast<double>(i) / kSamples;
+        x[2 * i + 1] = std::pow(10.0, 12.0 * i / kSamples - 12.0);
+        q[2 * i] = q[2 * i + 1] = 1.0;
+    }
+    double top = 1.0 + kShortSlack, growth = 1.0;
+    int eA = exponent_for_largest(top), eQ = 0;
     out->first = std::ldexp(1.0, eA);
     for (int32_t at = 0; at < n_steps; ++at) {
-        const double a = coefficients[3 * at], b = coefficients[3 * at + 1], c = coefficients[3 * at + 2];
-        double most_c = 0.0, most_t = 0.0, most_a = 0.0, most_q = 0.0;
-        for (int i = 0; i <= kSamples; ++i) {
-            const double p = a + x[i] * (b + x[i] * c);
-            most_c = std::max(most_c, std::fabs(p));
-            most_t = std::max(most_t, std::fabs(x[i] * p));
+        const double* const step = coefficients + 3 * at;
+        const double a = step[0], b = step[1], c = step[2];
+        auto poly = [&](double y) { return a + y * (b + y * c); };
+        const double most_c = largest(top, poly), most_t = largest(top, [&](double y) { return y * poly(y); }),
+                     most_a = step_top(step, top);
+        double most_q = 0.0;
+        for (int i = 0; i < kCarried; ++i) {
+            const double p = poly(x[i]);
             x[i] *= p * p;
             q[i] *= p;
-            most_a = std::max(most_a, x[i]);
             most_q = std::max(most_q, std::fabs(q[i]));
         }
         // small negative eigenvalues, which roundings make, grow by a^2
         if (at + 1 < n_steps) growth *= std::max(1.0, std::max(a * a, most_c * most_c));
         if (!(growth <= 65536.0) || !(most_a <= 1024.0) || !(most_q <= 65536.0)) return false;
-        const double margin = std::pow(1.02, at + 1);
-        const int eC = exponent_for(most_c * margin), eT = exponent_for(most_t * margin),
-                  eN = exponent_for(most_a * margin), eP = at == 0 ? eC : exponent_for(most_q * margin);
+        const int eC = exponent_for_largest(most_c), eT = exponent_for_largest(most_t), eN = exponent_for_largest(most_a),
+                  eP = at == 0 ? eC : exponent_for_largest(most_q);
         ShortStep& s = out->step[at];
         s.a = static_cast<float>(a * pow2(eC));
         s.b = static_cast<float>(b * pow2(eC - eA));
@@ -147,6 +195,7 @@ bool make_short_program(const double* coefficients, int32_t n_steps, ShortProgra
         s.q = pow2(eP - eC - eQ);
         eA = eN;
         eQ = eP;
+        top = most_a * (1.0 + kShortSlack);
     }
     out->last = pow2(-eQ);
     return true;
