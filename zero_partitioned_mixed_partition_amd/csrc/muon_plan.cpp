@@ -16,7 +16,7 @@ int exponent_for(double bound) { return 14 - static_cast<int>(std::ceil(std::log
 
 float pow2(int e) { return static_cast<float>(std::ldexp(1.0, e)); }
 
-constexpr int kSamples = 2048;
+constexpr int kSamples = 1024;
 
 // The largest |f(x)| over [0, top], by samples.
 template <typename F>
@@ -29,13 +29,39 @@ double largest(double top, F f) {
 // For an exponent: a margin for what lies between the samples.
 int exponent_for_largest(double most) { return exponent_for(1.02 * most); }
 
-// The largest eigenvalue that a step leaves of those in [0, top].
-double step_top(const double* step, double top) {
-    return largest(top, [&](double x) {
-        const double p = step[0] + x * (step[1] + x * step[2]);
-        return x * p * p;
-    });
-}
+// A step's factor a + b x + c x^2 and what is made of it, with their largest absolute values over [0, top]: at its end or where
+// the derivative is 0.
+struct Step {
+    double a, b, c;
+
+    double at(double x) const { return a + x * (b + x * c); }
+    double left(double x) const { return x * at(x) * at(x); }            // the eigenvalue that it leaves of x
+    double largest_factor(double top) const {
+        const double x = c != 0.0 ? -b / (2.0 * c) : 0.0;
+        return std::max({std::fabs(a), std::fabs(at(top)), x > 0.0 && x < top ? std::fabs(at(x)) : 0.0});
+    }
+    double largest_times_x(double top) const {
+        return over(top, 2.0 * b, 3.0 * c, [&](double x) { return std::fabs(x * at(x)); });
+    }
+    double largest_left(double top) const {
+        return over(top, 3.0 * b, 5.0 * c, [&](double x) { return left(x); });
+    }
+
+private:
+    // The largest f at top and at the roots of a + p x + q x^2 in (0, top).
+    template <typename F>
+    double over(double top, double p, double q, F f) const {
+        double most = f(top);
+        const double under = p * p - 4.0 * a * q;
+        if (under < 0.0) return most;
+        const double h = -0.5 * (p + std::copysign(std::sqrt(under), p));
+        for (const double x : {h != 0.0 ? a / h : 0.0, q != 0.0 ? h / q : 0.0})
+            if (x > 0.0 && x < top) most = std::max(most, f(x));
+        return most;
+    }
+};
+
+Step step_at(const double* coefficients, int32_t i) { return {coefficients[3 * i], coefficients[3 * i + 1], coefficients[3 * i + 2]}; }
 
 // How far the roundings of a step can carry an eigenvalue of X X^T past the end of its interval, relative to it. An fp16
 // value is off by at most 2^-11 of itself, and X counts twice, A once, C twice; in two fp16 parts 2^-22 of it.
@@ -45,8 +71,8 @@ constexpr double kSlack = 5.0 / (1 << 11), kShortSlack = 5.0 / (1 << 22);
 bool steady(const double* coefficients, int32_t n_steps, double slack) {
     double exact = 1.0, longer = 1.0;
     for (int32_t i = 0; i < n_steps; ++i) {
-        exact = step_top(coefficients + 3 * i, exact);
-        longer = step_top(coefficients + 3 * i, longer * (1.0 + slack));
+        exact = step_at(coefficients, i).largest_left(exact);
+        longer = step_at(coefficients, i).largest_left(longer * (1.0 + slack));
         if (!(longer <= 1.25 * exact)) return false;
     }
     return true;
@@ -92,10 +118,9 @@ zero_status make_program(const double* coefficients, int32_t n_steps, bool pairs
     int32_t from = kT0, to = kT1;
     for (int32_t at = 0; at < n_steps;) {
         const bool first = at == 0;
-        const double a = taken[3 * at], b = taken[3 * at + 1], c = taken[3 * at + 2];
+        const Step s0 = step_at(taken, at);
         // (in the pair's A' roundings grow by the square of its first step's a)
-        const bool pair = at + 1 < n_steps && (pairs || first) && std::fabs(a) <= 4.0;
-        auto poly = [&](double x) { return a + x * (b + x * c); };
+        const bool pair = at + 1 < n_steps && (pairs || first) && std::fabs(s0.a) <= 4.0;
         auto product = [&](Kind kind, int32_t lhs, int32_t rhs, int32_t o, double alpha) {
             Product p{};
             p.kind = kind;
@@ -104,32 +129,30 @@ zero_status make_program(const double* coefficients, int32_t n_steps, bool pairs
             out->push_back(p);
             return &out->back();
         };
-        auto polynomial = [&](double a0, double b0, double c0, int32_t from_s, int32_t to_s, int eA, int eC) {
-            Product* p = product(Kind::kSquare, from_s, from_s, to_s, c0 * pow2(eC - 2 * eA));
+        auto polynomial = [&](const Step& s, int32_t from_s, int32_t to_s, int eA, int eC) {
+            Product* p = product(Kind::kSquare, from_s, from_s, to_s, s.c * pow2(eC - 2 * eA));
             p->add = from_s;
-            p->beta = static_cast<float>(b0 * pow2(eC - eA));
-            p->diag = static_cast<float>(a0 * pow2(eC));
+            p->beta = static_cast<float>(s.b * pow2(eC - eA));
+            p->diag = static_cast<float>(s.a * pow2(eC));
         };
-        const int eA = exponent_for_largest(top), eC = exponent_for_largest(largest(top, poly));
+        const int eA = exponent_for_largest(top), eC = exponent_for_largest(s0.largest_factor(top));
         product(Kind::kGram, kX, kX, kS0, pow2(eA - 2 * eX))->kappa_power = first ? 2 : 0;
-        polynomial(a, b, c, kS0, kS1, eA, eC);
+        polynomial(s0, kS0, kS1, eA, eC);
         int32_t q = kS1;
         int eQ = eC;
-        double next = step_top(taken + 3 * at, top);
+        double next = s0.largest_left(top);
         if (pair) {
-            const double a1 = taken[3 * at + 3], b1 = taken[3 * at + 4], c1 = taken[3 * at + 5];
+            const Step s1 = step_at(taken, at + 1);
             const double between = next * (1.0 + kSlack);
-            auto poly1 = [&](double x) { return a1 + x * (b1 + x * c1); };
-            auto after = [&](double x) { return x * poly(x) * poly(x); };       // the eigenvalue after the first step
-            const int eT = exponent_for_largest(largest(top, [&](double x) { return x * poly(x); }));
-            const int eA1 = exponent_for_largest(between), eC1 = exponent_for_largest(largest(between, poly1));
-            eQ = exponent_for_largest(largest(top, [&](double x) { return poly(x) * poly1(after(x)); }));
+            const int eT = exponent_for_largest(s0.largest_times_x(top));
+            const int eA1 = exponent_for_largest(between), eC1 = exponent_for_largest(s1.largest_factor(between));
+            eQ = exponent_for_largest(largest(top, [&](double x) { return s0.at(x) * s1.at(s0.left(x)); }));
             product(Kind::kSquare, kS1, kS0, kS2, pow2(eT - eC - eA));
             product(Kind::kSquare, kS2, kS1, kS0, pow2(eA1 - eT - eC));
-            polynomial(a1, b1, c1, kS0, kS2, eA1, eC1);
+            polynomial(s1, kS0, kS2, eA1, eC1);
             product(Kind::kSquare, kS2, kS1, kS0, pow2(eQ - eC1 - eC));
             q = kS0;
-            next = step_top(taken + 3 * at + 3, between);
+            next = s1.largest_left(between);
         }
         if (!(next <= std::ldexp(1.0, 40)))
             return fail(ZERO_EINVAL, std::string(who) + ": these coefficients let singular values, with what roundings add "
@@ -143,7 +166,7 @@ zero_status make_program(const double* coefficients, int32_t n_steps, bool pairs
         // Q times what rounding the first X left: in directions that X hardly has Q is its value at 0, a or a a', and only
         // there is the rounding magnified (simulated on twelve spectra: as exact as the product, to two digits).
         if (first && low)
-            p->low = static_cast<float>(pow2((last ? 0 : eN) - eX) * a * (pair ? taken[3 * at - 3] : 1.0));
+            p->low = static_cast<float>(pow2((last ? 0 : eN) - eX) * s0.a * (pair ? taken[3 * at - 3] : 1.0));
         p->kappa_power = first ? 1 : 0;
         std::swap(from, to);
         eX = eN;
@@ -158,38 +181,39 @@ bool make_short_program(const double* coefficients, int32_t n_steps, ShortProgra
     out->n_steps = n_steps;
     // Eigenvalues of A and of Q, carried through the steps: evenly spaced ones, and as many from 1e-12 up at equal ratios,
     // which cover every interval that small ones grow into.
-    constexpr int kCarried = 2 * kSamples + 2;
+    constexpr int kCarried = kSamples, kHalf = kCarried / 2, kLanes = 8;
     double x[kCarried], q[kCarried];
-    for (int i = 0; i <= kSamples; ++i) {
-        x[2 * i] = static_cast<double>(i) / kSamples;
-        x[2 * i + 1] = std::pow(10.0, 12.0 * i / kSamples - 12.0);
-        q[2 * i] = q[2 * i + 1] = 1.0;
+    double small = 1.0;
+    const double ratio = std::pow(10.0, -12.0 / kHalf);
+    for (int i = 0; i < kHalf; ++i, small *= ratio) {
+        x[i] = static_cast<double>(i) / kHalf;
+        x[kHalf + i] = small;
+        q[i] = q[kHalf + i] = 1.0;
     }
     double top = 1.0 + kShortSlack, growth = 1.0;
     int eA = exponent_for_largest(top), eQ = 0;
     out->first = std::ldexp(1.0, eA);
     for (int32_t at = 0; at < n_steps; ++at) {
-        const double* const step = coefficients + 3 * at;
-        const double a = step[0], b = step[1], c = step[2];
-        auto poly = [&](double y) { return a + y * (b + y * c); };
-        const double most_c = largest(top, poly), most_t = largest(top, [&](double y) { return y * poly(y); }),
-                     most_a = step_top(step, top);
-        double most_q = 0.0;
-        for (int i = 0; i < kCarried; ++i) {
-            const double p = poly(x[i]);
-            x[i] *= p * p;
-            q[i] *= p;
-            most_q = std::max(most_q, std::fabs(q[i]));
-        }
+        const Step step = step_at(coefficients, at);
+        const double most_c = step.largest_factor(top), most_t = step.largest_times_x(top), most_a = step.largest_left(top);
+        double lanes[kLanes] = {};
+        for (int i = 0; i < kCarried; i += kLanes)
+            for (int k = 0; k < kLanes; ++k) {
+                const double p = step.at(x[i + k]);
+                x[i + k] *= p * p;
+                q[i + k] *= p;
+                lanes[k] = std::max(lanes[k], std::fabs(q[i + k]));
+            }
+        const double most_q = *std::max_element(lanes, lanes + kLanes);
         // small negative eigenvalues, which roundings make, grow by a^2
-        if (at + 1 < n_steps) growth *= std::max(1.0, std::max(a * a, most_c * most_c));
+        if (at + 1 < n_steps) growth *= std::max(1.0, most_c * most_c);
         if (!(growth <= 65536.0) || !(most_a <= 1024.0) || !(most_q <= 65536.0)) return false;
         const int eC = exponent_for_largest(most_c), eT = exponent_for_largest(most_t), eN = exponent_for_largest(most_a),
                   eP = at == 0 ? eC : exponent_for_largest(most_q);
         ShortStep& s = out->step[at];
-        s.a = static_cast<float>(a * pow2(eC));
-        s.b = static_cast<float>(b * pow2(eC - eA));
-        s.c = static_cast<float>(c * pow2(eC - 2 * eA));
+        s.a = static_cast<float>(step.a * pow2(eC));
+        s.b = static_cast<float>(step.b * pow2(eC - eA));
+        s.c = static_cast<float>(step.c * pow2(eC - 2 * eA));
         s.t = pow2(eT - eC - eA);
         s.next = pow2(eN - eT - eC);
         s.q = pow2(eP - eC - eQ);
