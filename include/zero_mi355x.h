@@ -659,17 +659,21 @@ zero_status zero_state8_dequantize(const uint8_t* codes, const uint8_t* scales, 
  * 1.2. A zero matrix gives zeros (with eps = 0 too); one that holds an infinity
  * or NaN gives NaN throughout, and no other matrix of the call is touched by it.
  * Precision: products of fp16 values (scaled by powers of two) summed in fp32,
- * with what rounding the first X of fp32 inputs left carried past the first of
- * them; about 1.5e-3 of the result's Frobenius norm off the exact steps, less than
- * rounding it to bf16 (1.7e-3), and up to 8e-3 where nearly all of the norm lies in
- * one direction or half of the singular values lie far below the rest. Where no matrix of a call has a short side above 128 and
- * the coefficients are like these all values are held in two fp16 parts, and it
- * is about 3e-5. Singular values below
- * about 1e-5 of the norm, and directions
- * that G does not have, come out as noise of up to 0.02; elements below 3e-10
- * (a norm far below eps) as zeros or noise of that size. Two steps are taken as
- * one on the smaller side where that saves time and the first's |a| is at most 4;
- * this and the products' tiles follow the sizes and number of a call's matrices.
+ * with what rounding each X left carried along; after five usual steps about
+ * 1.5e-3 of the result's Frobenius norm off the exact ones, less than rounding it
+ * to bf16 (1.7e-3), and up to 6e-3 where few directions hold nearly all of the
+ * norm or half of the singular values lie far below the rest. Singular values
+ * below about 1e-5 of the norm, and directions that G does not have, come out as
+ * noise of up to 0.02; elements below 3e-10 (a norm far below eps) as zeros or
+ * noise of that size. Every step multiplies what lies in such directions by its a:
+ * after nine usual ones the noise is up to 0.2, and a matrix whose singular
+ * values lie above 1e-3 of the largest up to 4e-2 off. Where no matrix of a call
+ * has a short side above 128 and the product of the squares of all a but the last
+ * is below 65,536, all values are held in two fp16 parts, and five usual steps are
+ * about 3e-5 off.
+ * Two steps are taken as one on the smaller side where that saves time and the
+ * first's |a| is at most 4; this and the products' tiles follow the sizes and
+ * number of a call's matrices.
  * The same call gives the same bits: no atomics.
  * Steps that contract to the very end of the interval that the one before leaves
  * and grow steeply past it (the published Polar Express coefficients, undivided)

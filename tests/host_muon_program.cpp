@@ -20,8 +20,8 @@ int main(int argc, char** argv) {
         std::printf("%d %s\n", static_cast<int>(st), zero_last_error());
         if (st != ZERO_OK) return 0;
         for (const Product& p : program)
-            std::printf("%d %d %d %d %d %d %.9g %.9g %.9g %.9g\n", static_cast<int>(p.kind), p.lhs, p.rhs, p.add, p.out,
-                        p.kappa_power, p.alpha, p.beta, p.diag, p.low);
+            std::printf("%d %d %d %d %d %d %d %d %d %.9g %.9g %.9g\n", static_cast<int>(p.kind), p.lhs, p.rhs, p.add, p.out,
+                        p.kappa_power, p.low_in, p.low_out, p.full, p.alpha, p.beta, p.diag);
         return 0;
     }
     ShortProgram program;

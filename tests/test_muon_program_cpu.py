@@ -48,10 +48,10 @@ def run(exe, *args, steps):
 
 
 def tiled(exe, steps, pairs, low):
-    """Status, message, and the products as (kind, lhs, rhs, add, out, kappa power, alpha, beta, diag, low)."""
+    """Status, message, and the products as (kind, lhs, rhs, add, out, kappa power, low in, low out, full, alpha, beta, diag)."""
     head, *rows = run(exe, "tiled", str(int(pairs)), str(int(low)), steps=steps)
     status, _, message = head.partition(" ")
-    return int(status), message, [[int(x) for x in r.split()[:6]] + [float(x) for x in r.split()[6:]] for r in rows]
+    return int(status), message, [[int(x) for x in r.split()[:9]] + [float(x) for x in r.split()[9:]] for r in rows]
 
 
 GRAM, SQUARE, APPLY, FINAL = range(4)
@@ -74,7 +74,7 @@ def emulate(products, g, eps=1e-7):
     x = held(u)
     rest = held(u - x)
     s = {}
-    for kind, lhs, rhs, add, out, power, alpha, beta, diag, low in products:
+    for kind, lhs, rhs, add, out, power, low_in, low_out, full, alpha, beta, diag in products:
         alpha *= kappa ** power
         if kind == GRAM:
             s[out] = held(alpha * (x @ x.T))
@@ -82,15 +82,20 @@ def emulate(products, g, eps=1e-7):
             v = alpha * (s[lhs] @ s[rhs].T) + diag * np.eye(len(x))
             if beta:
                 v += beta * s[add]
-            v = np.tril(v) + np.tril(v, -1).T                # computed on and below the diagonal, mirrored
+            if not full:                                     # computed on the tiles at and below the diagonal, mirrored
+                tile = np.arange(len(v)) // 64
+                v = np.where(tile[:, None] >= tile, v, v.T)
             s[out] = held(v)
         else:
-            v = alpha * (s[lhs] @ x)
-            if low:
-                v += low * kappa * rest
+            v = s[lhs] @ x
+            if low_in:
+                v += np.diag(s[lhs])[:, None] * rest
+            v *= alpha
             if kind == FINAL:
+                assert not low_out
                 return v
             x = held(v)
+            rest = held(v - x) if low_out else None
 
 
 def matrix(kind, m=40, n=70):
@@ -140,6 +145,28 @@ def test_steps_that_end_at_the_edge_of_their_interval(exe, name, pairs):
 def test_steps_that_grow_are_refused(exe, steps):
     status, message, _ = tiled(exe, steps, False, True)
     assert status != 0 and "grow past 2^20" in message
+
+
+SPECTRA = {"rank 1": lambda k, m: (k < 1) * 1.0, "rank 3": lambda k, m: (k < 3) * 1.0, "flat": lambda k, m: np.ones(m),
+           "32 over 1e-3": lambda k, m: np.where(k < 32, 1.0, 1e-3), "8 over 1e-4": lambda k, m: np.where(k < 8, 1.0, 1e-4),
+           "half over 1e-3": lambda k, m: np.where(k < m // 2, 1.0, 1e-3), "1/k^2": lambda k, m: (1.0 + k) ** -2.0,
+           "1e-3 by ratios": lambda k, m: 10.0 ** (-3 * k / m), "1e-6 by ratios": lambda k, m: 10.0 ** (-6 * k / m)}
+
+
+@pytest.mark.parametrize("fp32", [True, False])
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("kind", list(SPECTRA))
+def test_what_rounding_x_leaves_is_carried_along(exe, kind, pairs, fp32):
+    """Hard singular values in random directions: FIVE of tests/test_gpu_muon_spectra.py (derived there), without bf16's
+    rounding."""
+    m, n = 150, 260
+    rng = np.random.default_rng(1)
+    u, v = np.linalg.qr(rng.normal(size=(m, m)))[0], np.linalg.qr(rng.normal(size=(n, m)))[0]
+    g = (u * SPECTRA[kind](np.arange(m), m)) @ v.T
+    g = (g.astype(np.float32) if fp32 else oracle.bf16_to_f32(oracle.f32_to_bf16(g.astype(np.float32)))).astype(np.float64)
+    _, _, products = tiled(exe, [USUAL] * 5, pairs, fp32)
+    want = oracle.muon.orthogonalize(g)
+    assert np.linalg.norm(emulate(products, g) - want) <= 6.6e-3 * np.linalg.norm(want)
 
 
 def short(exe, steps):

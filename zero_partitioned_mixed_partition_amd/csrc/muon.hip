@@ -398,11 +398,10 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
 
     // A lane holds one column of each MFMA tile, four consecutive rows at a time; LDS turns them into whole rows, in
     // either order of storage, so that memory is read and written 16 bytes a lane and 2 T bytes a row.
-    float alpha = p.alpha, low = p.low;
+    float alpha = p.alpha;
     if (p.kappa_power > 0) {
         const float kappa = m.kappa[d.id];
         alpha = p.kappa_power == 2 ? alpha * (kappa * kappa) : alpha * kappa;
-        low *= kappa;
     }
     const int down = wr + lane / kSide * 4, over = wc + lane % kSide;  // the lane's first row, and its column
     const int quad = lane % 4;
@@ -431,8 +430,8 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
             }
         }
     };
-    // And `from` there.
-    auto read_rows = [&](const f16* from, int64_t ld) {
+    // And `from` there, each piece as change(piece, row, number) makes it.
+    auto read_rows = [&](const f16* from, int64_t ld, auto change) {
         constexpr int kAtOnce = kOwn < 8 ? kOwn : kOwn % 8 == 0 ? 8 : 6;
 #pragma unroll 1
         for (int k0 = 0; k0 < kOwn; k0 += kAtOnce) {
@@ -442,7 +441,8 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
                 x[k] = *reinterpret_cast<const f16x8*>(from + row_of(k0 + k) * ld + piece_of(k0 + k) * 8);
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k)
-                *reinterpret_cast<f16x8*>(lds + place(row_of(k0 + k), piece_of(k0 + k) * 2)) = x[k];
+                *reinterpret_cast<f16x8*>(lds + place(row_of(k0 + k), piece_of(k0 + k) * 2)) =
+                    change(x[k], row_of(k0 + k), piece_of(k0 + k));
         }
     };
     // Calls f(i, j) for the lane's groups of four rows.
@@ -453,19 +453,30 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
             for (int j = 0; j < NI; ++j) f(i, j);
     };
     f16x4 values[MI][NI];
-    __syncthreads();
-    // The first apply's low part of X, times Q's value at the eigenvalue 0.
+    // Q's diagonal times what rounding X left, both as fp16 times a power of two: their product needs no more bits. (In rows
+    // and columns that a tile shares with the one before, that one may have written its own by now: what this one makes of
+    // them is not stored.)
+    f16* const q = lds + kStages * 2 * kOperand;         // 2^-14 of it
     if constexpr (!kSquareOut)
-        if (low != 0.0f) {
+        if (p.low_in) {
+            const int64_t step = stride(d.M) + 1;
+            const f16* const diagonal = buffer(m, d, p.lhs) + (tall ? c0 : r0) * step;
+            for (int k = threadIdx.x; k < T; k += 64 * kWaves) q[k] = diagonal[k * step] * static_cast<f16>(0x1p-14f);
+        }
+    __syncthreads();
+    if constexpr (!kSquareOut)
+        if (p.low_in) {
             const int64_t low_ld = stride(height);
-            read_rows(buffer(m, d, zero::muon::kLow) + c0 * low_ld + r0, low_ld);
+            read_rows(buffer(m, d, zero::muon::kLow) + c0 * low_ld + r0, low_ld, [&](f16x8 x, int r, int piece) {
+                if (!tall) return x * *reinterpret_cast<const f16x8*>(q + piece * 8);
+                return x * q[r];
+            });
             __syncthreads();
             each([&](int i, int j) {
                 const f16x4 x = *reinterpret_cast<const f16x4*>(lds + place(over + j * kSide, (down + i * kSide) / 4));
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[i][j][k] = alpha * acc[i][j][k] + low * static_cast<float>(x[k]);
+                for (int k = 0; k < 4; ++k) acc[i][j][k] += 0x1p14f * static_cast<float>(x[k]);
             });
-            alpha = 1.0f;
             __syncthreads();
         }
     if constexpr (kSquareOut) {
@@ -473,7 +484,7 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
         const int64_t ldm = stride(d.M);
         const int64_t direct = r0 * ldm + c0, mirrored = c0 * ldm + r0;
         if (p.add != zero::muon::kNone) {                // symmetric: its mirrored tile's rows are this one's columns
-            read_rows(buffer(m, d, p.add) + mirrored, ldm);
+            read_rows(buffer(m, d, p.add) + mirrored, ldm, [](f16x8 x, int, int) { return x; });
             __syncthreads();
         }
         const int diagonal = c0 - r0 + over - down;               // row minus `down` of the lane's first column
@@ -507,9 +518,20 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
         const int64_t down_ld = stride(tall ? d.N : d.M), along_ld = stride(tall ? d.M : d.N);
         f16* const along = buffer(m, d, tall ? p.out_t : p.out);
         f16* const across = buffer(m, d, tall ? p.out : p.out_t);
+        // What rounding leaves first, then the rounded values, formed again: both do not fit the registers.
+        if (p.low_out) {
+            each([&](int i, int j) {
+                f16x4 x, rest;
+                split4(alpha * acc[i][j][0], alpha * acc[i][j][1], alpha * acc[i][j][2], alpha * acc[i][j][3], &x, &rest);
+                *reinterpret_cast<f16x4*>(lds + place(over + j * kSide, (down + i * kSide) / 4)) = rest;
+            });
+            __syncthreads();
+            write_rows(buffer(m, d, zero::muon::kLow) + c0 * down_ld + r0, down_ld, skip_cols, skip_rows);
+            __syncthreads();
+        }
         each([&](int i, int j) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) values[i][j][k] = static_cast<f16>(alpha * acc[i][j][k]);
+            f16x4 rest;
+            split4(alpha * acc[i][j][0], alpha * acc[i][j][1], alpha * acc[i][j][2], alpha * acc[i][j][3], &values[i][j], &rest);
             *reinterpret_cast<f16x4*>(lds + place(over + j * kSide, (down + i * kSide) / 4)) = values[i][j];
         });
         __syncthreads();
@@ -568,11 +590,16 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
 template <int T, int kStages, bool kSquareOut, int kEnd>
 __device__ __forceinline__ void product(const Matrices& m, const Product& p, const Update& u, uint32_t run, uint32_t whole) {
     constexpr int kValues = kStages * 2 * T * kDepth;    // values of all stages
-    __shared__ __align__(16) f16 lds[kValues];
+    // (With an apply's diagonal of Q behind them: an array of its own makes the compiler wait for all loads on their way to
+    // LDS before it reads the fragments, 2.9 ms more for two applies of 8192 x 8192 x 8192.)
+    __shared__ __align__(16) f16 lds[kValues + (kSquareOut ? 0 : T)];
     static_assert(kValues >= T * T, "the tile fits where the stages were");
     if (kEnd == 2 && skipped(u.clip)) return;
     uint32_t t = xcd_tile(run), quarter = 0;
-    const bool cut = has_quarters<T, kSquareOut> && t >= whole;
+    const bool full = kSquareOut && p.full;              // two workgroups for a tile and the one mirrored to it
+    const bool above = full && t % 2 != 0;
+    if (full) t /= 2;
+    const bool cut = has_quarters<T, kSquareOut> && !full && t >= whole;
     if (cut) {
         quarter = (t - whole) % 4;
         t = whole + (t - whole) / 4;
@@ -587,13 +614,19 @@ __device__ __forceinline__ void product(const Matrices& m, const Product& p, con
         triangle_tile(t, (height + T - 1) / T, &bi, &bj);
     else
         rect_tile(t, (height + T - 1) / T, (width + T - 1) / T, &bi, &bj);
+    if (above) {
+        if (bi == bj) return;
+        const int32_t swapped = bi;
+        bi = bj;
+        bj = swapped;
+    }
     // The last tiles end with the matrix; the rows and columns that they share with the tiles before are those tiles'.
     Place at;
     at.r0 = min(bi * T, height - T);
     at.c0 = min(bj * T, width - T);
     at.skip_rows = bi * T - at.r0;
     at.skip_cols = bj * T - at.c0;
-    at.mirror = bi != bj;
+    at.mirror = !full && bi != bj;
     if constexpr (has_quarters<T, kSquareOut>) {
         if (cut) {
             constexpr int kHalf = T / 2;
@@ -635,8 +668,9 @@ template <int T, int kStages, bool kSquareOut, int kEnd>
 void launch_product(const Matrices& m, const Product& p, const Update& u, hipStream_t stream) {
     // Whole runs on every XCD; no run longer than an eighth of the tiles, so that a short grid reaches every XCD.
     const uint32_t tiles = m.total[kSquareOut ? zero::muon::kByPair : zero::muon::kByTile];
-    const uint32_t whole = has_quarters<T, kSquareOut> ? zero::muon::whole_tiles(tiles) : tiles;
-    const uint32_t total = whole + 4 * (tiles - whole);
+    const bool full = kSquareOut && p.full;
+    const uint32_t whole = has_quarters<T, kSquareOut> && !full ? zero::muon::whole_tiles(tiles) : tiles;
+    const uint32_t total = full ? 2 * tiles : whole + 4 * (tiles - whole);
     const uint32_t run = std::min(32u, (total + 7) / 8);
     const uint32_t blocks = (total + 8 * run - 1) / (8 * run) * (8 * run);
     hipLaunchKernelGGL((product_kernel<T, kStages, kSquareOut, kEnd>), dim3(blocks),
@@ -722,7 +756,7 @@ zero_status check_sides(int64_t rows, int64_t cols, const std::string& what) {
     return ZERO_OK;
 }
 
-constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / 512 - 256;         // fewer than 2^32 work-items a launch
+constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / 512 - 256;         // fewer than 2^32 work-items a launch of twice as many
 
 // A stack's sizes: its first matrix's descriptor (sides, chunks), the workgroups, the products' times and the workspace.
 // ZERO_ERANGE where one launch does not hold it.

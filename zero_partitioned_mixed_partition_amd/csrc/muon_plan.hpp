@@ -10,10 +10,13 @@
 // the diagonal and mirrored. Two steps can share one pass over X:
 //   A' = C A C (the next step's A),   X <- (C' C) X,
 // which takes three m^3 products more and one m^2 n product with its X X^T less.
+// C' C is symmetric but for the roundings of C, which a mirrored half would let
+// grow: where strong directions have converged (a pair after the first) all of
+// it is computed.
 //
 // In flops, r = n / m: a step alone 3 r + 1 times m^3 (A r, its square 1, the
-// apply 2 r), a pair 3 r + 5 against 6 r + 2. Five steps in pairs 9 r + 11,
-// with one pair only 12 r + 8, one by one 15 r + 5.
+// apply 2 r), the first pair 3 r + 5 against 6 r + 2, another 3 r + 6. Five steps
+// in pairs 9 r + 12, with one pair only 12 r + 8, one by one 15 r + 5.
 #pragma once
 
 #include <cstdint>
@@ -33,7 +36,7 @@ enum Buffer : int32_t {
     kS0 = 3,     // [M][M]: three square ones for A, C and their products
     kS1 = 4,
     kS2 = 5,
-    kLow = 6,    // what rounding the first X to fp16 left (fp32 inputs), the source transposed
+    kLow = 6,    // what rounding X to fp16 left, the source transposed
     kNone = 7,
 };
 
@@ -53,7 +56,9 @@ struct Product {
     int32_t lhs, rhs, add, out, out_t;
     int32_t kappa_power;
     float alpha, beta, diag;
-    float low;               // not 0: low * kappa * kLow is added
+    int32_t low_in;          // an apply: lhs's diagonal times what rounding X left is added to the product
+    int32_t low_out;         // and what rounding its own result leaves is kept
+    int32_t full;            // a square product: every tile is computed, none mirrored
 };
 
 // The most steps one call takes.
@@ -149,7 +154,7 @@ void shape(Desc* d, int64_t rows, int64_t cols, int64_t tile);
 // Workgroups of a matrix in each grid.
 int64_t grid_count(const Desc& d, int grid, int64_t square_tile, int64_t rect_tile);
 
-// Bytes of a matrix's arrays (kLow at the end, where the input is fp32).
+// Bytes of a matrix's arrays.
 int64_t area_bytes(const Desc& d);
 
 // ------------------------------------------------------------ matrices with a short side of at most 128
