@@ -46,7 +46,8 @@ class Hyper:
 
 @dataclass
 class MuonHyper:
-    """Muon's settings (zero_muon_step); the rate of a matrix is lr times muon_scale of its sides."""
+    """Muon's settings (zero_muon_step); the rate of a matrix is lr times muon_scale of its sides. lr is one number: a
+    schedule assigns it between steps."""
     lr: float = 1e-3
     momentum: float = 0.95
     nesterov: bool = True
@@ -55,8 +56,12 @@ class MuonHyper:
     coefficients: Sequence[Tuple[float, float, float]] = zb.MUON_COEFFICIENTS
 
     def as_kwargs(self) -> dict:
-        return dict(lr=self.lr, momentum=self.momentum, nesterov=self.nesterov, weight_decay=self.weight_decay,
-                    eps=self.eps, coefficients=self.coefficients)
+        try:
+            lr = float(self.lr)
+        except (TypeError, ValueError, RuntimeError):
+            raise ValueError("Muon's lr is one number: assign it between steps (only AdamW's may be a device schedule)") from None
+        return dict(lr=lr, momentum=self.momentum, nesterov=self.nesterov, weight_decay=self.weight_decay,
+                    eps=self.eps, coefficients=tuple(tuple(step) for step in self.coefficients))
 
 
 class RankStep:
@@ -108,7 +113,10 @@ class RankStep:
                  holds a part of one): where tensors are dealt to ranks whole, a
                  rank's plan is that of its own tensors with n_ranks=1. A matrix's
                  momentum is its exp_avg_tensors entry, its exp_avg_sq_tensors
-                 entry is empty. fp32 state only.
+                 entry is empty. fp32 state only. self.muon's values are read at
+                 every step, so a schedule assigns self.muon.lr. A captured step
+                 keeps those of its capture, with device_step too, which moves on
+                 AdamW's scalars alone: capture again for another rate.
     seed         with state_bits=8, the run's seed of the stochastic rounding (the
                  same on every rank: each rank draws the words of its own place in
                  the flat buffer).
@@ -142,6 +150,8 @@ class RankStep:
             raise ValueError("Muon updates whole matrices: per-parameter state only")
         if muon is not None and state_bits != 32:
             raise ValueError("Muon's momentum is fp32: state_bits is 32 with it")
+        if muon is not None:
+            muon.as_kwargs()                             # refuses what is no setting
         self.state_bits, self.seed = state_bits, seed
         self.plan, self.rank, self.hyper, self.max_norm = plan, rank, hyper, max_norm
         self.device = device
@@ -154,6 +164,7 @@ class RankStep:
         self.segments = plan.segments(rank) if per_param else []
         self.muon = muon
         self.muon_segments = _whole_matrices(plan, self.segments, muon_shapes or {})
+        self._muon_matrices: Optional[zb.MuonTable] = None
         moment = torch.float32 if state_bits == 32 else torch.uint8
         self.exp_avg_scale = self.exp_avg_sq_scale = None
         if per_param:
@@ -263,11 +274,12 @@ class RankStep:
         state holds one update fewer than t. (A caller that wants skipped
         iterations left uncounted reads the coefficient back, self.scale, and
         lowers self.t.)"""
+        settings = self.muon.as_kwargs() if self.muon_segments else {}
         self.t += 1
         clip = self.scale if self.max_norm > 0 else None
         if self.muon_segments:                           # independent of AdamW's part, and before its step is counted
             self._prepared("muon", stream, lambda st: self._muon_table().prepare_step(
-                clip_scale=clip, stream=st, **self.muon.as_kwargs()))()
+                clip_scale=clip, stream=st, **settings), tuple(settings.values()))()
         if self.state_bits == 8:
             self._adamw8(clip, stream)
             return
@@ -398,12 +410,17 @@ class RankStep:
                                    [self.grad[x] for x in sl], [own[x] for x in sl])
 
     def _muon_table(self) -> zb.MuonTable:
-        """The weight matrices' device table (the gradient and the parameter shard cut at the segments)."""
+        """The weight matrices' device table (the gradient and the parameter shard cut at the segments), made once: a
+        captured step goes on using it when other settings are prepared."""
+        if self._muon_matrices is not None:
+            return self._muon_matrices
         own = self.param_shards[self.rank]
         at = list(self.muon_segments)
         sl = [slice(self.segments[i][2], self.segments[i][2] + self.segments[i][3]) for i in at]
-        return zb.MuonTable([self.master_tensors[i] for i in at], [self.exp_avg_tensors[i] for i in at],
-                            [self.grad[x] for x in sl], [own[x] for x in sl], [self.muon_segments[i] for i in at])
+        self._muon_matrices = zb.MuonTable([self.master_tensors[i] for i in at], [self.exp_avg_tensors[i] for i in at],
+                                           [self.grad[x] for x in sl], [own[x] for x in sl],
+                                           [self.muon_segments[i] for i in at])
+        return self._muon_matrices
 
     def steps_applied(self) -> int:
         """Updates applied: the device count with device_step (a synchronous read),
