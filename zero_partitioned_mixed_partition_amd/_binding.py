@@ -1319,17 +1319,22 @@ def _stack_count(t, rows: int, cols: int) -> int:
     return n // (rows * cols)
 
 
+def _side_stream(stream, device):
+    """The stream of a handle where that is not the current one's, else None."""
+    import torch
+    if stream is None or int(stream) == torch.cuda.current_stream(device).cuda_stream:
+        return None
+    return torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
+
+
 def _own_workspace(nbytes: int, t, stream):
     """A workspace for one call on `stream` (a handle; None: the current stream), from torch's allocator."""
     import torch
     ws = torch.empty(nbytes, dtype=torch.uint8, device=t.device)
-    if stream is not None and nbytes:
-        current = torch.cuda.current_stream(t.device)
-        if int(stream) != current.cuda_stream:
-            side = (torch.cuda.ExternalStream(int(stream), device=t.device) if int(stream)
-                    else torch.cuda.default_stream(t.device))
-            side.wait_stream(current)          # whose queued work may still use the memory
-            ws.record_stream(side)
+    side = _side_stream(stream, t.device) if nbytes else None
+    if side is not None:
+        side.wait_stream(torch.cuda.current_stream(t.device))      # whose queued work may still use the memory
+        ws.record_stream(side)
     return ws
 
 
@@ -1461,6 +1466,24 @@ class MuonTable:
     def workspace_bytes(self) -> int:
         return int(_muont_ws(self._h))
 
+    def _workspace_on(self, stream, first):
+        """The table's workspace, for a call on `stream`. Made by the first one, and handed to each other stream once: that
+        waits for the stream on which it was made, whose work before may still use the memory, and the memory is handed out
+        again only after what the stream holds then. (A stream that is being captured cannot wait for one outside:
+        the first call on another is prepared before.)"""
+        import torch
+        handle = _stream(stream, first)
+        if self._workspace is None:
+            self._workspace = _own_workspace(self.workspace_bytes, first, stream)
+            self._made_on = torch.cuda.current_stream(first.device)
+            self._streams = {handle, self._made_on.cuda_stream}
+        elif handle not in self._streams and not torch.cuda.is_current_stream_capturing():
+            to = _side_stream(handle, first.device) or torch.cuda.current_stream(first.device)
+            to.wait_stream(self._made_on)
+            self._workspace.record_stream(to)
+            self._streams.add(handle)
+        return self._workspace
+
     def prepare_step(self, lr: float, momentum: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0,
                      coefficients=MUON_COEFFICIENTS, eps: float = 1e-7, clip_scale=None, workspace=None,
                      stream=None) -> "Prepared":
@@ -1473,9 +1496,7 @@ class MuonTable:
             first = self._keep[0][0]
             dev = first.get_device()
             if workspace is None:
-                if self._workspace is None:
-                    self._workspace = _own_workspace(self.workspace_bytes, first, stream)
-                workspace = self._workspace
+                workspace = self._workspace_on(stream, first)
             ptrs = [_clip_ptr(clip_scale, first), _on_device(workspace, dev, 1, "workspace"), workspace.numel(),
                     _stream(stream, first)]
         p = Prepared(_muont_step, [self._h, lr, momentum, int(nesterov), weight_decay, steps, n_steps, eps] + ptrs,
