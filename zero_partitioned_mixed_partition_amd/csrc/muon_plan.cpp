@@ -243,13 +243,18 @@ namespace {
 constexpr int64_t kTiles[kTileSizes] = {64, 128, 192, 256};
 
 // Microseconds on MI355X of one product: a launch with its descriptors and first loads, each tile's epilogue, and a
-// stage of a tile alone on its compute unit or as a share of a full one. Fitted to 12 matrices of a 1.3 B GPT, 6 of
-// GPT-2 small, 14,336 x 4096 and 8192 x 8192 with each tile: within 15% of their launches.
+// stage of a tile alone on its compute unit or as a share of a full one. Against traces of 487 x 1000, 12 of 768 x 768, 14,336 x
+// 4096, two 768 x 2304 and 8192 x 8192, lists of 6 and 12 of two GPTs and 7 of Llama's: square products within 10 %, but for
+// lists whose matrices have unlike sides (12 of the 1.3 B GPT: X X^T 299 us for 358, others 114 for 130; Llama's 302 for 340 to
+// 360), applies, whose epilogue also keeps and adds what rounding leaves, within 12 %, but for the last one of an update (20 to 50 %
+// more, its 10 bytes an element).
 struct TileCost {
     double launch, tile, alone, share;
 };
-constexpr TileCost kCosts[kTileSizes] = {
+constexpr TileCost kSquareCosts[kTileSizes] = {
     {5.0, 0.6, 0.30, 0.23}, {6.0, 2.0, 0.62, 0.52}, {3.0, 6.0, 0.96, 1.02}, {3.0, 9.0, 1.18, 1.45}};
+constexpr TileCost kApplyCosts[kTileSizes] = {
+    {5.0, 2.0, 0.30, 0.23}, {6.0, 4.5, 0.62, 0.52}, {}, {3.0, 34.0, 1.18, 1.45}};        // (no applies with 192)
 
 double product_time(const TileCost& c, double tiles, double stages) {
     if (tiles == 0.0) return 0.0;
@@ -263,10 +268,10 @@ double square_time(int k, double tiles, double stages) {
         const double whole = whole_tiles(static_cast<uint32_t>(tiles));
         if (whole < tiles) {
             const double each = stages / tiles;          // a quarter of a tile is one of 128, alone on its unit
-            return product_time(kCosts[k], whole, each * whole) + kCosts[1].tile + each * kCosts[1].alone;
+            return product_time(kSquareCosts[k], whole, each * whole) + kSquareCosts[1].tile + each * kSquareCosts[1].alone;
         }
     }
-    return product_time(kCosts[k], tiles, stages);
+    return product_time(kSquareCosts[k], tiles, stages);
 }
 
 int64_t padded(int64_t side, int64_t tile) { return std::max(pad(side, 64), tile); }
@@ -299,7 +304,7 @@ void TileChoice::best(int64_t* square, int64_t* rect, Times* times) const {
             if (kTiles[j] == 192) continue;
             const Total& x = total_[k][j];
             const Times t{square_time(k, x.square, x.gram), square_time(k, x.square, x.squares),
-                          product_time(kCosts[j], x.rect, x.apply)};
+                          product_time(kApplyCosts[j], x.rect, x.apply)};
             const double time = program_time(t, 5, true);
             if (*square == 0 || time < least) {
                 *square = kTiles[k];
