@@ -224,16 +224,19 @@ class RankStep:
         self.partials[:self.plan.num_ranks].copy_(p.to(self.device))
 
     def _prepared(self, key, stream, build, sig=None):
-        """Marshal a call's arguments once and reuse them while the stream and
-        `sig` (the caller's buffers) stay the same. One entry per key: a new
-        signature replaces the old entry and releases the buffers it held."""
+        """Marshal a call's arguments once per stream and reuse them while `sig` (the caller's buffers) stays
+        the same. A new signature replaces the old entries and releases the buffers they held; another stream's
+        entry of the same signature stays, since a captured step goes on reading the tables of its own."""
         if stream is None:
             stream = torch.cuda.current_stream(self.device).cuda_stream
-        cached = self._calls.get(key)
-        if cached is None or cached[0] != stream or cached[1] != sig:
-            cached = (stream, sig, build(stream))
-            self._calls[key] = cached
-        return cached[2]
+        calls = self._calls.setdefault(key, {})
+        cached = calls.get(stream)
+        if cached is None or cached[0] != sig:
+            cached = (sig, build(stream))
+            for other in [s for s, (held, _) in calls.items() if held != sig]:
+                del calls[other]
+            calls[stream] = cached
+        return cached[1]
 
     def reduce(self, windows: Sequence[Tuple[int, int, Sequence[torch.Tensor]]], stream=None):
         """windows: (begin, count, replica tensors) per window, in arrival order."""
