@@ -701,8 +701,9 @@ zero_status zero_state8_dequantize(const uint8_t* codes, const uint8_t* scales, 
  *              Must not overlap x or the workspace.
  * Errors: ZERO_EINVAL (an unknown x_type, a negative count or side, bad steps
  * or eps, coefficients that let singular values, with what roundings add to
- * them, grow past 2^20; with something to do, null pointers, a workspace not 256-byte aligned, overlapping arrays,
- * named in zero_last_error()); ZERO_ERANGE (a side past its limit, or more
+ * them, grow past 2^20 or a step multiply by more than 2^60; with something to do,
+ * null pointers, a workspace not 256-byte aligned, overlapping arrays, named in
+ * zero_last_error()); ZERO_ERANGE (a side past its limit, or more
  * workgroups than one launch holds); ZERO_ENOSPACE; ZERO_ENOMEM; ZERO_EHIP.
  *
  * zero_muon_step: the update of `count` matrices one after the other. Per

@@ -33,7 +33,8 @@ def divided(steps, s):
 @pytest.fixture(scope="module")
 def exe(tmp_path_factory):
     out = str(tmp_path_factory.mktemp("muon") / "program")
-    b = subprocess.run(["g++", "-O1", "-std=c++17", f"-I{ROCM}/include", "-D__HIP_PLATFORM_AMD__", f"-I{CSRC}",
+    b = subprocess.run(["g++", "-O1", "-g", "-std=c++17", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+                        f"-I{ROCM}/include", "-D__HIP_PLATFORM_AMD__", f"-I{CSRC}",
                         f"-I{os.path.join(ROOT, 'include')}", os.path.join(ROOT, "tests", "host_muon_program.cpp"),
                         os.path.join(CSRC, "muon_plan.cpp"), os.path.join(CSRC, "status.cpp"), "-o", out,
                         f"-L{ROCM}/lib", "-lamdhip64", f"-Wl,-rpath,{ROCM}/lib"], capture_output=True, text=True, timeout=300)
@@ -42,7 +43,8 @@ def exe(tmp_path_factory):
 
 
 def run(exe, *args, steps):
-    r = subprocess.run([exe, *args, *[repr(float(x)) for s in steps for x in s]], capture_output=True, text=True, timeout=60)
+    r = subprocess.run([exe, *args, *[repr(float(x)) for s in steps for x in s]], capture_output=True, text=True, timeout=60,
+                       env=dict(os.environ, ASAN_OPTIONS="detect_leaks=0"))
     assert r.returncode == 0, r.stderr
     return r.stdout.splitlines()
 
@@ -145,6 +147,16 @@ def test_steps_that_end_at_the_edge_of_their_interval(exe, name, pairs):
 def test_steps_that_grow_are_refused(exe, steps):
     status, message, _ = tiled(exe, steps, False, True)
     assert status != 0 and "grow past 2^20" in message
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("steps", [[(1e308, 1e308, 1e308)], [(1e308, -1e308, 1e308)] * 2, [(0.0, 0.0, 0.0), (1e200, 0.0, 0.0)],
+                                   [(1e-30, 0.0, 0.0), USUAL, (-1e60, 1e80, 0.0), USUAL]])
+def test_factors_past_any_exponent_are_refused(exe, steps, pairs):
+    """With the address and undefined-behaviour checks of the compiler."""
+    status, message, _ = tiled(exe, steps, pairs, True)
+    assert status != 0 and ("grow past 2^20" in message or "more than 2^60" in message)
+    assert short(exe, steps) is None
 
 
 SPECTRA = {"rank 1": lambda k, m: (k < 1) * 1.0, "rank 3": lambda k, m: (k < 3) * 1.0, "flat": lambda k, m: np.ones(m),

@@ -12,7 +12,7 @@ namespace {
 
 // The power of two e for which values up to `bound` are held as value * 2^e: the largest lies in (2^13, 2^14], a
 // factor of 4 below fp16's largest for what roundings add.
-int exponent_for(double bound) { return 14 - static_cast<int>(std::ceil(std::log2(std::max(bound, 1e-6)))); }
+int exponent_for(double bound) { return 14 - static_cast<int>(std::ceil(std::log2(std::max(std::min(bound, 1e30), 1e-6)))); }
 
 float pow2(int e) { return static_cast<float>(std::ldexp(1.0, e)); }
 
@@ -135,6 +135,11 @@ zero_status make_program(const double* coefficients, int32_t n_steps, bool pairs
             p->beta = static_cast<float>(s.b * pow2(eC - eA));
             p->diag = static_cast<float>(s.a * pow2(eC));
         };
+        // (A factor that large on an interval that the steps before made that small: the exponents would not fit a float.)
+        const auto too_large = [](const Step& s, double end) { return !(s.largest_factor(end) <= 0x1p60); };
+        const double between = s0.largest_left(top) * (1.0 + kSlack);        // the end of the interval after this step
+        if (too_large(s0, top) || (pair && too_large(step_at(taken, at + 1), between)))
+            return fail(ZERO_EINVAL, std::string(who) + ": a step with these coefficients multiplies by more than 2^60");
         const int eA = exponent_for_largest(top), eC = exponent_for_largest(s0.largest_factor(top));
         product(Kind::kGram, kX, kX, kS0, pow2(eA - 2 * eX))->kappa_power = first ? 2 : 0;
         polynomial(s0, kS0, kS1, eA, eC);
@@ -143,7 +148,6 @@ zero_status make_program(const double* coefficients, int32_t n_steps, bool pairs
         double next = s0.largest_left(top);
         if (pair) {
             const Step s1 = step_at(taken, at + 1);
-            const double between = next * (1.0 + kSlack);
             const int eT = exponent_for_largest(s0.largest_times_x(top));
             const int eA1 = exponent_for_largest(between), eC1 = exponent_for_largest(s1.largest_factor(between));
             eQ = exponent_for_largest(largest(top, [&](double x) { return s0.at(x) * s1.at(s0.left(x)); }));
@@ -212,7 +216,7 @@ bool make_short_program(const double* coefficients, int32_t n_steps, ShortProgra
         const double most_q = *std::max_element(lanes, lanes + kLanes);
         // small negative eigenvalues, which roundings make, grow by a^2
         if (at + 1 < n_steps) growth *= std::max(1.0, most_c * most_c);
-        if (!(growth <= 65536.0) || !(most_a <= 1024.0) || !(most_q <= 65536.0)) return false;
+        if (!(most_c <= 0x1p60) || !(growth <= 65536.0) || !(most_a <= 1024.0) || !(most_q <= 65536.0)) return false;
         const int eC = exponent_for_largest(most_c), eT = exponent_for_largest(most_t), eN = exponent_for_largest(most_a),
                   eP = at == 0 ? eC : exponent_for_largest(most_q);
         ShortStep& s = out->step[at];
