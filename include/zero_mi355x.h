@@ -670,9 +670,9 @@ zero_status zero_state8_dequantize(const uint8_t* codes, const uint8_t* scales, 
  * noise of that size. Every step multiplies what lies in such directions by its a:
  * after nine usual ones the noise is up to 0.2, and a matrix whose singular
  * values lie above 1e-3 of the largest up to 4e-2 off. Where no matrix of a call
- * has a short side above 128 and the product of the squares of all a but the last
- * is below 65,536, all values are held in two fp16 parts, and five usual steps are
- * about 3e-5 off.
+ * has a short side above 128 and the product of the squares of the steps' largest
+ * factors (a, of the usual ones) but the last's is below 65,536, all values are held
+ * in two fp16 parts, and five usual steps are about 3e-5 off.
  * Two steps are taken as one on the smaller side where that saves time and the
  * first's |a| is at most 4; this and the products' tiles follow the sizes and
  * number of a call's matrices.
@@ -743,8 +743,11 @@ zero_status zero_muon_step(float* master, float* momentum, const uint16_t* grad,
 
 /* zero_muon_step over a list of matrices of any shapes, described once in
  * device memory (as zero_mt_table_*): every product is one launch over all of
- * them. The results are zero_muon_step's on each matrix, up to the choice of tiles and
- * of how the steps are grouped (below its stated precision), which follows the whole list.
+ * them. The results are zero_muon_step's on each matrix within its stated
+ * precision: the form, the tiles and how the steps are grouped follow the whole
+ * list, so one matrix with a short side above 128 takes those up to 128, which a
+ * list of their own would leave 3e-5 off, to the precision of one fp16 part (up to
+ * 1e-2 on short sides far below 128).
  * Create: host arrays of n_matrices pointers, sides and scales; a matrix without
  * elements is left out. hipMalloc and a synchronous hipMemcpy on the current
  * device, once (128 bytes a matrix and 4 per workgroup). The table keeps the pointers,

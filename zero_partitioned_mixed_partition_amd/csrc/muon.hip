@@ -230,10 +230,10 @@ constexpr bool has_quarters = T == 256 && kSquareOut;
 
 // One T x T tile of a product, both operands rows of contiguous K.
 //
-// With 256 the MFMAs bound it and the chip's power their clock: two applies of 8192 x 8192 x 8192 take 1.60 ms, 1375
-// TFLOP/s (the library's product of that size 1395), the MFMAs busy 71 % of the time at 1.84 GHz (2048 of a stage's 2,800
-// cycles; its loads, 64 KB into one compute unit's LDS, need 1024). Symmetric products run at the same rate, half of
-// each computed. Where the tiles are few (487 x 1000: 36 of 64 x 64, 7.2 us a product) it is latency: 1.4 us of launch,
+// With 256 the MFMAs bound it and the chip's power their clock: without what carrying the roundings adds to the epilogue two
+// applies of 8192 x 8192 x 8192 take 1.60 ms, 1375 TFLOP/s (the library's product of that size 1395), the MFMAs busy 71 % of the
+// time at 1.84 GHz (2048 of a stage's 2,800 cycles; its loads, 64 KB into one compute unit's LDS, need 1024), with it
+// 1.79 to 1.86 ms. Symmetric products run at 1.2 PFLOP/s, half of each computed. Where the tiles are few (487 x 1000: 36 of 64 x 64, 7.2 us a product) it is latency: 1.4 us of launch,
 // 1 to the first load, 2.4 for eight stages, 1.8 for the way out through LDS. Rows of K come straight from memory to
 // LDS (16 bytes a lane), so that no register holds what is on its way.
 template <int T, int kStages, bool kSquareOut, int kEnd>     // kEnd: 0 workspace, 1 orthogonalised matrix, 2 weight update
@@ -303,8 +303,8 @@ __device__ __forceinline__ void tile(const Matrices& m, const Product& p, const 
     };
     constexpr int kReads = MI + NI, kProducts = MI * NI;
     // In assembly, so that the sum stays where it is: the compiler may give the result of this shape other registers, and
-    // with 256 of them moves them all in every stage. (A product that adds to
-    // the one before needs no wait; one before the sums are read is the compiler's no longer: see below.)
+    // with 256 of them moves them all in every stage. (A product that adds to the one before needs no wait. The wait between the
+    // last product and the first read of a sum, which the compiler puts after its own instruction, stands behind the loop.)
     auto multiply = [&](const Fragments& f, int q) {
         asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc[q / NI][q % NI]) : "v"(f.a[q / NI]), "v"(f.b[q % NI]));
     };
@@ -721,9 +721,9 @@ zero_status launch(const Matrices& m, const Call& c, hipStream_t stream, const c
     if (m.side != 0 && make_short_program(c.coefficients, c.n_steps, &steps))
         return launch_short(c.source, m, c.momentum, c.update, steps, c.eps, stream, who);
     std::vector<Product> program;
-    // Pairs where they save a fiftieth of the time or more (six GPT-2 small matrices: 350 us against 364; 487 x 1000: 135
-    // against 129): at equal time the single steps, whose A comes from X itself, are more exact (about 1.2e-3 of the
-    // result's norm against 1.2e-3 to 1.9e-3).
+    // Pairs where they save a fiftieth of the time or more (six GPT-2 small matrices: 404 us against 429; 487 x 1000: 130
+    // against 127): at equal time the single steps, whose A comes from X itself, are more exact (up to 4.7e-3 of the result's
+    // norm on hard singular values against 6.1e-3).
     const bool pairs = zero::muon::program_time(c.times, c.n_steps, true) <
                        0.98 * zero::muon::program_time(c.times, c.n_steps, false);
     try {
