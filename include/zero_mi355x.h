@@ -663,7 +663,7 @@ zero_status zero_state8_dequantize(const uint8_t* codes, const uint8_t* scales, 
  * Precision: products of fp16 values (scaled by powers of two) summed in fp32,
  * with what rounding each X left carried along; after five usual steps about
  * 1.5e-3 of the result's Frobenius norm off the exact ones, less than rounding it
- * to bf16 (1.7e-3), and up to 6e-3 where few directions hold nearly all of the
+ * to bf16 (1.7e-3), and up to 7e-3 where few directions hold nearly all of the
  * norm or half of the singular values lie far below the rest. Singular values
  * below about 1e-5 of the norm, and directions that G does not have, come out as
  * noise of up to 0.02; elements below 3e-10 (a norm far below eps) as zeros or
@@ -746,8 +746,9 @@ zero_status zero_muon_step(float* master, float* momentum, const uint16_t* grad,
  * them. The results are zero_muon_step's on each matrix within its stated
  * precision: the form, the tiles and how the steps are grouped follow the whole
  * list, so one matrix with a short side above 128 takes those up to 128, which a
- * list of their own would leave 3e-5 off, to the precision of one fp16 part (up to
- * 1e-2 on short sides far below 128).
+ * list of their own would leave 3e-5 off, to the precision of one fp16 part (where
+ * few directions hold nearly all of the norm up to 1e-2 on short sides of 64, and
+ * 5e-2 below 16).
  * Create: host arrays of n_matrices pointers, sides and scales; a matrix without
  * elements is left out. hipMalloc and a synchronous hipMemcpy on the current
  * device, once (128 bytes a matrix and 4 per workgroup). The table keeps the pointers,
